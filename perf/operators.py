@@ -219,7 +219,7 @@ def prepare(case, seed):
         cu = np.concatenate([[0], np.cumsum(add)])
         b = np.repeat(np.arange(r), add)
         pos = old[b] + np.arange(len(b)) - cu[b]
-        st.update(k=k, v=v, cu=_i32(cu), slots=_i32(table[b, pos // page] * page + pos % page), request=_i32(b),
+        st.update(k=k, v=v, cu=_i32(cu), after=_i32(new), slots=_i32(table[b, pos // page] * page + pos % page), request=_i32(b),
                   pos=_i32(pos), items=int(case["tokens"]) // page + r)
     else:
         st.update(q=_normal(gen, (r, case["q_heads"], d), dtype), longest=int(new.max()))
@@ -262,7 +262,7 @@ def _own(st, case, op):
                     free_count=p.free_count)
     if op == "write":
         c = st["cache"]
-        c.write(0, st["k"], st["v"], st["cu"], st["slots"], st["lens"])
+        c.write(0, st["k"], st["v"], st["cu"], st["slots"], st["after"])
         return dict(pages=_values(c.pages(0), case), scales=c.scales(0), tails=c.tails(0))
     if op == "decode":
         return st["cache"].decode(0, st["q"], st["table"], st["lens"], _scale(case))
