@@ -13,12 +13,15 @@ import os
 
 import torch
 
+from . import paged as _paged
 from . import workloads as _W
+from .paged import PAGE_E4M3, PAGE_INT8, PagedKVCache, StepPlan, prompt_attention
 
 __all__ = [
     "KVQError", "QuantizedKVCache", "lib", "library_path",
     "SYM_PER_TOKEN", "ASYM_PER_TOKEN", "ASYM_PER_CHANNEL", "CODEBOOK_PER_TOKEN", "F32", "F16",
     "E2M1_LEVELS",
+    "PagedKVCache", "StepPlan", "prompt_attention", "PAGE_INT8", "PAGE_E4M3",
 ]
 
 SYM_PER_TOKEN = 0
@@ -96,6 +99,7 @@ _SIGNATURES = {
     "kvq_selftest_codebook_quotient": [_P, _P],
     "kvq_prefill_attention": [_P, _I, _P, _I, _I, ctypes.c_float, _P, _I, _P],
     "kvq_selftest_wait_timeout": [_P, _I, _P],
+    **_paged.SIGNATURES,
 }
 
 _lib = None

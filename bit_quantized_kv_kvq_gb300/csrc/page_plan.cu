@@ -1,0 +1,236 @@
+// Planning of a paged step on the GPU: block tables, slot maps and positions
+// from request lengths (kvq_paged_reserve), and the return of pages
+// (kvq_paged_release).
+//
+// Request b holds n tokens in ceil(n / P) pages and takes m more: it grows by
+// ceil((n + m) / P) - ceil(n / P) pages. Two exclusive prefix sums over the
+// requests, of m and of the growth, give every packed token its request and
+// position and every new page its place on the free stack, so everything after
+// the sums is independent per token and per page.
+#include "paged_internal.h"
+
+namespace kvq {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kPer = kMaxRequests / kThreads;  // requests per thread
+
+// Exclusive prefix sums of (x, y) over the block; totals in *tx, *ty.
+__device__ __forceinline__ void block_scan2(long long& x, long long& y, long long* tx, long long* ty) {
+  __shared__ long long wx[32], wy[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long ix = x, iy = y;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long ux = __shfl_up_sync(0xffffffffu, ix, d), uy = __shfl_up_sync(0xffffffffu, iy, d);
+    if (lane >= d) ix += ux, iy += uy;
+  }
+  if (lane == 31) wx[warp] = ix, wy[warp] = iy;
+  __syncthreads();
+  if (warp == 0) {
+    long long a = wx[lane], b = wy[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long ua = __shfl_up_sync(0xffffffffu, a, d), ub = __shfl_up_sync(0xffffffffu, b, d);
+      if (lane >= d) a += ua, b += ub;
+    }
+    wx[lane] = a, wy[lane] = b;
+  }
+  __syncthreads();
+  x = ix - x + (warp ? wx[warp - 1] : 0);
+  y = iy - y + (warp ? wy[warp - 1] : 0);
+  *tx = wx[31];
+  *ty = wy[31];
+}
+
+// The last index b in [0, n) with key[b] <= x (keys ascending, key[0] <= x).
+__device__ __forceinline__ int last_le(const int* key, int n, int x) {
+  int lo = 0;
+  while (n > 1) {
+    const int half = n >> 1;
+    if (key[lo + half] <= x) lo += half, n -= half;
+    else n = half;
+  }
+  return lo;
+}
+
+// One cluster. Every CTA makes the sums for itself (a few thousand lengths)
+// and takes its share of the tokens and pages; the cluster barrier between
+// reading the lengths and writing the state lets lens_out and free_count_out
+// be the input arrays.
+__global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) {
+  extern __shared__ int sm[];
+  const int R = a.requests;
+  int* cu = sm;                // [R + 1] packed token where the request starts
+  int* first = sm + R + 1;     // [R + 1] pages taken before the request's
+  int* old = sm + 2 * (R + 1); // [R] length before
+  __shared__ int bad_s;
+  uint32_t rank, ranks;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const int P = 1 << a.page_shift;
+  if (threadIdx.x == 0) bad_s = 0;
+  __syncthreads();
+
+  const int free_count = *a.free_count;
+  int n[kPer], m[kPer], g[kPer];
+  long long add = 0, grow = 0;
+  bool bad = false, full = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = threadIdx.x * kPer + i;
+    n[i] = b < R ? a.lens[b] : 0;
+    m[i] = b < R ? a.add[b] : 0;
+    bad |= n[i] < 0 || m[i] < 0;
+    const long long have = ((long long)n[i] + P - 1) >> a.page_shift;
+    const long long need = ((long long)n[i] + m[i] + P - 1) >> a.page_shift;
+    full |= need > a.max_pages;
+    g[i] = (int)(need - have);
+    add += m[i];
+    grow += g[i];
+  }
+  const bool over = free_count < 0 || free_count > a.num_pages;
+  const int flags = (bad || over ? 1 : 0) | (full ? 2 : 0);
+  if (flags) atomicOr(&bad_s, flags);
+  long long total, pages;
+  block_scan2(add, grow, &total, &pages);  // its barriers publish bad_s too
+  const bool fits = bad_s == 0 && total <= a.max_tokens && pages <= free_count;
+  if (fits) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = threadIdx.x * kPer + i;
+      if (b < R) cu[b] = (int)add, first[b] = (int)grow, old[b] = n[i];
+      add += m[i];
+      grow += g[i];
+      if (b == R - 1) cu[R] = (int)add, first[R] = (int)grow;
+    }
+  }
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+
+  const int at0 = rank * kThreads + threadIdx.x, stride = ranks * kThreads;
+  if (!fits) {
+    for (int i = at0; i < a.max_tokens; i += stride) a.slots[i] = -1, a.positions[i] = -1;
+    if (rank == 0) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int b = threadIdx.x * kPer + i;
+        if (b < R) a.lens_out[b] = n[i];
+      }
+      for (int b = threadIdx.x; b <= R; b += kThreads) a.cu[b] = 0;
+      if (threadIdx.x == 0) {
+        *a.free_count_out = free_count;
+        raise_status(a.status, (bad_s & 1) ? kStatusBadIndex : kStatusNoRoom);
+      }
+    }
+    return;
+  }
+  if (rank == 0) {
+    for (int b = threadIdx.x; b <= R; b += kThreads) {
+      a.cu[b] = cu[b];
+      if (b < R) a.lens_out[b] = old[b] + (cu[b + 1] - cu[b]);
+    }
+    if (threadIdx.x == 0) *a.free_count_out = free_count - (int)pages;
+  }
+  for (int k = at0; k < (int)pages; k += stride) {
+    const int b = last_le(first, R + 1, k);
+    const int j = ((old[b] + P - 1) >> a.page_shift) + (k - first[b]);
+    const int page = a.free_pages[free_count - 1 - k];
+    if (page < 0 || page >= a.num_pages) raise_status(a.status, kStatusBadIndex);
+    a.table[(int64_t)b * a.max_pages + j] = page;
+  }
+  for (int i = at0; i < a.max_tokens; i += stride) {
+    int slot = -1, pos = -1;
+    if (i < (int)total) {
+      const int b = last_le(cu, R + 1, i);
+      pos = old[b] + (i - cu[b]);
+      const int j = pos >> a.page_shift, have = (old[b] + P - 1) >> a.page_shift;
+      const int page = j < have ? a.table[(int64_t)b * a.max_pages + j]
+                                : a.free_pages[free_count - 1 - (first[b] + j - have)];
+      if (page >= 0 && page < a.num_pages) slot = (page << a.page_shift) + (pos & (P - 1));
+      else raise_status(a.status, kStatusBadIndex);
+    }
+    a.slots[i] = slot;
+    a.positions[i] = pos;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseArgs a) {
+  __shared__ int first[kMaxRequests + 1];
+  const int R = a.requests;
+  const int P = 1 << a.page_shift;
+  int count = *a.free_count;
+  long long mine = 0, unused = 0;
+  int g[kPer];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = threadIdx.x * kPer + i;
+    g[i] = 0;
+    if (b < R && a.done[b] != 0) {
+      const int n = a.lens[b];
+      const long long pages = ((long long)n + P - 1) >> a.page_shift;
+      if (n < 0 || pages > a.max_pages) bad = true;
+      else g[i] = (int)pages;
+    }
+    mine += g[i];
+  }
+  if (count < 0 || count > a.num_pages) bad = true;
+  long long total;
+  block_scan2(mine, unused, &total, &unused);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = threadIdx.x * kPer + i;
+    if (b < R) first[b] = (int)(mine < INT32_MAX ? mine : INT32_MAX);
+    mine += g[i];
+    if (b == R - 1) first[R] = (int)(mine < INT32_MAX ? mine : INT32_MAX);
+  }
+  if (bad) raise_status(a.status, kStatusBadIndex);
+  __syncthreads();
+  if (count < 0 || count > a.num_pages) return;  // the stack is not touched
+  const long long room = a.num_pages - count;
+  if (total > room) {
+    if (threadIdx.x == 0) raise_status(a.status, kStatusBadIndex);
+    total = room;
+  }
+  for (int k = threadIdx.x; k < (int)total; k += kThreads) {
+    const int b = last_le(first, R + 1, k);
+    const int page = a.table[(int64_t)b * a.max_pages + (k - first[b])];
+    // an entry out of range keeps its place on the stack, where reserve refuses it
+    if (page < 0 || page >= a.num_pages) raise_status(a.status, kStatusBadIndex);
+    a.free_pages[count + k] = page;
+  }
+  for (int b = threadIdx.x; b < R; b += kThreads)
+    if (a.done[b] != 0) a.lens[b] = 0;
+  if (threadIdx.x == 0) *a.free_count = count + (int)total;
+}
+
+}  // namespace
+
+cudaError_t launch_reserve(const ReserveArgs& a, cudaStream_t st) {
+  static SmemAttr attr;
+  const size_t smem = (size_t)(3 * a.requests + 2) * 4;
+  const cudaError_t e = attr.ensure(reserve_kernel, (3 * kMaxRequests + 2) * 4);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  const int ctas = a.max_tokens > 2 * kThreads ? 8 : 1;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = ctas;
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, reserve_kernel, a);
+}
+
+cudaError_t launch_release(const ReleaseArgs& a, cudaStream_t st) {
+  release_kernel<<<1, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace kvq

@@ -33,7 +33,8 @@
  *  - fp16 means IEEE binary16. Layouts are C order (last index fastest).
  *  - One cache serves num_layers layers; a layer's lengths are uniform over
  *    the batch unless kvq_prefill_quantize_varlen gave each batch row its
- *    own. head_dim must be 128.
+ *    own. head_dim must be 128. (The paged cache has its own lengths and
+ *    head sizes, see there.)
  *  - Calls that enqueue work (prefill, append, decode, status) need the
  *    device that holds the cache buffer to be current; otherwise they
  *    return KVQ_ERR_INVALID_ARG. Caches on several devices may be used from
@@ -94,7 +95,8 @@ typedef enum kvq_mode {
   KVQ_CODEBOOK_PER_TOKEN = 3
 } kvq_mode;
 
-typedef enum kvq_dtype { KVQ_F32 = 0, KVQ_F16 = 1 } kvq_dtype;
+/* KVQ_BF16 is taken by the paged cache and kvq_prompt_attention only. */
+typedef enum kvq_dtype { KVQ_F32 = 0, KVQ_F16 = 1, KVQ_BF16 = 2 } kvq_dtype;
 
 typedef struct kvq_config {
   int32_t num_layers;       /* >= 1                                                   */
@@ -353,6 +355,159 @@ KVQ_API kvq_status kvq_cache_length(const kvq_cache* cache, int32_t layer, int32
  * every layer are cleared too (a decode that gave up may have left them set). */
 KVQ_API kvq_status kvq_cache_status(kvq_cache* cache, void* stream, uint32_t* word);
 
+/* ------------------------------------------------------------------------
+ * Paged cache: the serving form of the cache, for a changing set of requests.
+ *
+ * Every layer holds num_pages pages of page_tokens tokens; a request owns the
+ * pages that its row of a block table names. Keys and values are held in 8
+ * bits with one fp32 scale per (page, kv-head, K or V):
+ *   s = absmax / Q over the page's tokens and channels of that head,
+ *   code = round(x / s) to the code type (nearest, ties to even), x_hat = code * s,
+ * Q = 127 for KVQ_PAGE_INT8 and 448 for KVQ_PAGE_E4M3 (1 sign, 4 exponent, 3
+ * fraction bits), division and scale in IEEE fp32; s == 0 stores code 0. A
+ * page is quantized once, when its last token is written; until then its rows
+ * stay in the request's tail in the input type, so that the codes do not
+ * depend on how a prompt was cut into calls. A page that takes in an infinity
+ * or NaN reads back as NaN for that head and tensor.
+ *
+ * Lengths, block tables, slot maps and the free list are caller-owned device
+ * arrays, shared by all layers and read by the kernels: a step needs no copy
+ * to or from the host and can be captured into a CUDA graph and replayed. What
+ * they hold is checked on the device: a value out of range sets the status
+ * word (kvq_paged_cache_status) and the work that it belongs to is left out.
+ *
+ * A step: kvq_paged_reserve once; then per layer kvq_paged_write, and
+ * kvq_prompt_attention for prompts or kvq_paged_decode_attention for single
+ * tokens; kvq_paged_release when requests end.
+ * ------------------------------------------------------------------------ */
+typedef enum kvq_page_code { KVQ_PAGE_INT8 = 0, KVQ_PAGE_E4M3 = 1 } kvq_page_code;
+
+typedef struct kvq_paged_config {
+  int32_t num_layers;    /* 1 .. 4096                                              */
+  int32_t max_requests;  /* request slots, 1 .. 4096                               */
+  int32_t num_kv_heads;  /* 1 .. 1024                                              */
+  int32_t head_dim;      /* 64 or 128                                              */
+  int32_t page_tokens;   /* 16, 32, 64 or 128                                      */
+  int32_t num_pages;     /* pages per layer, >= 1; num_pages * page_tokens < 2^31  */
+  int32_t max_pages;     /* row length of a block table, >= 1;
+                            max_pages * page_tokens < 2^31                         */
+  int32_t code;          /* kvq_page_code                                          */
+  int32_t dtype;         /* of K, V, Q: KVQ_F16 or KVQ_BF16                        */
+} kvq_paged_config;
+
+/* Device arrays of one layer: pages 8-bit codes [num_pages][H_kv][2][page_tokens][D]
+ * (2: keys, values), scales fp32 [num_pages][H_kv][2], tails (the rows of each
+ * request's open page, at their place in the page) [max_requests][H_kv][2]
+ * [page_tokens][D] in the config's dtype. */
+typedef struct kvq_paged_layout {
+  int64_t pages_bytes, scales_bytes, tails_bytes;
+  void* pages;
+  void* scales;
+  void* tails;
+} kvq_paged_layout;
+
+typedef struct kvq_paged_cache kvq_paged_cache; /* opaque host-side handle */
+
+/* Device bytes the cache needs (all layers + a 256-byte header). Host only. */
+KVQ_API kvq_status kvq_paged_cache_bytes(const kvq_paged_config* cfg, size_t* bytes);
+
+/* As kvq_cache_create: validates, lays out `dev_buf` (256-byte aligned) and
+ * zeroes it on `stream`. The handle holds no state but the layout: several
+ * host threads may use it at once. */
+KVQ_API kvq_status kvq_paged_cache_create(const kvq_paged_config* cfg, void* dev_buf, size_t bytes, void* stream,
+                                          kvq_paged_cache** out);
+
+/* Frees the host handle only; the device buffer stays the caller's. */
+KVQ_API kvq_status kvq_paged_cache_destroy(kvq_paged_cache* cache);
+
+KVQ_API kvq_status kvq_paged_cache_get_layout(const kvq_paged_cache* cache, int32_t layer, kvq_paged_layout* out);
+
+/* Synchronizes `stream`, reads the status word and clears it. KVQ_OK,
+ * KVQ_ERR_CAPACITY (a reserve found too few pages, too small a table row or
+ * too small slot arrays), KVQ_ERR_TIMEOUT or KVQ_ERR_DEVICE_STATUS (a length,
+ * slot, page or count out of range). *word (optional) receives the bits. */
+KVQ_API kvq_status kvq_paged_cache_status(kvq_paged_cache* cache, void* stream, uint32_t* word);
+
+/* Plans one step for `requests` (<= max_requests) slots: request b holds
+ * lens[b] tokens and takes new_tokens[b] >= 0 more, packed one request after
+ * the other in the step's inputs.
+ *   cu_tokens [requests + 1]  prefix sums of new_tokens
+ *   slots     [max_tokens]    per packed token page * page_tokens + place in page
+ *   positions [max_tokens]    per packed token its position in its request
+ *   table     [requests][max_pages]  pages from the top of the free stack
+ *             free_pages[0 .. *free_count) enter the rows that grow, in order
+ *             of request and position; other entries are left as they are
+ *   lens_out  [requests], free_count_out [1]  the state after the step; either
+ *             may be the array it replaces
+ * slots and positions past the last packed token are -1. The step is planned
+ * whole or not at all: where it does not fit (pages, a table row, max_tokens)
+ * or a length is negative, the table stays, cu_tokens is all 0, slots and
+ * positions are all -1, lens_out and free_count_out repeat the inputs, and
+ * the status word is set. All arrays int32 on the device. One launch. */
+KVQ_API kvq_status kvq_paged_reserve(kvq_paged_cache* cache, int32_t requests, const int32_t* lens,
+                                     const int32_t* new_tokens, int32_t* table, const int32_t* free_pages,
+                                     const int32_t* free_count, int32_t max_tokens, int32_t* cu_tokens,
+                                     int32_t* slots, int32_t* positions, int32_t* lens_out,
+                                     int32_t* free_count_out, void* stream);
+
+/* Ends the requests with done[b] != 0: their pages go back on top of the free
+ * stack (in order of request and position), lens[b] becomes 0; table rows stay
+ * as they are. free_pages has room for num_pages entries; pages past that are
+ * dropped and set the status word; a table entry out of range goes back as it
+ * is and sets it too. A page that two rows name must be released by one of
+ * them only. One launch. */
+KVQ_API kvq_status kvq_paged_release(kvq_paged_cache* cache, int32_t requests, const int32_t* done, int32_t* lens,
+                                     const int32_t* table, int32_t* free_pages, int32_t* free_count, void* stream);
+
+/* Writes the step's packed tokens into layer `layer`. k, v: [max_tokens]
+ * [H_kv][D] in the config's dtype, token rows k_stride / v_stride elements
+ * apart (multiples of 8, >= H_kv * D). cu_tokens, slots: as reserve wrote
+ * them; lens: the lengths AFTER the step (lens_out). Pages whose last token is among the
+ * packed ones are quantized (with the rows the tail holds of them), the rows
+ * of each request's new open page go to its tail. One launch. */
+KVQ_API kvq_status kvq_paged_write(kvq_paged_cache* cache, int32_t layer, int32_t requests, const void* k,
+                                   const void* v, int64_t k_stride, int64_t v_stride, int32_t max_tokens,
+                                   const int32_t* cu_tokens, const int32_t* slots, const int32_t* lens,
+                                   void* stream);
+
+/* Workspace bytes of kvq_paged_decode_attention for num_q_heads query heads
+ * and any number of requests up to max_requests. Host only. */
+KVQ_API kvq_status kvq_paged_decode_workspace_bytes(const kvq_paged_cache* cache, int32_t num_q_heads,
+                                                    size_t* bytes);
+
+/* One query token per request over the lens[b] tokens of its pages and tail:
+ *   e_t = softmax_scale * <q, k_hat_t>,  p = softmax(e),  o = sum_t p_t v_hat_t.
+ * q: [requests][H_q][D] in the config's dtype, rows q_stride elements apart (a
+ * multiple of 8, >= H_q * D); H_q any multiple of H_kv. out: [requests][H_q][D] in
+ * out_dtype (KVQ_F32 or the config's dtype); a request with lens[b] == 0 gets
+ * zeros. The tiles of all requests are cut into equal ranges by the kernel
+ * from lens, so the grid does not depend on the lengths. workspace: 16-byte
+ * aligned, any content, not shared with calls that overlap on the GPU. Two
+ * launches (the second merges the ranges' partial sums in a fixed order). */
+KVQ_API kvq_status kvq_paged_decode_attention(kvq_paged_cache* cache, int32_t layer, int32_t requests, const void* q,
+                                              int64_t q_stride, int32_t num_q_heads, const int32_t* table,
+                                              const int32_t* lens, float softmax_scale, void* out,
+                                              int32_t out_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* Causal attention over whole prompts, packed one after the other, on their
+ * own keys and values (no cache): token i of a sequence attends tokens 0 .. i
+ * of it. q: [max_tokens][H_q][D]; k, v: [max_tokens][H_kv][D]; dtype KVQ_F16 or
+ * KVQ_BF16, D 64 or 128, token rows q_stride / k_stride / v_stride elements
+ * apart (multiples of 8, no less than a row). H_q is a multiple of H_kv.
+ * cu_tokens: [num_seqs + 1] int32 on the device, sequence s holds tokens
+ * cu_tokens[s] .. cu_tokens[s + 1] - 1 (the array kvq_paged_reserve writes);
+ * num_seqs <= 4096. out: [max_tokens][H_q][D] in dtype; rows outside every sequence
+ * are left as they are. A later token does not reach an earlier one's output,
+ * not even by an infinity or NaN among its values. status: an optional uint32
+ * device word that receives the bits of kvq_paged_cache_status (a range that
+ * cu_tokens puts outside [0, max_tokens] is left out and sets one). All pointers
+ * must be of the current device. softmax_scale: finite and >= 0. One launch. */
+KVQ_API kvq_status kvq_prompt_attention(const void* q, const void* k, const void* v, int64_t q_stride,
+                                        int64_t k_stride, int64_t v_stride, int32_t max_tokens, int32_t num_seqs,
+                                        const int32_t* cu_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                        int32_t head_dim, int32_t dtype, float softmax_scale, void* out,
+                                        uint32_t* status, void* stream);
+
 /* Thread-local description of the last error ("" if none). */
 KVQ_API const char* kvq_last_error(void);
 
@@ -364,7 +519,7 @@ KVQ_API const char* kvq_last_error(void);
  * the last CTA of each stream inside the decode kernel), except the generic
  * decode used for the rarer codec combinations (per-token keys with
  * outliers, sub-32-channel groups), which adds 1 for a combine launch;
- * each self-test call 1. Occupancy queries launch
+ * each self-test call 1; the paged calls as their comments say. Occupancy queries launch
  * nothing and are not counted. */
 KVQ_API uint64_t kvq_kernel_launches(void);
 

@@ -1,0 +1,215 @@
+"""Causal attention over packed prompts against fp64, within a bound derived
+from its roundings: lengths around the tile borders, head groups, strides,
+sequences of no tokens, rows outside every sequence, infinities and NaN."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_kv_kvq_gb300 as kvq
+from oracle import paged_oracle as PO
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+def ints(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def rows(t, hq, h, d, dtype, seed, spread=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(t, hq + 2 * h, d, generator=gen)
+    x[:, :hq] *= spread
+    return x.to(dtype)
+
+
+def reference(q, k, v, cu, scale):
+    """(o, sum p |v|, score size) in fp64 on the GPU."""
+    g = q.shape[1] // k.shape[1]
+    o = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    w, size = torch.zeros_like(o), torch.zeros(q.shape[:2], dtype=torch.float64, device="cuda")
+    for lo, hi in zip(cu[:-1], cu[1:]):
+        if hi <= lo:
+            continue
+        qs = q[lo:hi].double().transpose(0, 1)
+        ks = k[lo:hi].double().transpose(0, 1).repeat_interleave(g, 0)
+        vs = v[lo:hi].double().transpose(0, 1).repeat_interleave(g, 0)
+        later = torch.ones(hi - lo, hi - lo, dtype=torch.bool, device="cuda").triu(1)
+        p = torch.softmax((qs @ ks.transpose(1, 2) * scale).masked_fill(later, float("-inf")), 2)
+        o[lo:hi] = (p @ vs).transpose(0, 1)
+        w[lo:hi] = (p @ vs.abs()).transpose(0, 1)
+        size[lo:hi] = ((qs.abs() @ ks.abs().transpose(1, 2)).masked_fill(later, 0).amax(2) * scale).T
+    return o, w, size
+
+
+def check(x, hq, h, cu, scale, out=None, tokens=None):
+    """x: fused rows; the bound: weights rounded to the type (half its eps each,
+    or 2^-25 of the row's largest below fp16's normal range), fp32 score sums
+    of D products (at most 2 D roundings of 2^-23 on the sum of magnitudes),
+    fp32 sums of the weighted values, the output's rounding."""
+    x = x.cuda()
+    q, k, v = x[:, :hq], x[:, hq:hq + h], x[:, hq + h:]
+    d = q.shape[2]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = kvq.prompt_attention(q, k, v, ints(cu), scale, out=out, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0 and o.dtype == x.dtype
+    ref, w, size = reference(q, k, v, cu, scale)
+    half = torch.finfo(x.dtype).eps / 2
+    n = max(hi - lo for lo, hi in zip(cu[:-1], cu[1:]))
+    tol = (half * 1.01 + 2 * 2 * d * 2.0 ** -23 * size[..., None] + n * 2.0 ** -23 + 2.0 ** -18) * w
+    tol = tol * 1.01 + n * 2.0 ** -25 * float(v.abs().max()) + half * ref.abs()
+    err = (o.double() - ref).abs()
+    live = torch.zeros(len(x), dtype=torch.bool, device="cuda")
+    for lo, hi in zip(cu[:-1], cu[1:]):
+        live[lo:hi] = True
+    bad = (err > tol)[live]
+    assert not bad.any(), (int(bad.sum()), float((err / tol)[live].max()))
+    return o
+
+
+LENS = [[1], [2], [63], [64], [65], [127], [128], [129], [255], [256], [257], [383], [511], [640, 1], [1] * 40,
+        [0, 5, 0, 0, 300, 7, 0], [129, 256, 1, 511, 128], [1000, 17, 333]]
+
+
+@pytest.mark.parametrize("lens", LENS, ids=str)
+@pytest.mark.parametrize("d,dtype", [(128, F16), (64, BF16)])
+def test_lengths(lens, d, dtype):
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    check(rows(cu[-1], 4, 2, d, dtype, seed=cu[-1]), 4, 2, cu, 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("h,g", [(1, 1), (2, 1), (1, 3), (3, 2), (2, 8), (1, 16), (8, 4)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_heads(h, g, d, dtype):
+    check(rows(300, h * g, h, d, dtype, seed=h * g), h * g, h, [0, 170, 300], 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("spread", [0.0, 8.0, 40.0])
+def test_flat_and_sharp_weights(dtype, spread):
+    check(rows(700, 2, 1, 128, dtype, seed=3, spread=spread), 2, 1, [0, 700], 1 / math.sqrt(128))
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-3, 1.0])
+def test_scales(scale):
+    check(rows(300, 2, 1, 64, F16, seed=3, spread=0.3), 2, 1, [0, 300], scale)
+
+
+def test_rising_scores():
+    """Every tile raises the maximum: the sums are rescaled each time."""
+    x = rows(600, 1, 1, 128, F16, seed=5)
+    x[:, 0] = 0.5
+    x[:, 1] = (torch.arange(600)[:, None] * 0.02 + 0.01 * torch.randn(600, 128)).half()
+    check(x, 1, 1, [0, 600], 0.1)
+    x[:, 1] = x[:, 1].flip(0)
+    check(x, 1, 1, [0, 600], 0.1)
+
+
+def test_a_long_prompt():
+    check(rows(5000, 2, 1, 128, BF16, seed=8), 2, 1, [0, 4999, 5000], 1 / math.sqrt(128))
+    check(rows(4097, 2, 1, 64, F16, seed=9), 2, 1, [0, 4097], 1 / 8)
+
+
+def test_rows_outside_every_sequence_are_left():
+    x = rows(400, 4, 2, 128, F16, seed=4)
+    x[350:] = float("nan")
+    x[:3] = float("inf")
+    out = torch.full((400, 4, 128), 7.0, dtype=F16, device="cuda")
+    kvq.prompt_attention(*(x.cuda()[:, a:b] for a, b in ((0, 4), (4, 6), (6, 8))), ints([3, 3, 200, 350]), 0.1, out=out)
+    assert (out[:3] == 7).all() and (out[350:] == 7).all()
+    inner = rows(400, 4, 2, 128, F16, seed=4)
+    want = check(inner[3:350], 4, 2, [0, 197, 347], 0.1)
+    # the same rows elsewhere in the pack: the same results but for the place of the tiles
+    assert torch.equal(out[3:350], want)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_later_tokens_do_not_reach_earlier_rows(bad, dtype):
+    """A bad value or key at one token leaves the rows before it, the other
+    sequences and the other heads bit for bit as they were."""
+    cu = [0, 90, 410, 500]
+    for at in (91, 150, 217, 218, 345, 409):
+        for part in ("k", "v"):
+            x = rows(500, 4, 2, 128, dtype, seed=6).cuda()
+            q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+            want = kvq.prompt_attention(q, k, v, ints(cu), 0.1)
+            (k if part == "k" else v)[at, 1, 5] = bad
+            got = kvq.prompt_attention(q, k, v, ints(cu), 0.1)
+            assert torch.equal(got[:at], want[:at]) and torch.equal(got[410:], want[410:])
+            assert torch.equal(got[:, :2], want[:, :2])
+            if part == "v":
+                hit = got[at:410, 2:]
+                keep = [c for c in range(128) if c != 5]
+                assert torch.equal(hit[..., keep], want[at:410, 2:][..., keep])
+                b = hit[..., 5].float()
+                assert torch.isnan(b).all() if math.isnan(bad) else (b[0] == bad).all() and (b == bad).sum() + torch.isnan(b).sum() == b.numel()
+
+
+def test_opposite_infinities_give_nan():
+    x = rows(200, 1, 1, 64, F16, seed=1)
+    x[100, 2, 3], x[120, 2, 3] = float("inf"), float("-inf")
+    x = x.cuda()
+    o = kvq.prompt_attention(x[:, :1], x[:, 1:2], x[:, 2:], ints([0, 200]), 0.01)[:, 0, 3].float()
+    assert torch.isfinite(o[:100]).all() and (o[100:120] == float("inf")).all() and torch.isnan(o[120:]).all()
+
+
+def test_bad_ranges_set_the_status():
+    x = rows(100, 2, 1, 64, F16, seed=2).cuda()
+    q, k, v = x[:, :2], x[:, 2:3], x[:, 3:]
+    for cu in ([0, 101], [-5, 50], [0, 40, 2 ** 31 - 1]):
+        out = torch.zeros(100, 2, 64, dtype=F16, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        kvq.prompt_attention(q, k, v, ints(cu), 0.1, out=out, status=status)
+        assert status.item() != 0
+        if len(cu) == 3:
+            assert torch.equal(out[:40], kvq.prompt_attention(q[:40], k[:40], v[:40], ints([0, 40]), 0.1))
+    # a sequence that ends before it starts holds no rows
+    out = torch.zeros(100, 2, 64, dtype=F16, device="cuda")
+    kvq.prompt_attention(q, k, v, ints([60, 30, 30]), 0.1, out=out)
+    assert not out.any()
+
+
+def test_stream_graph_and_launch_count():
+    x = rows(300, 4, 2, 128, BF16, seed=2).cuda()
+    q, k, v, cu = x[:, :4], x[:, 4:6], x[:, 6:], ints([0, 100, 300])
+    n = kvq.kernel_launches()
+    want = kvq.prompt_attention(q, k, v, cu, 0.1)
+    assert kvq.kernel_launches() == n + 1
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    got = kvq.prompt_attention(q, k, v, cu, 0.1, stream=st)
+    st.synchronize()
+    assert torch.equal(got, want)
+    out = torch.zeros_like(want)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        kvq.prompt_attention(q, k, v, cu, 0.1, out=out)
+    for lens in ([0, 100, 300], [0, 250, 260]):
+        cu.copy_(ints(lens))
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[:lens[2]], kvq.prompt_attention(q, k, v, cu, 0.1)[:lens[2]])
+
+
+def test_arguments_are_checked():
+    x = rows(10, 4, 2, 64, F16, seed=2).cuda()
+    q, k, v, cu = x[:, :4], x[:, 4:6], x[:, 6:], ints([0, 10])
+    for bad in (lambda: kvq.prompt_attention(q.float(), k, v, cu, 0.1), lambda: kvq.prompt_attention(q, k.bfloat16(), v, cu, 0.1),
+                lambda: kvq.prompt_attention(q, k, v, cu.long(), 0.1), lambda: kvq.prompt_attention(q.cpu(), k, v, cu, 0.1)):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: kvq.prompt_attention(q, k[:9], v, cu, 0.1), lambda: kvq.prompt_attention(q, k, v[:, :1], cu, 0.1),
+                lambda: kvq.prompt_attention(q.transpose(0, 1), k, v, cu, 0.1),
+                lambda: kvq.prompt_attention(q, k, v, cu, 0.1, out=torch.empty(10, 4, 32, dtype=F16, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: kvq.prompt_attention(q[:, :3], k, v, cu, 0.1), lambda: kvq.prompt_attention(q, k, v, cu, -0.1),
+                lambda: kvq.prompt_attention(x[..., :32].contiguous()[:, :4], x[..., :32].contiguous()[:, 4:6],
+                                             x[..., :32].contiguous()[:, 6:], cu, 0.1)):
+        with pytest.raises(kvq.KVQError):
+            bad()
