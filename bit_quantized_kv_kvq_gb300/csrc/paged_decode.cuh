@@ -193,9 +193,9 @@ struct Warp {
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-          const float now = fmaxf(m[nt][i], x);
-          const float f = now == -INFINITY ? 1.0f : exp2_fast(m[nt][i] - now);
-          m[nt][i] = now;
+          const bool mine = x > m[nt][i] + 8.0f;  // each head by its own scores
+          const float f = mine ? exp2_fast(m[nt][i] - x) : 1.0f;
+          m[nt][i] = mine ? x : m[nt][i];
           l[nt][i] *= f;
 #pragma unroll
           for (int j = 0; j < kSteps; ++j) o[nt][j][i] *= f, o[nt][j][2 + i] *= f;

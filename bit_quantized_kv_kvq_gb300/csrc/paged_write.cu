@@ -60,10 +60,11 @@ __global__ void __launch_bounds__(WriteCfg<P, D, CODE, BF16>::kThreads)
   if (m <= 0) return;
   const int j = w - (c0 / P + b);
   const int new_len = a.lens[b], old = new_len - m;
-  if (c0 < 0 || m > a.max_tokens - c0 || new_len < m || j < 0) {
+  if (c0 < 0 || m > a.max_tokens - c0 || new_len < m) {
     if (threadIdx.x == 0) raise_status(c.status, kStatusBadIndex);
     return;
   }
+  if (j < 0) return;  // before the first request's
   const int page0 = old / P, pages = new_len / P - page0;  // completed in this call
   const int half = threadIdx.x / Cfg::kHalf;               // 0: keys, 1: values
   const int tid = threadIdx.x - half * Cfg::kHalf;
