@@ -315,51 +315,72 @@ __global__ void __launch_bounds__(kThreads, 1)
       // nothing is in flight into this CTA's shared memory when it ends
       for (int k = max(0, i - C::kStages); k < i; ++k) wait(full_of(k), phase_of(k), a.status);
       for (int u = 0; u < (tiles1 > 0 ? 2 : 1); ++u) wait(&sh.q_full[u], 0, a.status);
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9) {
+      // The whole warp follows the schedule and one elected lane issues: with
+      // uniform control flow the operands stay in uniform registers, and an
+      // m128n128k16 issues every 64 clocks, the tensor cores' rate (in a
+      // branch of one lane it took 90).
       constexpr uint32_t kQK = t5::instr_desc(128, 128, BF16, false), kPV = t5::instr_desc(128, D, BF16, true);
-      const int nt[2] = {tiles0, tiles1};
+      const uint32_t tmem = sh.tmem;
+      const uint64_t dq = t5::smem_desc(smem_u32(smem), 16), dk = t5::smem_desc(smem_u32(ring), 16);
+      const uint64_t dv = t5::smem_desc(smem_u32(ring), kRows * 128);
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity, a.status)); };
       auto qk = [&](int u, int i) {
-        const uint32_t q = smem_u32(smem + u * C::kTile), k = smem_u32(ring + (i % C::kStages) * C::kTile);
+        const uint64_t q = dq + (uint32_t)(u * C::kTile >> 4), k = dk + (uint32_t)((i % C::kStages) * C::kTile >> 4);
+        if (t5::elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * (kRows * 128) + (kk % 4) * 32;
-          t5::mma_ss(sh.tmem + u * 128, t5::smem_desc(q + off, 16), t5::smem_desc(k + off, 16), kQK, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4;
+            t5::mma_ss(tmem + u * 128, q + off, k + off, kQK, kk > 0);
+          }
+          t5::commit(&sh.s_full[u]);
         }
-        t5::commit(&sh.s_full[u]);
+        __syncwarp();
       };
-      bool ok = wait(full_of(0), 0, a.status);
-      for (int u = 0; u < 2 && ok; ++u)
-        if (nt[u] > 0) {
-          ok = wait(&sh.q_full[u], 0, a.status);
+      auto pv = [&](int u, int i, bool first, bool last) {
+        const uint64_t v = dv + (uint32_t)((i % C::kStages) * C::kTile >> 4);
+        if (t5::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kRows / 16; ++kk)
+            t5::mma_ts(tmem + 256 + u * D, tmem + u * 128 + kk * 8, v + kk * (2048 >> 4), kPV, !first || kk > 0);
+          if (last) t5::commit(&sh.o_done[u]);
+        }
+        __syncwarp();
+      };
+      auto commit_one = [&](uint64_t* bar) {
+        if (t5::elect_one()) t5::commit(bar);
+        __syncwarp();
+      };
+      const int nt[2] = {tiles0, tiles1};
+      bool ok = wait_all(full_of(0), 0);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (ok && nt[u] > 0) {
+          ok = wait_all(&sh.q_full[u], 0);
           if (ok) qk(u, 0);
         }
-      if (ok) t5::commit(&sh.kv_empty[0]);
+      if (ok) commit_one(&sh.kv_empty[0]);
       for (int j = 0; j < tiles && ok; ++j) {
         const int vi = 2 * j + 1;
-        ok = wait(full_of(vi), phase_of(vi), a.status);
-        if (ok && cut(vi)) ok = wait(&sh.v_checked[j - (tiles0 - 1)], 0, a.status);
-        if (ok && j + 1 < tiles) ok = wait(full_of(vi + 1), phase_of(vi + 1), a.status);
-        const uint32_t v = smem_u32(ring + ((2 * j + 1) % C::kStages) * C::kTile);
-        for (int u = 0; u < 2 && ok; ++u) {
-          if (j < nt[u]) {
-            ok = wait(&sh.p_full[u], j & 1, a.status);
-            if (!ok) break;
-            t5::fence_after();
+        ok = wait_all(full_of(vi), phase_of(vi));
+        if (ok && cut(vi)) ok = wait_all(&sh.v_checked[j - (tiles0 - 1)], 0);
+        if (ok && j + 1 < tiles) ok = wait_all(full_of(vi + 1), phase_of(vi + 1));
 #pragma unroll
-            for (int kk = 0; kk < kRows / 16; ++kk)
-              t5::mma_ts(sh.tmem + 256 + u * D, sh.tmem + u * 128 + kk * 8, t5::smem_desc(v + kk * 2048, kRows * 128), kPV,
-                         j > 0 || kk > 0);
-            if (j == nt[u] - 1) t5::commit(&sh.o_done[u]);
+        for (int u = 0; u < 2; ++u) {
+          if (ok && j < nt[u]) {
+            ok = wait_all(&sh.p_full[u], j & 1);
+            t5::fence_after();
+            if (ok) pv(u, vi, j == 0, j == nt[u] - 1);
           }
-          if (j + 1 < nt[u]) qk(u, 2 * j + 2);
+          if (ok && j + 1 < nt[u]) qk(u, vi + 1);
         }
         if (ok) {
-          t5::commit(&sh.kv_empty[(2 * j + 1) % C::kStages]);
-          if (j + 1 < tiles) t5::commit(&sh.kv_empty[(2 * j + 2) % C::kStages]);
+          commit_one(&sh.kv_empty[vi % C::kStages]);
+          if (j + 1 < tiles) commit_one(&sh.kv_empty[(vi + 1) % C::kStages]);
         }
       }
-      t5::commit(&sh.drain);
-      wait(&sh.drain, 0, a.status);
+      commit_one(&sh.drain);
+      wait_all(&sh.drain, 0);
     } else if (warp >= 10) {
       for (int j = tiles0 - 1; j < tiles; ++j) {
         const int c = j - (tiles0 - 1);
