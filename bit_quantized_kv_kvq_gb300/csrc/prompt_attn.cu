@@ -10,12 +10,15 @@
 // S was) and V as TMA loaded it. P is rounded to the input type (half an eps
 // of each weight, zero mean: that of an output element); m, l, S and O are fp32.
 //
-// A CTA holds two units of 128 query rows x one head: two heads of a group on
+// A block is two units of 128 query rows x one head: two heads of a group on
 // the same rows (they share every key tile and its end), or, where the group
 // is odd, two row blocks of one head. While the tensor cores work for one
 // unit, the other's 128 threads (one row each) turn its scores into weights.
-// Warps 0-3 and 4-7: softmax of the units; 8: TMA; 9: tensor core issue;
-// 10, 11: the values of the tiles that the diagonal cuts (see check_values).
+// One persistent CTA per SM runs through blocks, and every role runs ahead of
+// the slower ones as far as its buffers go, so that a block's loads and first
+// scores overlap the end of the one before. Warps 0-3 and 4-7: softmax of the
+// units; 8: TMA; 9: tensor core issue; 10: the values of the tiles that the
+// diagonal cuts (check_values); 11: the order of the blocks (Order).
 #include "paged_internal.h"
 #include "tcgen05.cuh"
 #include "tensor_map.cuh"
@@ -34,13 +37,23 @@ struct Cfg {
   static constexpr int kSmem = 1024 + (2 + kStages) * kTile;
 };
 
+// A block of query rows: token c0 + q0 of a sequence of n tokens on.
+struct Block {
+  int c0, n, q0, hq0;  // hq0 < 0: no more blocks
+};
+
 struct Shared {
-  uint64_t q_full[2], s_full[2], p_full[2], o_done[2], drain;
-  uint64_t v_full[2], v_checked[2];  // value tiles that the diagonal cuts (the last one or two): loaded, checked
-  uint64_t kv_full[8], kv_empty[8];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], drain;
+  uint64_t kv_full[8], kv_empty[8];    // by ring stage
+  uint64_t v_full[8], v_checked[8];    // by ring stage: values of a tile that the diagonal cuts
+  uint64_t block_full[2], block_empty[2];
+  uint64_t fix_ready[2], fix_free[2];  // by parity of the block: `first` written, read
+  uint64_t* last_load[8];              // the barrier of the last load into each stage, and its phase
+  uint32_t last_phase[8];
+  Block block[2];
   uint32_t tmem;
-  int any_nonfinite;
-  int first[3][128];  // first token of the cut tiles whose value is NaN, +inf, -inf, per channel
+  int any_nonfinite[2];
+  int first[2][3][128];  // first token of the cut tiles whose value is NaN, +inf, -inf, per channel
 };
 
 template <bool BF16>
@@ -70,162 +83,514 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// Whole warp: false where the wait gave up.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
-  if (mbar_wait_bounded(bar, parity)) return true;
-  raise_status(status, kStatusTimeout);
-  return false;
+  const bool done = mbar_wait_bounded(bar, parity);
+  if (!done) raise_status(status, kStatusTimeout);
+  return __all_sync(0xffffffffu, done);
 }
+
+// Two barriers at once (the second may be NULL): one latency where both are done.
+__device__ __forceinline__ bool wait2(uint64_t* x, uint32_t px, uint64_t* y, uint32_t py, uint32_t* status) {
+  const bool dx = mbar_try_wait(x, px), dy = y == nullptr || mbar_try_wait(y, py);
+  if (__all_sync(0xffffffffu, dx && dy)) return true;
+  return wait(x, px, status) && (y == nullptr || wait(y, py, status));
+}
+
+// What all warps follow: the block's units and their key tiles.
+struct Units {
+  int tiles[2], row0[2], hq[2], most;
+  __device__ __forceinline__ Units(const Block& b, bool pair) {
+    row0[0] = b.q0;
+    row0[1] = pair ? b.q0 : b.q0 + kRows;
+    hq[0] = b.hq0;
+    hq[1] = pair ? b.hq0 + 1 : b.hq0;
+    tiles[0] = row0[0] / kRows + 1;
+    tiles[1] = row0[1] < b.n ? row0[1] / kRows + 1 : 0;
+    most = max(tiles[0], tiles[1]);
+  }
+  // The diagonal cuts the last tile of each unit: its values are checked.
+  __device__ __forceinline__ bool cut(int j) const { return j >= tiles[0] - 1; }
+};
+
+// The block of step `it`, for one warp; false at the end or on a timeout.
+__device__ __forceinline__ bool take_block(Shared* sh, int it, uint32_t* status, Block& b) {
+  const int slot = it & 1;
+  if (!wait(&sh->block_full[slot], (it >> 1) & 1, status)) return false;
+  b = sh->block[slot];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) arrive(&sh->block_empty[slot]);
+  return b.hq0 >= 0;
+}
+
+// Blocks in order of their number of key tiles, the longest first: level by
+// level of the row block's index, in each level the sequences that reach it
+// and their heads. CTA c of G takes blocks c, 2G - 1 - c, 2G + c, ...: the
+// turns even out the CTAs' sums. nb: row blocks of each sequence.
+struct Order {
+  const int* nb;
+  int seqs, lots, level;
+  uint32_t base, count;  // blocks before this level, and of it (below 2^31, the launch sees to it)
+
+  __device__ __forceinline__ Order(const int* nb_, int seqs_, int lots_) : nb(nb_), seqs(seqs_), lots(lots_) {
+    level = 0;
+    for (int s = threadIdx.x & 31; s < seqs; s += 32) level = max(level, nb[s]);
+    level = __reduce_max_sync(0xffffffffu, level);
+    base = count = 0;
+  }
+  __device__ __forceinline__ uint32_t reach(int s0) const {  // of 32 sequences, those with a row block `level`
+    const int s = s0 + (threadIdx.x & 31);
+    return __ballot_sync(0xffffffffu, s < seqs && nb[s] > level);
+  }
+  __device__ __forceinline__ Block get(const PromptArgs& a, int it, int span, bool pair) {
+    const uint32_t want = it * gridDim.x + (it & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    while (level >= 0 && want >= base + count) {
+      base += count;
+      --level;
+      int c = 0;
+      for (int s0 = 0; level >= 0 && s0 < seqs; s0 += 32) c += __popc(reach(s0));
+      count = (uint32_t)c * lots;
+    }
+    Block b;
+    b.c0 = b.n = b.q0 = 0;
+    b.hq0 = -1;
+    if (level < 0) return b;
+    int at = (int)((want - base) / (uint32_t)lots), s = 0;
+    const int lot = (int)((want - base) % (uint32_t)lots);
+    for (int s0 = 0; s0 < seqs; s0 += 32) {
+      const uint32_t m = reach(s0);
+      if (__popc(m) > at) {
+        const int lane = threadIdx.x & 31;
+        const bool mine = ((m >> lane) & 1) && __popc(m & ((1u << lane) - 1)) == at;
+        s = s0 + __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+        break;
+      }
+      at -= __popc(m);
+    }
+    b.c0 = a.cu[s];
+    b.n = a.cu[s + 1] - b.c0;
+    b.q0 = level * span;
+    b.hq0 = pair ? 2 * lot : lot;
+    return b;
+  }
+};
 
 // 0 * inf would carry a later token's infinity or NaN to an earlier row. In
 // the tiles that the diagonal cuts, the tensor cores get 0 in their place; the
-// rows from that token on get them at the end (Shared::first).
+// rows from that token on get them at the end (Shared::first). One warp; a
+// tile of finite values (0 * x summed is 0) costs one multiply-add a pair.
+template <bool BF16>
+__device__ __forceinline__ uint32_t fma_zero(uint32_t x, uint32_t acc) {
+  if (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+  else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+  return acc;
+}
 template <int D, bool BF16>
-__device__ __forceinline__ void check_values(unsigned char* tile, int k0, Shared* sh) {
-  constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u, kStep = BF16 ? 0x0080u : 0x0400u;
-  const int tid = threadIdx.x - 320;
-  for (int i = tid; i < kRows * D / 8; i += 64) {
-    uint4* at = reinterpret_cast<uint4*>(tile) + i;
-    uint4 x = *at;
-    // an exponent of all ones carries into the sign bit's place
-    const uint32_t hit = ((x.x & (kInf * 0x10001u)) + kStep * 0x10001u) | ((x.y & (kInf * 0x10001u)) + kStep * 0x10001u) |
-                         ((x.z & (kInf * 0x10001u)) + kStep * 0x10001u) | ((x.w & (kInf * 0x10001u)) + kStep * 0x10001u);
-    if ((hit & 0x80008000u) == 0) continue;
-    // 16-byte chunk i of the tile: 64-channel half, token row, swizzled place
-    const int row = (i >> 3) & 127, ch = (i >> 10) * 64 + (((i & 7) ^ (row & 7)) << 3);
-    __align__(16) uint16_t e[8];
-    *reinterpret_cast<uint4*>(e) = x;
+__device__ __forceinline__ void check_values(unsigned char* tile, int k0, int (*first)[128], int* any) {
+  constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
+  constexpr int kBatch = 8;
+  for (int i0 = threadIdx.x & 31; i0 < kRows * D / 8; i0 += 32 * kBatch) {
+    uint4 x[kBatch];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if ((e[j] & kInf) == kInf) {
-        const int kind = (e[j] & 0x7fffu) != kInf ? 0 : (e[j] >> 15) ? 2 : 1;
-        atomicMin(&sh->first[kind][ch + j], k0 + row);
-        sh->any_nonfinite = 1;
-        e[j] = 0;
-      }
-    *at = *reinterpret_cast<uint4*>(e);
+    for (int k = 0; k < kBatch; ++k) x[k] = reinterpret_cast<uint4*>(tile)[i0 + 32 * k];
+    uint32_t acc[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      acc[0] = fma_zero<BF16>(x[k].x, acc[0]);
+      acc[1] = fma_zero<BF16>(x[k].y, acc[1]);
+      acc[2] = fma_zero<BF16>(x[k].z, acc[2]);
+      acc[3] = fma_zero<BF16>(x[k].w, acc[3]);
+    }
+    // +-0 where all were finite
+    if ((((acc[0] | acc[1]) | (acc[2] | acc[3])) & 0x7fff7fffu) == 0) continue;
+#pragma unroll 1
+    for (int k = 0; k < kBatch; ++k) {
+      // 16-byte chunk i of the tile: 64-channel half, token row, swizzled place
+      const int i = i0 + 32 * k, row = (i >> 3) & 127, ch = (i >> 10) * 64 + (((i & 7) ^ (row & 7)) << 3);
+      uint16_t* e = reinterpret_cast<uint16_t*>(tile) + i * 8;
+#pragma unroll 1
+      for (int j = 0; j < 8; ++j)
+        if ((e[j] & kInf) == kInf) {
+          const int kind = (e[j] & 0x7fffu) != kInf ? 0 : (e[j] >> 15) ? 2 : 1;
+          atomicMin(&first[kind][ch + j], k0 + row);
+          *any = 1;
+          e[j] = 0;
+        }
+    }
   }
 }
 
-// One unit's rows: scores to weights tile by tile, then the output.
+// 2 N scores of a row to weights: p = 2^(s sc - ref), packed, and their sum.
+template <bool BF16, int N>
+__device__ __forceinline__ uint64_t to_weights(const uint32_t* s, uint64_t sc2, float ref, uint32_t* p) {
+  const uint64_t ref2 = f2_pack(-ref, -ref);
+  uint64_t sum0 = f2_pack(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float x, y;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, ref2), x, y);
+    x = exp2_fast(x);
+    y = exp2_fast(y);
+    if (i & 1) sum1 = f2_add(sum1, f2_pack(x, y));
+    else sum0 = f2_add(sum0, f2_pack(x, y));
+    p[i] = pack2<BF16>(x, y);
+  }
+  return f2_add(sum0, sum1);
+}
+
+template <int N>
+__device__ __forceinline__ float max_of(const uint32_t* s) {
+  float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < N; c += 8) {
+    t0 = fmaxf(fmaxf(t0, __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
+    t1 = fmaxf(fmaxf(t1, __uint_as_float(s[c + 2])), __uint_as_float(s[c + 3]));
+    t2 = fmaxf(fmaxf(t2, __uint_as_float(s[c + 4])), __uint_as_float(s[c + 5]));
+    t3 = fmaxf(fmaxf(t3, __uint_as_float(s[c + 6])), __uint_as_float(s[c + 7]));
+  }
+  return fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+}
+
+// The reference m of a row's exponentials moves only when a score passes it by
+// 8 (weights stay below 2^8), so that few tiles scale O (o: it has a value).
+// Each row goes by its own scores: its bits do not depend on its neighbours.
+template <int D>
+__device__ __forceinline__ void raise_reference(float top, float& m, float& l, uint32_t tO, bool o) {
+  const bool up = top > m + 8.0f;
+  if (!__any_sync(0xffffffffu, up)) return;
+  const float f = up ? exp2_fast(m - top) : 1.0f;
+  m = up ? top : m;
+  l *= f;
+  if (!o) return;
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    uint32_t x[32];
+    t5::ld32(tO + c, x);
+    t5::wait_ld32(x);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+    t5::st32(tO + c, x);
+  }
+}
+
+// 64 bytes of an output row: whole 32-byte sectors where `out` is so aligned.
+__device__ __forceinline__ void store_row(uint16_t* to, const uint32_t* w, bool wide) {
+  if (wide) {
+#pragma unroll
+    for (int q = 0; q < 16; q += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 2 * q), "r"(w[q]), "r"(w[q + 1]),
+                   "r"(w[q + 2]), "r"(w[q + 3]), "r"(w[q + 4]), "r"(w[q + 5]), "r"(w[q + 6]), "r"(w[q + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int q = 0; q < 16; q += 4)
+      *reinterpret_cast<uint4*>(to + 2 * q) = make_uint4(w[q], w[q + 1], w[q + 2], w[q + 3]);
+  }
+}
+
+// One unit's warps: scores to weights tile by tile, then the output rows.
 template <int D, bool BF16>
-__device__ __forceinline__ void softmax_unit(const PromptArgs& a, Shared* sh, unsigned char* stage, int unit, int row0,
-                                             int tiles, int n, int c0, int hq, int check) {
+__device__ __forceinline__ void softmax_role(const PromptArgs& a, Shared* sh, const int unit, const bool pair) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, r = warp * 32 + lane;
   const uint32_t lanes = sh->tmem + ((uint32_t)(warp * 32) << 16);
   const uint32_t tS = lanes + unit * 128, tP = tS, tO = lanes + 256 + unit * D;
   const float sc = a.scale_log2;
-  float m = -INFINITY, l = 0.0f;
-  bool ok = true;
-  for (int j = 0; j < tiles && ok; ++j) {
-    ok = __all_sync(0xffffffffu, wait(&sh->s_full[unit], j & 1, a.status));
-    if (!ok) break;
-    t5::fence_after();
-    uint32_t s[128];
+  const uint64_t sc2 = f2_pack(sc, sc);
+  const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+  uint32_t tile_phase = 0, out_phase = 0;
+  Block b;
+  for (int it = 0; take_block(sh, it, a.status, b); ++it) {
+    const Units un(b, pair);
+    const int tiles = unit ? un.tiles[1] : un.tiles[0], row = (unit ? un.row0[1] : un.row0[0]) + r;
+    float m = -INFINITY, l = 0.0f;
+    for (int j = 0; j < tiles; ++j, tile_phase ^= 1) {
+      if (!wait(&sh->s_full[unit], tile_phase, a.status)) return;
+      t5::fence_after();
+      uint64_t sum;
+      if (j < tiles - 1) {
+        uint32_t s[128], p[32];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) t5::ld32(tS + 32 * c, s + 32 * c);
+        for (int c = 0; c < 4; ++c) t5::ld32(tS + 32 * c, s + 32 * c);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) t5::wait_ld32(s + 32 * c);
-    if (j == tiles - 1) {  // the tile the diagonal cuts: keys of this block after the row
-#pragma unroll
-      for (int c = 0; c < 128; ++c)
-        if (c > r) s[c] = 0xff800000u;
-    }
-    float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < 128; c += 8) {
-      t0 = fmaxf(fmaxf(t0, __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
-      t1 = fmaxf(fmaxf(t1, __uint_as_float(s[c + 2])), __uint_as_float(s[c + 3]));
-      t2 = fmaxf(fmaxf(t2, __uint_as_float(s[c + 4])), __uint_as_float(s[c + 5]));
-      t3 = fmaxf(fmaxf(t3, __uint_as_float(s[c + 6])), __uint_as_float(s[c + 7]));
-    }
-    const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sc;
-    // The reference m moves only when a score passes it by 8 (weights stay
-    // below 2^8), so that few tiles scale O. Each row goes by its own scores:
-    // a row's bits do not depend on its neighbours. s_full came after the last PV.
-    const bool up = top > m + 8.0f;
-    if (__any_sync(0xffffffffu, up)) {
-      const float f = up ? exp2_fast(m - top) : 1.0f;
-      m = up ? top : m;
-      l *= f;
-      if (j > 0) {
+        for (int c = 0; c < 4; ++c) t5::wait_ld32(s + 32 * c);
+        raise_reference<D>(max_of<128>(s) * sc, m, l, tO, j > 0);  // s_full came after the last PV
+        const float ref = m == -INFINITY ? 0.0f : m;
+        sum = to_weights<BF16, 32>(s, sc2, ref, p);
+        t5::st32(tP, p);
+        sum = f2_add(sum, to_weights<BF16, 32>(s + 64, sc2, ref, p));
+        t5::st32(tP + 32, p);
+      } else {
+        // The tile the diagonal cuts, by groups of 32 keys: the warp's rows see
+        // all of the first `warp` groups, up to the row's own key of the next,
+        // and nothing after. (P of a group lies where scores already read were.)
+        float top = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          t5::ld32(tO + c, o);
-          t5::wait_ld32(o);
+        for (int c = 0; c <= warp; ++c) {
+          uint32_t s[32];
+          t5::ld32(tS + 32 * c, s);
+          t5::wait_ld32(s);
+          if (c == warp) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          t5::st32(tO + c, o);
+            for (int i = 0; i < 32; ++i)
+              if (i > lane) s[i] = 0xff800000u;
+          }
+          top = fmaxf(top, max_of<32>(s));
+        }
+        raise_reference<D>(top * sc, m, l, tO, j > 0);
+        const float ref = m == -INFINITY ? 0.0f : m;
+        sum = f2_pack(0.0f, 0.0f);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t s[32], p[16];
+          if (c <= warp) {
+            t5::ld32(tS + 32 * c, s);
+            t5::wait_ld32(s);
+            if (c == warp) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i > lane) s[i] = 0xff800000u;
+            }
+            sum = f2_add(sum, to_weights<BF16, 16>(s, sc2, ref, p));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[i] = 0u;
+          }
+          t5::st16(tP + 16 * c, p);
         }
       }
+      t5::wait_st();
+      t5::fence_before();
+      arrive(&sh->p_full[unit]);
+      float x, y;
+      f2_unpack(sum, x, y);
+      l += x + y;
     }
-    const float ref = m == -INFINITY ? 0.0f : m;
-    const uint64_t sc2 = f2_pack(sc, sc), ref2 = f2_pack(-ref, -ref);
-    uint64_t sum0 = f2_pack(0.0f, 0.0f), sum1 = sum0;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t p[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int c = half * 64 + 2 * i;
-        float x, y;
-        f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, ref2), x, y);
-        x = exp2_fast(x);
-        y = exp2_fast(y);
-        if (i & 1) sum1 = f2_add(sum1, f2_pack(x, y));
-        else sum0 = f2_add(sum0, f2_pack(x, y));
-        p[i] = pack2<BF16>(x, y);
-      }
-      t5::st32(tP + half * 32, p);
-    }
-    float x, y;
-    f2_unpack(f2_add(sum0, sum1), x, y);
-    l += x + y;
-    t5::wait_st();
-    t5::fence_before();
-    arrive(&sh->p_full[unit]);
-  }
-  if (tiles == 0) return;  // all of the unit's threads
-  if (ok) ok = __all_sync(0xffffffffu, wait(&sh->o_done[unit], 0, a.status) && wait(&sh->v_checked[check], 0, a.status));
-  if (ok) {
-    t5::fence_after();
-    const float inv = 1.0f / l;
-    const int row = row0 + r;
-    const bool fix = sh->any_nonfinite != 0;
+    const int par = it & 1;
+    // an empty unit waits too: its arrival on fix_free counts for this block
+    if (!wait(&sh->fix_ready[par], (it >> 1) & 1, a.status)) return;
+    if (tiles > 0) {
+      if (!wait(&sh->o_done[unit], out_phase, a.status)) return;
+      out_phase ^= 1;
+      t5::fence_after();
+      const float inv = 1.0f / l;
+      const bool fix = sh->any_nonfinite[par] != 0;
+      uint16_t* out = a.out + ((int64_t)(b.c0 + row) * a.q_heads + (unit ? un.hq[1] : un.hq[0])) * D;
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
-      uint32_t o[32];
-      t5::ld32(tO + c, o);
-      t5::wait_ld32(o);
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32], w[16];
+        t5::ld32(tO + c, o);
+        t5::wait_ld32(o);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        float x = __uint_as_float(o[i]) * inv;
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
         if (fix) {
-          if (row >= sh->first[1][c + i]) x += INFINITY;
-          if (row >= sh->first[2][c + i]) x -= INFINITY;
-          if (row >= sh->first[0][c + i]) x = NAN;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float x = __uint_as_float(o[i]);
+            if (row >= sh->first[par][1][c + i]) x += INFINITY;
+            if (row >= sh->first[par][2][c + i]) x -= INFINITY;
+            if (row >= sh->first[par][0][c + i]) x = NAN;
+            o[i] = __float_as_uint(x);
+          }
         }
-        o[i] = __float_as_uint(x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack2<BF16>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+        if (row < b.n) store_row(out + c, w, wide);
       }
+      t5::fence_before();  // O has been read: ordered before the next block's first weights
+    }
+    __syncwarp();
+    if (lane == 0) arrive(&sh->fix_free[par]);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void load_role(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                                          const PromptArgs& a, Shared* sh, unsigned char* smem, bool pair) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31, group = a.q_heads / a.kv_heads;
+  unsigned char* ring = smem + 2 * C::kTile;
+  uint32_t q_phase[2] = {0, 0}, full_phase = 0, cut_phase = 0;
+  int i = 0;  // loads into the ring so far
+  bool ok = true;
+  Block b;
+  for (int it = 0; ok && take_block(sh, it, a.status, b); ++it) {
+    const Units un(b, pair);
+    const int h = b.hq0 / group;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = pack2<BF16>(__uint_as_float(o[8 * q + 2 * i]), __uint_as_float(o[8 * q + 2 * i + 1]));
-        const int chunk = c / 8 + q;
-        *reinterpret_cast<uint4*>(stage + r * (D * 2) + ((chunk ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int u = 0; u < 2; ++u) {
+      if (!ok || un.tiles[u] == 0) continue;
+      // the first wait is for the phase before the first and passes at once
+      ok = wait(&sh->q_empty[u], q_phase[u] ^ 1, a.status);
+      if (!ok) break;
+      q_phase[u] ^= 1;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sh->q_full[u], C::kTile);
+        for (int x = 0; x < D / 64; ++x)
+          tma_tile(smem_u32(smem + u * C::kTile + x * (kRows * 128)), &mq, x * 64, un.hq[u], b.c0 + un.row0[u],
+                   &sh->q_full[u]);
+      }
+    }
+    for (int k = 0; ok && k < 2 * un.most; ++k, ++i) {  // keys, values, keys, ...
+      const int st = i % C::kStages;
+      ok = wait(&sh->kv_empty[st], ((i / C::kStages) & 1) ^ 1, a.status);
+      if (!ok) break;
+      const bool cut = (k & 1) && un.cut(k >> 1);
+      uint64_t* bar = cut ? &sh->v_full[st] : &sh->kv_full[st];
+      const uint32_t phase = ((cut ? cut_phase : full_phase) >> st) & 1;
+      if (cut) cut_phase ^= 1u << st;
+      else full_phase ^= 1u << st;
+      if (lane == 0) {
+        sh->last_load[st] = bar;
+        sh->last_phase[st] = phase;
+        mbar_arrive_expect_tx(bar, C::kTile);
+        for (int x = 0; x < D / 64; ++x)
+          tma_tile(smem_u32(ring + st * C::kTile + x * (kRows * 128)), k & 1 ? &mv : &mk, x * 64, h,
+                   b.c0 + (k >> 1) * kRows, bar);
       }
     }
   }
-  // through the unit's query tile (no longer read) to whole rows in order
-  asm volatile("bar.sync %0, 128;" ::"r"(1 + unit) : "memory");
-  if (!ok) return;
-  for (int i = r; i < kRows * (D / 8); i += 128) {
-    const int row = i / (D / 8), chunk = i % (D / 8);
-    if (row0 + row < n)
-      *reinterpret_cast<uint4*>(a.out + ((int64_t)(c0 + row0 + row) * a.q_heads + hq) * D + chunk * 8) =
-          *reinterpret_cast<const uint4*>(stage + row * (D * 2) + ((chunk ^ (row & 7)) << 4));
+  __syncwarp();
+  // nothing is in flight into this CTA's shared memory when it ends
+  for (int st = 0; st < min(i, C::kStages); ++st) wait(sh->last_load[st], sh->last_phase[st], a.status);
+  for (int u = 0; u < 2; ++u) wait(&sh->q_full[u], q_phase[u] ^ 1, a.status);
+}
+
+// The whole warp follows the schedule and one elected lane issues: with
+// uniform control flow the operands stay in uniform registers, and an
+// m128n128k16 issues every 64 clocks, the tensor cores' rate (in a branch of
+// one lane it took 90). One warp serves both units, first one, then the other:
+// that keeps their softmaxes out of step (with a warp for each unit they ran
+// side by side, and the tensor cores idled: 1620 us instead of 1390 for a
+// prompt of 16384).
+template <int D, bool BF16>
+__device__ __forceinline__ void mma_role(const PromptArgs& a, Shared* sh, unsigned char* smem, bool pair) {
+  using C = Cfg<D>;
+  constexpr uint32_t kQK = t5::instr_desc(128, 128, BF16, false), kPV = t5::instr_desc(128, D, BF16, true);
+  const uint32_t tmem = sh->tmem;
+  const unsigned char* ring = smem + 2 * C::kTile;
+  const uint64_t dq = t5::smem_desc(smem_u32(smem), 16), dk = t5::smem_desc(smem_u32(ring), 16);
+  const uint64_t dv = t5::smem_desc(smem_u32(ring), kRows * 128);
+  uint32_t q_phase = 0, p_phase[2] = {0, 0}, full_phase = 0, cut_phase = 0;
+  // S of unit u from the key tile in stage st
+  auto scores = [&](int u, int st) {
+    const uint64_t q = dq + (uint32_t)(u * C::kTile >> 4), k = dk + (uint32_t)(st * C::kTile >> 4);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint32_t off = ((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4;
+      t5::mma_ss(tmem + u * 128, q + off, k + off, kQK, kk > 0);
+    }
+    t5::commit(&sh->s_full[u]);
+  };
+  int i = 0;
+  bool ok = true;
+  Block b;
+  for (int it = 0; ok && take_block(sh, it, a.status, b); ++it) {
+    const Units un(b, pair);
+    {
+      const int st = i % C::kStages;
+      ok = wait(&sh->kv_full[st], (full_phase >> st) & 1, a.status);
+      full_phase ^= 1u << st;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (ok && un.tiles[u] > 0) {
+          ok = wait(&sh->q_full[u], (q_phase >> u) & 1, a.status);
+          q_phase ^= 1u << u;
+          if (ok && t5::elect_one()) {
+            scores(u, st);
+            if (un.tiles[u] == 1) t5::commit(&sh->q_empty[u]);
+          }
+          __syncwarp();
+        }
+      if (ok && t5::elect_one()) t5::commit(&sh->kv_empty[st]);
+      __syncwarp();
+    }
+    for (int j = 0; j < un.most && ok; ++j) {
+      const int sv = (i + 2 * j + 1) % C::kStages, sk = (i + 2 * j + 2) % C::kStages;
+      const bool more = j + 1 < un.most, cut = un.cut(j);
+      // this tile's values and the next one's keys
+      const uint32_t vp = ((cut ? cut_phase : full_phase) >> sv) & 1;
+      ok = wait2(cut ? &sh->v_checked[sv] : &sh->kv_full[sv], vp, more ? &sh->kv_full[sk] : nullptr,
+                 (full_phase >> sk) & 1, a.status);
+      if (cut) cut_phase ^= 1u << sv;
+      else full_phase ^= 1u << sv;
+      if (more) full_phase ^= 1u << sk;
+      const uint64_t v = dv + (uint32_t)(sv * C::kTile >> 4);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bool mine = j < un.tiles[u], next = j + 1 < un.tiles[u];
+        if (ok && mine) {
+          ok = wait(&sh->p_full[u], p_phase[u], a.status);
+          p_phase[u] ^= 1;
+          t5::fence_after();
+        }
+        if (ok && t5::elect_one()) {
+          if (mine) {
+#pragma unroll
+            for (int kk = 0; kk < kRows / 16; ++kk)
+              t5::mma_ts(tmem + 256 + u * D, tmem + u * 128 + kk * 8, v + kk * (2048 >> 4), kPV, j > 0 || kk > 0);
+            if (!next) t5::commit(&sh->o_done[u]);
+          }
+          if (u) t5::commit(&sh->kv_empty[sv]);
+          if (next) {
+            scores(u, sk);
+            if (j + 1 == un.tiles[u] - 1) t5::commit(&sh->q_empty[u]);
+          }
+          if (u && more) t5::commit(&sh->kv_empty[sk]);
+        }
+        __syncwarp();
+      }
+    }
+    i += 2 * un.most;
+  }
+  __syncwarp();
+  if (t5::elect_one()) t5::commit(&sh->drain);
+  __syncwarp();
+  wait(&sh->drain, 0, a.status);
+}
+
+// Hands out the blocks.
+__device__ __forceinline__ void order_role(const PromptArgs& a, Shared* sh, Order order, int span, bool pair) {
+  for (int it = 0;; ++it) {
+    const Block b = order.get(a, it, span, pair);
+    const int slot = it & 1;
+    if (it >= 2 && !wait(&sh->block_empty[slot], ((it >> 1) - 1) & 1, a.status)) return;
+    if ((threadIdx.x & 31) == 0) {
+      sh->block[slot] = b;
+      arrive(&sh->block_full[slot]);
+    }
+    __syncwarp();
+    if (b.hq0 < 0) return;
+  }
+}
+
+template <int D, bool BF16>
+__device__ __forceinline__ void check_role(const PromptArgs& a, Shared* sh, unsigned char* ring, bool pair) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31;
+  uint32_t cut_phase = 0;
+  int i = 0;
+  Block b;
+  for (int it = 0; take_block(sh, it, a.status, b); ++it) {
+    const Units un(b, pair);
+    const int par = it & 1;
+    // the rows of the block before the last have read what this one overwrites
+    if (!wait(&sh->fix_free[par], ((it >> 1) & 1) ^ 1, a.status)) return;
+    if (it < 2 || sh->any_nonfinite[par]) {
+      for (int k = lane; k < 3 * 128; k += 32) sh->first[par][k / 128][k % 128] = kNever;
+      __syncwarp();
+      if (lane == 0) sh->any_nonfinite[par] = 0;
+    }
+    __syncwarp();
+    for (int j = un.tiles[0] - 1; j < un.most; ++j) {
+      const int st = (i + 2 * j + 1) % C::kStages;
+      if (!wait(&sh->v_full[st], (cut_phase >> st) & 1, a.status)) return;
+      cut_phase ^= 1u << st;
+      check_values<D, BF16>(ring + st * C::kTile, j * kRows, sh->first[par], &sh->any_nonfinite[par]);
+      fence_proxy_async_smem();  // the tensor cores read what was written here
+      arrive(&sh->v_checked[st]);
+    }
+    arrive(&sh->fix_ready[par]);
+    i += 2 * un.most;
   }
 }
 
@@ -237,159 +602,58 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   __shared__ Shared sh;
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int span = pair ? kRows : 2 * kRows;  // query rows of the CTA
-  const int lots = pair ? a.q_heads / 2 : a.q_heads;                          // heads or pairs of them
-  const int lot = blockIdx.x % lots, w = (gridDim.x - 1 - blockIdx.x) / lots;  // the longest blocks first
-  const int group = a.q_heads / a.kv_heads;
-  const int* cu = a.cu;
-  // row blocks of sequence s start at floor(cu[s] / span) + s: room for all of them
-  const int s = warp_last_le(a.seqs, w, [&](int i) { return (int)((uint32_t)cu[i] / (uint32_t)span) + i; });
-  const int c0 = cu[s], n = cu[s + 1] - c0;
-  if (n <= 0) return;
-  if (c0 < 0 || n > a.tokens - c0) {
-    if (threadIdx.x == 0 && lot == 0) raise_status(a.status, kStatusBadIndex);
-    return;
-  }
-  const int block = w - (c0 / span + s), q0 = block * span;
-  if (block < 0 || q0 >= n) return;
-  const int hq0 = pair ? 2 * lot : lot, h = hq0 / group;
-  const int row1 = pair ? q0 : q0 + kRows;  // of unit 1
-  const int tiles0 = q0 / kRows + 1, tiles1 = row1 < n ? row1 / kRows + 1 : 0;
-  const int tiles = max(tiles0, tiles1);
+  int* nb = reinterpret_cast<int*>(smem + (2 + C::kStages) * C::kTile);  // [seqs]
+  const int warp = threadIdx.x >> 5;
+  const int span = pair ? kRows : 2 * kRows;           // query rows of a block
+  const int lots = pair ? a.q_heads / 2 : a.q_heads;   // heads or pairs of them
 
+  if (threadIdx.x == 32) {
+    prefetch_map(&mq);
+    prefetch_map(&mk);
+    prefetch_map(&mv);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], 128);
       mbar_init(&sh.o_done[i], 1);
-      mbar_init(&sh.v_full[i], 1);
-      mbar_init(&sh.v_checked[i], 64);
+      mbar_init(&sh.block_full[i], 1);
+      mbar_init(&sh.block_empty[i], 11);  // every warp but the one that fills it
+      mbar_init(&sh.fix_ready[i], 32);
+      mbar_init(&sh.fix_free[i], 8);
     }
     mbar_init(&sh.drain, 1);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sh.kv_full[i], 1);
       mbar_init(&sh.kv_empty[i], 1);
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_checked[i], 32);
     }
     mbar_fence_init();
-    sh.any_nonfinite = 0;
   }
-  for (int i = threadIdx.x; i < 3 * D; i += kThreads) sh.first[i / D][i % D] = kNever;
+  for (int s = threadIdx.x; s < a.seqs; s += kThreads) {
+    const int c0 = a.cu[s], n = a.cu[s + 1] - c0;
+    const bool bad = n > 0 && (c0 < 0 || n > a.tokens - c0);
+    if (bad && blockIdx.x == 0) raise_status(a.status, kStatusBadIndex);
+    nb[s] = n > 0 && !bad ? (n + span - 1) / span : 0;
+  }
   if (warp == 9) t5::alloc(&sh.tmem, 512);
   t5::fence_before();
   __syncthreads();
   t5::fence_after();
 
-  unsigned char* ring = smem + 2 * C::kTile;
-  // Load i (2 j: keys of tile j, 2 j + 1: its values) and its barrier. The cut
-  // tiles' values have one each, used once, so that the checking warps need
-  // not follow the ring's phases.
-  auto cut = [&](int i) { return (i & 1) && (i >> 1) >= tiles0 - 1; };
-  auto full_of = [&](int i) { return cut(i) ? &sh.v_full[(i >> 1) - (tiles0 - 1)] : &sh.kv_full[i % C::kStages]; };
-  auto phase_of = [&](int i) { return cut(i) ? 0u : (uint32_t)(i / C::kStages) & 1u; };
   if (warp < 8) {
+    // 256 threads x 208 + 128 x 88 registers = 384 x 168, what the launch holds
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int unit = warp >> 2;
-    softmax_unit<D, BF16>(a, &sh, smem + unit * C::kTile, unit, unit ? row1 : q0, unit ? tiles1 : tiles0, n, c0,
-                          unit && pair ? hq0 + 1 : hq0, unit && !pair ? 1 : 0);
+    softmax_role<D, BF16>(a, &sh, warp >> 2, pair);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8 && lane == 0) {
-      for (int u = 0; u < (tiles1 > 0 ? 2 : 1); ++u) {
-        mbar_arrive_expect_tx(&sh.q_full[u], C::kTile);
-        for (int b = 0; b < D / 64; ++b)
-          tma_tile(smem_u32(smem + u * C::kTile + b * (kRows * 128)), &mq, b * 64, u && pair ? hq0 + 1 : hq0,
-                   c0 + (u ? row1 : q0), &sh.q_full[u]);
-      }
-      int i = 0;
-      for (; i < 2 * tiles; ++i) {
-        const int st = i % C::kStages;
-        if (i >= C::kStages && !wait(&sh.kv_empty[st], (i / C::kStages - 1) & 1, a.status)) break;
-        uint64_t* bar = full_of(i);
-        mbar_arrive_expect_tx(bar, C::kTile);
-        for (int b = 0; b < D / 64; ++b)
-          tma_tile(smem_u32(ring + st * C::kTile + b * (kRows * 128)), i & 1 ? &mv : &mk, b * 64, h,
-                   c0 + (i >> 1) * kRows, bar);
-      }
-      // nothing is in flight into this CTA's shared memory when it ends
-      for (int k = max(0, i - C::kStages); k < i; ++k) wait(full_of(k), phase_of(k), a.status);
-      for (int u = 0; u < (tiles1 > 0 ? 2 : 1); ++u) wait(&sh.q_full[u], 0, a.status);
-    } else if (warp == 9) {
-      // The whole warp follows the schedule and one elected lane issues: with
-      // uniform control flow the operands stay in uniform registers, and an
-      // m128n128k16 issues every 64 clocks, the tensor cores' rate (in a
-      // branch of one lane it took 90).
-      constexpr uint32_t kQK = t5::instr_desc(128, 128, BF16, false), kPV = t5::instr_desc(128, D, BF16, true);
-      const uint32_t tmem = sh.tmem;
-      const uint64_t dq = t5::smem_desc(smem_u32(smem), 16), dk = t5::smem_desc(smem_u32(ring), 16);
-      const uint64_t dv = t5::smem_desc(smem_u32(ring), kRows * 128);
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity, a.status)); };
-      auto qk = [&](int u, int i) {
-        const uint64_t q = dq + (uint32_t)(u * C::kTile >> 4), k = dk + (uint32_t)((i % C::kStages) * C::kTile >> 4);
-        if (t5::elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4;
-            t5::mma_ss(tmem + u * 128, q + off, k + off, kQK, kk > 0);
-          }
-          t5::commit(&sh.s_full[u]);
-        }
-        __syncwarp();
-      };
-      auto pv = [&](int u, int i, bool first, bool last) {
-        const uint64_t v = dv + (uint32_t)((i % C::kStages) * C::kTile >> 4);
-        if (t5::elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < kRows / 16; ++kk)
-            t5::mma_ts(tmem + 256 + u * D, tmem + u * 128 + kk * 8, v + kk * (2048 >> 4), kPV, !first || kk > 0);
-          if (last) t5::commit(&sh.o_done[u]);
-        }
-        __syncwarp();
-      };
-      auto commit_one = [&](uint64_t* bar) {
-        if (t5::elect_one()) t5::commit(bar);
-        __syncwarp();
-      };
-      const int nt[2] = {tiles0, tiles1};
-      bool ok = wait_all(full_of(0), 0);
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        if (ok && nt[u] > 0) {
-          ok = wait_all(&sh.q_full[u], 0);
-          if (ok) qk(u, 0);
-        }
-      if (ok) commit_one(&sh.kv_empty[0]);
-      for (int j = 0; j < tiles && ok; ++j) {
-        const int vi = 2 * j + 1;
-        ok = wait_all(full_of(vi), phase_of(vi));
-        if (ok && cut(vi)) ok = wait_all(&sh.v_checked[j - (tiles0 - 1)], 0);
-        if (ok && j + 1 < tiles) ok = wait_all(full_of(vi + 1), phase_of(vi + 1));
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (ok && j < nt[u]) {
-            ok = wait_all(&sh.p_full[u], j & 1);
-            t5::fence_after();
-            if (ok) pv(u, vi, j == 0, j == nt[u] - 1);
-          }
-          if (ok && j + 1 < nt[u]) qk(u, vi + 1);
-        }
-        if (ok) {
-          commit_one(&sh.kv_empty[vi % C::kStages]);
-          if (j + 1 < tiles) commit_one(&sh.kv_empty[(vi + 1) % C::kStages]);
-        }
-      }
-      commit_one(&sh.drain);
-      wait_all(&sh.drain, 0);
-    } else if (warp >= 10) {
-      for (int j = tiles0 - 1; j < tiles; ++j) {
-        const int c = j - (tiles0 - 1);
-        if (!__all_sync(0xffffffffu, wait(&sh.v_full[c], 0, a.status))) break;
-        check_values<D, BF16>(ring + ((2 * j + 1) % C::kStages) * C::kTile, j * kRows, &sh);
-        fence_proxy_async_smem();  // the tensor cores read what was written here
-        arrive(&sh.v_checked[c]);
-      }
-    }
+    if (warp == 8) load_role<D>(mq, mk, mv, a, &sh, smem, pair);
+    else if (warp == 9) mma_role<D, BF16>(a, &sh, smem, pair);
+    else if (warp == 10) check_role<D, BF16>(a, &sh, smem + 2 * C::kTile, pair);
+    else order_role(a, &sh, Order(nb, a.seqs, lots), span, pair);
   }
   __syncwarp();
   t5::fence_before();
@@ -420,13 +684,18 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t st) {
   if (e == cudaSuccess) e = encode(&mv, a.v, D, a.kv_heads, a.tokens, a.v_stride, BF16);
   if (e != cudaSuccess) return e;
   static SmemAttr attr;
-  e = attr.ensure(prompt_kernel<D, BF16>, Cfg<D>::kSmem);
+  const size_t smem = Cfg<D>::kSmem + (size_t)a.seqs * 4;
+  e = attr.ensure(prompt_kernel<D, BF16>, Cfg<D>::kSmem + kMaxRequests * 4);
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int pair = (a.q_heads / a.kv_heads) % 2 == 0;
   const int span = pair ? kRows : 2 * kRows;
-  const int64_t grid = (int64_t)(pair ? a.q_heads / 2 : a.q_heads) * (a.tokens / span + a.seqs);
-  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-  prompt_kernel<D, BF16><<<(unsigned)grid, kThreads, Cfg<D>::kSmem, st>>>(mq, mk, mv, a, pair);
+  const int64_t most = (int64_t)(pair ? a.q_heads / 2 : a.q_heads) * (a.tokens / span + a.seqs);  // blocks at most
+  if (most > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
+  prompt_kernel<D, BF16><<<(unsigned)(most < sms ? most : sms), kThreads, smem, st>>>(mq, mk, mv, a, pair);
   return cudaGetLastError();
 }
 

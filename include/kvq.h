@@ -496,7 +496,7 @@ KVQ_API kvq_status kvq_paged_decode_attention(kvq_paged_cache* cache, int32_t la
  * apart (multiples of 8, no less than a row). H_q is a multiple of H_kv.
  * cu_tokens: [num_seqs + 1] int32 on the device, sequence s holds tokens
  * cu_tokens[s] .. cu_tokens[s + 1] - 1 (the array kvq_paged_reserve writes);
- * num_seqs <= 4096. out: [max_tokens][H_q][D] in dtype; rows outside every sequence
+ * num_seqs <= 4096, max_tokens <= 2^26. out: [max_tokens][H_q][D] in dtype; rows outside every sequence
  * are left as they are. A later token does not reach an earlier one's output,
  * not even by an infinity or NaN among its values. status: an optional uint32
  * device word that receives the bits of kvq_paged_cache_status (a range that
