@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kPer = kMaxRequests / kThreads;  // requests per thread
+constexpr int kCluster = 8;
 
 // Exclusive prefix sums of (x, y) over the block; totals in *tx, *ty.
 __device__ __forceinline__ void block_scan2(long long& x, long long& y, long long* tx, long long* ty) {
@@ -212,15 +213,18 @@ cudaError_t launch_reserve(const ReserveArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)(3 * a.requests + 2) * 4;
   const cudaError_t e = attr.ensure(reserve_kernel, (3 * kMaxRequests + 2) * 4);
   if (e != cudaSuccess) return e;
+  if (a.max_tokens <= 2 * kThreads) {
+    reserve_kernel<<<1, kThreads, smem, st>>>(a);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg = {};
-  const int ctas = a.max_tokens > 2 * kThreads ? 8 : 1;
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(kCluster);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = ctas;
+  at.val.clusterDim.x = kCluster;
   at.val.clusterDim.y = 1;
   at.val.clusterDim.z = 1;
   cfg.attrs = &at;

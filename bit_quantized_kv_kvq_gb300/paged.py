@@ -59,9 +59,25 @@ SIGNATURES = {
 StepPlan = namedtuple("StepPlan", "cu_tokens slots positions lens free_count")
 
 
-def _kvq():
-    from . import lib, check, _stream_ptr
-    return lib(), check, _stream_ptr
+_lib = None
+_Tensor, _int32 = torch.Tensor, torch.int32
+_current_stream = torch._C._cuda_getCurrentRawStream
+_capturing = torch.cuda.is_current_stream_capturing
+
+
+def _bind():
+    """The library's entry points and the error check, looked up once: the calls
+    below are made per layer and step, where the host's time counts."""
+    global _lib, _check
+    from . import check, lib
+    _lib, _check = lib(), check
+    return _lib
+
+
+def _raw_stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    return _current_stream(device.index)
 
 
 def _empty(shape, dtype, device, stream):
@@ -74,9 +90,10 @@ def _empty(shape, dtype, device, stream):
 
 
 def _ints(t, name, shape, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device:
+    """Pointer of an int32 tensor of the given shape."""
+    if not isinstance(t, _Tensor) or t.dtype is not _int32 or t.device != device:
         raise TypeError("%s must be an int32 tensor on %s" % (name, device))
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -86,17 +103,16 @@ def _ints(t, name, shape, device):
 def _rows(t, name, dtype, device, heads=None, dim=None):
     """(pointer, token stride) of packed rows [token][head][channel]: the
     tokens may lie apart (a slice of a fused projection), a row may not."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.device != device:
         raise TypeError("%s must be a %s tensor on %s" % (name, dtype, device))
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
-        raise ValueError("%s has shape %s, expected [tokens][%s][%s]" % (name, tuple(t.shape), heads, dim))
-    _, h, d = t.shape
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or (dim is not None and shape[2] != dim):
+        raise ValueError("%s has shape %s, expected [tokens][%s][%s]" % (name, tuple(shape), heads, dim))
+    n, h, d = shape
     st, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError("the rows of %s must be contiguous" % name)
-    if t.shape[0] <= 1:  # its stride is not read
-        st = h * d
-    return t.data_ptr(), st
+    return t.data_ptr(), st if n > 1 else h * d  # of one token the stride is not read
 
 
 class PagedKVCache:
@@ -105,22 +121,25 @@ class PagedKVCache:
 
     def __init__(self, num_layers, max_requests, num_kv_heads, head_dim, page_tokens, num_pages, max_pages,
                  code=PAGE_INT8, dtype=torch.float16, device=None, stream=None):
-        lib, check, stream_ptr = _kvq()
+        lib = _lib or _bind()
         if dtype not in (torch.float16, torch.bfloat16):
             raise TypeError("dtype must be torch.float16 or torch.bfloat16")
         self.cfg = PagedConfig(num_layers, max_requests, num_kv_heads, head_dim, page_tokens, num_pages, max_pages,
                                code, _DTYPES[dtype])
         self.dtype = dtype
         n = ctypes.c_size_t()
-        check(lib.kvq_paged_cache_bytes(ctypes.byref(self.cfg), ctypes.byref(n)))
+        _check(lib.kvq_paged_cache_bytes(ctypes.byref(self.cfg), ctypes.byref(n)))
         self.nbytes = n.value
         self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device if device is not None else "cuda")
         self.device = self.buffer.device
         h = _P()
-        check(lib.kvq_paged_cache_create(ctypes.byref(self.cfg), self.buffer.data_ptr(), self.nbytes,
-                                         stream_ptr(stream), ctypes.byref(h)))
+        _check(lib.kvq_paged_cache_create(ctypes.byref(self.cfg), self.buffer.data_ptr(), self.nbytes,
+                                          _raw_stream(stream, self.device), ctypes.byref(h)))
         self.handle = h
-        self._ws = {}
+        self._ws_bytes, self._ws = {}, {}
+        self._views = {}
+        self._table_pages, self._all_pages = max_pages, num_pages
+        self._heads, self._dim = num_kv_heads, head_dim
 
     # -- hot path -----------------------------------------------------------
     def reserve(self, lens, new_tokens, table, free_pages, free_count, max_tokens, lens_out=None,
@@ -129,119 +148,142 @@ class PagedKVCache:
         rest as a StepPlan. ``plan``: an earlier step's StepPlan whose tensors
         are written again (for captured steps); lens_out / free_count_out may
         be ``lens`` / ``free_count``."""
-        lib, check, stream_ptr = _kvq()
-        c, dev = self.cfg, self.device
+        lib = _lib or _bind()
+        dev = self.device
         r = lens.shape[0]
+        table_p = _ints(table, "table", (r, self._table_pages), dev)
         if plan is None:
-            # one allocation, cut up
-            cu, slots, positions, lo, fo = _empty(2 * r + 2 + 2 * max_tokens, torch.int32, dev, stream).split(
-                [r + 1, max_tokens, max_tokens, r, 1])
-            plan = StepPlan(cu, slots, positions, lens_out if lens_out is not None else lo,
-                            free_count_out if free_count_out is not None else fo)
+            # one allocation, cut up; what is cut here needs no check
+            t = max_tokens
+            if t < 0:
+                raise ValueError("max_tokens must be >= 0")
+            buf = _empty(2 * r + 2 + 2 * t, _int32, dev, stream)
+            cu, slots, positions, lo, fo = buf.split_with_sizes([r + 1, t, t, r, 1])
+            cu_p = buf.data_ptr()
+            slots_p = cu_p + 4 * (r + 1)
+            positions_p = slots_p + 4 * t
+            lo_p = positions_p + 4 * t
+            fo_p = lo_p + 4 * r
+            if lens_out is not None:
+                lo, lo_p = lens_out, _ints(lens_out, "lens_out", (r,), dev)
+            if free_count_out is not None:
+                fo, fo_p = free_count_out, _ints(free_count_out, "free_count_out", (1,), dev)
+            plan = StepPlan(cu, slots, positions, lo, fo)
         elif lens_out is not None or free_count_out is not None:
             raise ValueError("plan already names the outputs")
-        check(lib.kvq_paged_reserve(
-            self.handle, r, _ints(lens, "lens", (r,), dev), _ints(new_tokens, "new_tokens", (r,), dev),
-            _ints(table, "table", (r, c.max_pages), dev), _ints(free_pages, "free_pages", (c.num_pages,), dev),
-            _ints(free_count, "free_count", (1,), dev), max_tokens, _ints(plan.cu_tokens, "cu_tokens", (r + 1,), dev),
-            _ints(plan.slots, "slots", (max_tokens,), dev), _ints(plan.positions, "positions", (max_tokens,), dev),
-            _ints(plan.lens, "lens_out", (r,), dev), _ints(plan.free_count, "free_count_out", (1,), dev),
-            stream_ptr(stream)))
+        else:
+            cu_p = _ints(plan.cu_tokens, "cu_tokens", (r + 1,), dev)
+            slots_p = _ints(plan.slots, "slots", (max_tokens,), dev)
+            positions_p = _ints(plan.positions, "positions", (max_tokens,), dev)
+            lo_p = _ints(plan.lens, "lens_out", (r,), dev)
+            fo_p = _ints(plan.free_count, "free_count_out", (1,), dev)
+        _check(lib.kvq_paged_reserve(
+            self.handle, r, _ints(lens, "lens", (r,), dev), _ints(new_tokens, "new_tokens", (r,), dev), table_p,
+            _ints(free_pages, "free_pages", (self._all_pages,), dev), _ints(free_count, "free_count", (1,), dev),
+            max_tokens, cu_p, slots_p, positions_p, lo_p, fo_p, _raw_stream(stream, dev)))
         return plan
 
     def release(self, done, lens, table, free_pages, free_count, stream=None):
         """Ends the requests with done != 0 (kvq_paged_release), in place."""
-        lib, check, stream_ptr = _kvq()
-        c, dev = self.cfg, self.device
+        lib = _lib or _bind()
+        dev = self.device
         r = lens.shape[0]
-        check(lib.kvq_paged_release(
+        _check(lib.kvq_paged_release(
             self.handle, r, _ints(done, "done", (r,), dev), _ints(lens, "lens", (r,), dev),
-            _ints(table, "table", (r, c.max_pages), dev), _ints(free_pages, "free_pages", (c.num_pages,), dev),
-            _ints(free_count, "free_count", (1,), dev), stream_ptr(stream)))
+            _ints(table, "table", (r, self._table_pages), dev), _ints(free_pages, "free_pages", (self._all_pages,), dev),
+            _ints(free_count, "free_count", (1,), dev), _raw_stream(stream, dev)))
 
     def write(self, layer, k, v, cu_tokens, slots, lens, stream=None):
         """Writes the step's packed tokens (kvq_paged_write). ``lens``: the
         lengths after the step."""
-        lib, check, stream_ptr = _kvq()
-        c, dev = self.cfg, self.device
+        lib = _lib or _bind()
+        dev = self.device
         r = lens.shape[0]
-        kp, ks = _rows(k, "k", self.dtype, dev, c.num_kv_heads, c.head_dim)
-        vp, vs = _rows(v, "v", self.dtype, dev, c.num_kv_heads, c.head_dim)
+        kp, ks = _rows(k, "k", self.dtype, dev, self._heads, self._dim)
+        vp, vs = _rows(v, "v", self.dtype, dev, self._heads, self._dim)
         t = k.shape[0]
         if v.shape[0] != t:
             raise ValueError("k and v hold %d and %d tokens" % (t, v.shape[0]))
-        check(lib.kvq_paged_write(self.handle, layer, r, kp, vp, ks, vs, t,
+        _check(lib.kvq_paged_write(self.handle, layer, r, kp, vp, ks, vs, t,
                                   _ints(cu_tokens, "cu_tokens", (r + 1,), dev), _ints(slots, "slots", (t,), dev),
-                                  _ints(lens, "lens", (r,), dev), stream_ptr(stream)))
+                                  _ints(lens, "lens", (r,), dev), _raw_stream(stream, dev)))
 
     def workspace_bytes(self, num_q_heads):
-        lib, check, _ = _kvq()
-        n = ctypes.c_size_t()
-        check(lib.kvq_paged_decode_workspace_bytes(self.handle, num_q_heads, ctypes.byref(n)))
-        return n.value
+        n = self._ws_bytes.get(num_q_heads)
+        if n is None:
+            size = ctypes.c_size_t()
+            _check(_lib.kvq_paged_decode_workspace_bytes(self.handle, num_q_heads, ctypes.byref(size)))
+            n = self._ws_bytes[num_q_heads] = size.value
+        return n
 
-    def workspace(self, num_q_heads):
-        """The cache's own workspace for decode(): calls that overlap on the
-        GPU need one each (``workspace=``)."""
-        ws = self._ws.get(num_q_heads)
+    def _workspace(self, hq, raw, stream):
+        if _capturing():
+            return _empty(self.workspace_bytes(hq), torch.uint8, self.device, stream)
+        ws = self._ws.get((hq, raw))
         if ws is None:
-            ws = torch.empty(self.workspace_bytes(num_q_heads), dtype=torch.uint8, device=self.device)
-            self._ws[num_q_heads] = ws
+            ws = self._ws[hq, raw] = _empty(self.workspace_bytes(hq), torch.uint8, self.device, stream)
         return ws
 
     def decode(self, layer, q, table, lens, softmax_scale, out=None, out_dtype=None, workspace=None, stream=None):
         """Attention of one query token per request (kvq_paged_decode_attention):
-        q [requests][H_q][D] -> out [requests][H_q][D], zeros where lens is 0."""
-        lib, check, stream_ptr = _kvq()
-        c, dev = self.cfg, self.device
-        qp, qs = _rows(q, "q", self.dtype, dev, dim=c.head_dim)
+        q [requests][H_q][D] -> out [requests][H_q][D], zeros where lens is 0.
+        Without ``workspace`` the cache keeps one for each stream, and a captured
+        call takes one of its own: neither streams nor graphs share it."""
+        lib = _lib or _bind()
+        dev = self.device
+        qp, qs = _rows(q, "q", self.dtype, dev, dim=self._dim)
         r, hq, d = q.shape
         if out is None:
             out = _empty((r, hq, d), out_dtype or self.dtype, dev, stream)
         elif tuple(out.shape) != (r, hq, d) or out.device != dev or not out.is_contiguous() or out.dtype not in _DTYPES:
             raise ValueError("out must be a contiguous tensor of shape %s on %s" % ((r, hq, d), dev))
-        ws = self.workspace(hq) if workspace is None else workspace
-        check(lib.kvq_paged_decode_attention(
-            self.handle, layer, r, qp, qs, hq, _ints(table, "table", (r, c.max_pages), dev),
-            _ints(lens, "lens", (r,), dev), softmax_scale, out.data_ptr(), _DTYPES[out.dtype], ws.data_ptr(),
-            ws.numel() * ws.element_size(), stream_ptr(stream)))
+        raw = _raw_stream(stream, dev)
+        ws = self._workspace(hq, raw, stream) if workspace is None else workspace
+        _check(lib.kvq_paged_decode_attention(
+            self.handle, layer, r, qp, qs, hq, _ints(table, "table", (r, self._table_pages), dev),
+            _ints(lens, "lens", (r,), dev), softmax_scale, out.data_ptr(), _DTYPES[out.dtype], ws.data_ptr(), ws.nbytes,
+            raw))
         return out
 
     # -- inspection ---------------------------------------------------------
-    def _view(self, layer, name, shape, dtype):
-        lib, check, _ = _kvq()
-        lo = PagedLayout()
-        check(lib.kvq_paged_cache_get_layout(self.handle, layer, ctypes.byref(lo)))
-        off = getattr(lo, name) - self.buffer.data_ptr()
-        return self.buffer[off:off + getattr(lo, name + "_bytes")].view(dtype).view(shape)
+    def _view(self, layer, name):
+        view = self._views.get((layer, name))
+        if view is None:
+            c, lo = self.cfg, PagedLayout()
+            _check(_lib.kvq_paged_cache_get_layout(self.handle, layer, ctypes.byref(lo)))
+            shape, dtype = {
+                "pages": ((c.num_pages, c.num_kv_heads, 2, c.page_tokens, c.head_dim),
+                          torch.int8 if c.code == PAGE_INT8 else torch.uint8),
+                "scales": ((c.num_pages, c.num_kv_heads, 2), torch.float32),
+                "tails": ((c.max_requests, c.num_kv_heads, 2, c.page_tokens, c.head_dim), self.dtype)}[name]
+            off = getattr(lo, name) - self.buffer.data_ptr()
+            view = self.buffer[off:off + getattr(lo, name + "_bytes")].view(dtype).view(shape)
+            self._views[layer, name] = view
+        return view
 
     def pages(self, layer):
         """Codes [page][kv head][K, V][token][channel]: int8, or uint8 bits of
         torch.float8_e4m3fn."""
-        c = self.cfg
-        return self._view(layer, "pages", (c.num_pages, c.num_kv_heads, 2, c.page_tokens, c.head_dim),
-                          torch.int8 if c.code == PAGE_INT8 else torch.uint8)
+        return self._view(layer, "pages")
 
     def scales(self, layer):
         """fp32 [page][kv head][K, V]."""
-        c = self.cfg
-        return self._view(layer, "scales", (c.num_pages, c.num_kv_heads, 2), torch.float32)
+        return self._view(layer, "scales")
 
     def tails(self, layer):
         """Rows of the open pages [request][kv head][K, V][token][channel]."""
-        c = self.cfg
-        return self._view(layer, "tails", (c.max_requests, c.num_kv_heads, 2, c.page_tokens, c.head_dim), self.dtype)
+        return self._view(layer, "tails")
 
     def status(self, stream=None):
         """Synchronizes and clears the status word; raises KVQError if it was set."""
-        lib, check, stream_ptr = _kvq()
+        lib = _lib or _bind()
         w = ctypes.c_uint32()
-        check(lib.kvq_paged_cache_status(self.handle, stream_ptr(stream), ctypes.byref(w)))
+        _check(lib.kvq_paged_cache_status(self.handle, _raw_stream(stream, self.device), ctypes.byref(w)))
         return w.value
 
     def close(self):
         if getattr(self, "handle", None):
-            _kvq()[0].kvq_paged_cache_destroy(self.handle)
+            _lib.kvq_paged_cache_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
@@ -256,7 +298,7 @@ def prompt_attention(q, k, v, cu_tokens, softmax_scale, out=None, status=None, s
     [tokens][H_q][D], k and v [tokens][H_kv][D] in fp16 or bf16, cu_tokens
     int32 [sequences + 1]. Rows of ``out`` outside every sequence are left as
     they are (uninitialised where ``out`` is not given)."""
-    lib, check, stream_ptr = _kvq()
+    lib = _lib or _bind()
     if not isinstance(q, torch.Tensor) or q.dtype not in (torch.float16, torch.bfloat16) or not q.is_cuda:
         raise TypeError("q must be a CUDA float16 or bfloat16 tensor")
     dev = q.device
@@ -271,8 +313,8 @@ def prompt_attention(q, k, v, cu_tokens, softmax_scale, out=None, status=None, s
     elif tuple(out.shape) != (t, hq, d) or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
         raise ValueError("out must be a contiguous %s tensor of shape %s on %s" % (q.dtype, (t, hq, d), dev))
     seqs = cu_tokens.shape[0] - 1
-    check(lib.kvq_prompt_attention(
+    _check(lib.kvq_prompt_attention(
         qp, kp, vp, qs, ks, vs, t, seqs, _ints(cu_tokens, "cu_tokens", (seqs + 1,), dev), hq, k.shape[1], d,
         _DTYPES[q.dtype], softmax_scale, out.data_ptr(),
-        None if status is None else _ints(status, "status", (1,), dev), stream_ptr(stream)))
+        None if status is None else _ints(status, "status", (1,), dev), _raw_stream(stream, dev)))
     return out
