@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
 
   const int at0 = rank * kThreads + threadIdx.x, stride = ranks * kThreads;
   if (!fits) {
-    for (int i = at0; i < a.max_tokens; i += stride) a.slots[i] = -1, a.positions[i] = -1;
+    for (int64_t i = at0; i < a.max_tokens; i += stride) a.slots[i] = -1, a.positions[i] = -1;
     if (rank == 0) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
@@ -140,19 +140,35 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
     if (page < 0 || page >= a.num_pages) raise_status(a.status, kStatusBadIndex);
     a.table[(int64_t)b * a.max_pages + j] = page;
   }
-  for (int i = at0; i < a.max_tokens; i += stride) {
-    int slot = -1, pos = -1;
-    if (i < (int)total) {
-      const int b = last_le(cu, R + 1, i);
-      pos = old[b] + (i - cu[b]);
-      const int j = pos >> a.page_shift, have = (old[b] + P - 1) >> a.page_shift;
-      const int page = j < have ? a.table[(int64_t)b * a.max_pages + j]
-                                : a.free_pages[free_count - 1 - (first[b] + j - have)];
-      if (page >= 0 && page < a.num_pages) slot = (page << a.page_shift) + (pos & (P - 1));
+  // four packed tokens a step: one search, then on from request to request
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
+  for (int64_t at = 4 * at0; at < a.max_tokens; at += 4 * stride) {
+    const int i0 = (int)at;
+    int slot[4], pos[4];
+    int b = i0 < (int)total ? last_le(cu, R + 1, i0) : R;
+    int page = 0, page_index = -1;  // of request b, the last one looked up
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      slot[k] = pos[k] = -1;
+      if (at + k >= total) continue;
+      const int i = i0 + k;
+      while (cu[b + 1] <= i) ++b, page_index = -1;
+      const int p = old[b] + (i - cu[b]), j = p >> a.page_shift;
+      if (j != page_index) {
+        const int have = (old[b] + P - 1) >> a.page_shift;
+        page = j < have ? a.table[(int64_t)b * a.max_pages + j] : a.free_pages[free_count - 1 - (first[b] + j - have)];
+        page_index = j;
+      }
+      pos[k] = p;
+      if (page >= 0 && page < a.num_pages) slot[k] = (page << a.page_shift) + (p & (P - 1));
       else raise_status(a.status, kStatusBadIndex);
     }
-    a.slots[i] = slot;
-    a.positions[i] = pos;
+    if (vec && at + 4 <= a.max_tokens) {
+      *reinterpret_cast<int4*>(a.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+      for (int k = 0; k < 4 && at + k < a.max_tokens; ++k) a.slots[i0 + k] = slot[k], a.positions[i0 + k] = pos[k];
+    }
   }
 }
 

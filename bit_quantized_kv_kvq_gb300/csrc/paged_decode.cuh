@@ -13,11 +13,11 @@
 // channels may be summed in any order, so a lane loads 16 contiguous bytes
 // and calls them the fragment's slots.
 //
-// The tiles (64 tokens of one request and kv-head) of all requests form one
+// The tiles (64 or 128 tokens of one request and kv-head) of all requests form one
 // line that is cut into equal ranges, one per CTA: the kernel makes the line
 // from the device lengths itself, so the grid needs no host knowledge and
 // ragged batches stay even. A CTA's four warps take 16 tokens of a tile each
-// and keep their own running maximum and sums. A (request, head) that one CTA
+// (32 with 64 channels: as many bytes in flight) and keep their own running maximum and sums. A (request, head) that one CTA
 // covers is finished there; the others leave partial sums, which a second
 // kernel merges in the order of the CTAs.
 #pragma once
@@ -29,8 +29,11 @@ namespace pdec {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kUnit = 64;  // tokens of a tile
 constexpr unsigned kFull = 0xffffffffu;
+
+// Groups of 16 tokens that a warp takes of a tile, and the tile's tokens.
+__host__ __device__ constexpr int sub_of(int dim) { return 128 / dim; }
+__host__ __device__ constexpr int unit_of(int dim) { return kWarps * 16 * sub_of(dim); }
 
 // Heads of one pass over the codes: 8 NT (NT column tiles of the products).
 __host__ __device__ constexpr int nt_of(int group) { return group <= 8 ? 1 : 2; }
@@ -373,6 +376,7 @@ struct TilePtr {
 template <int D, int CODE, bool BF16, int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) paged_decode_kernel(const Params prm) {
   using W = Warp<D, CODE, BF16, NT>;
+  constexpr int kSub = sub_of(D), kUnit = unit_of(D);
   const PagedDev& c = prm.c;
   const PagedDecodeArgs& a = prm.a;
   extern __shared__ int prefix[];  // [requests + 1]
@@ -448,11 +452,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) paged_decode_kernel
     w.begin(a.q + b * a.q_stride + (int64_t)head0 * D, heads, a.scale_log2);
     const int32_t* row = a.table + (int64_t)b * c.max_pages;
 
-    auto page_of = [&](int tok) { return row[tok >> c.page_shift]; };
-    auto tile_of = [&](int page, int tok) {
+    auto tile_of = [&](int page, int tok, bool live) {
       TilePtr p;
       const bool ok = page >= 0 && page < c.num_pages;
-      if (!ok && lane == 0) raise_status(c.status, kStatusBadIndex);
+      if (!ok && live && lane == 0) raise_status(c.status, kStatusBadIndex);
       const int64_t ph = ((int64_t)(ok ? page : 0) * c.heads + h) * 2;
       p.k = c.pages + (ph << c.page_shift) * D + (tok & (P - 1)) * D;
       const float2 s = *reinterpret_cast<const float2*>(c.scales + ph);
@@ -461,46 +464,57 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) paged_decode_kernel
       if (!ok) p.k = nullptr;
       return p;
     };
-    int tok = t0 * kUnit + warp * 16;
-    const int end = t1 * kUnit;
-    const int page_end = min(end, full);
+    const int end = t1 * kUnit, page_end = min(end, full);
+    int tok = t0 * kUnit + warp * 16 * kSub;
     if (tok < page_end) {
-      uint4 kr[2][W::kChunks];
-      uint32_t vr[4][W::kVw];
-      TilePtr p = tile_of(page_of(tok), tok);
-      const uint8_t* base = p.k ? p.k : c.pages;
-      w.load_k(base, kr);
-      w.load_v(base + (size_t)P * D, vr);
-      int next_page = tok + kUnit < page_end ? page_of(tok + kUnit) : 0;
+      uint4 kr[kSub][2][W::kChunks];
+      uint32_t vr[kSub][4][W::kVw];
+      TilePtr p[kSub];
+      int next[kSub];
+      // a group past the complete pages, or of a page out of range, takes no part
+      auto page_at = [&](int tk) { return tk < page_end ? row[tk >> c.page_shift] : -1; };
+      auto base_of = [&](const TilePtr& q) { return q.k ? q.k : c.pages; };
+#pragma unroll
+      for (int i = 0; i < kSub; ++i) {
+        p[i] = tile_of(page_at(tok + 16 * i), tok + 16 * i, tok + 16 * i < page_end);
+        w.load_k(base_of(p[i]), kr[i]);
+        w.load_v(base_of(p[i]) + (size_t)P * D, vr[i]);
+        next[i] = page_at(tok + kUnit + 16 * i);
+      }
       for (;;) {
-        const int nt_tok = tok + kUnit;
-        const bool more = nt_tok < page_end;
-        const int after = nt_tok + kUnit < page_end ? page_of(nt_tok + kUnit) : 0;
-        TilePtr pn = p;
-        float s[NT][4];
-        w.scores(kr, s);
-        if (more) {
-          pn = tile_of(next_page, nt_tok);
-          w.load_k(pn.k ? pn.k : c.pages, kr);
-        }
-        uint32_t pb[NT][2];
-        const bool ok = p.k != nullptr;  // a page out of range takes no part
-        if (ok) {
-          w.weights(s, p.ks, p.ks, true, true, pb);
-          w.values(vr, p.vs, pb);
+        const int then = tok + kUnit;
+        const bool more = then < page_end;
+        TilePtr pn[kSub];
+        int after[kSub];
+#pragma unroll
+        for (int i = 0; i < kSub; ++i) after[i] = page_at(then + kUnit + 16 * i);
+#pragma unroll
+        for (int i = 0; i < kSub; ++i) {
+          float s[NT][4];
+          w.scores(kr[i], s);
+          pn[i] = p[i];
+          if (more) {
+            pn[i] = tile_of(next[i], then + 16 * i, then + 16 * i < page_end);
+            w.load_k(base_of(pn[i]), kr[i]);
+          }
+          if (p[i].k) {
+            uint32_t pb[NT][2];
+            w.weights(s, p[i].ks, p[i].ks, true, true, pb);
+            w.values(vr[i], p[i].vs, pb);
+          }
+          if (more) w.load_v(base_of(pn[i]) + (size_t)P * D, vr[i]);
         }
         if (!more) break;
-        w.load_v((pn.k ? pn.k : c.pages) + (size_t)P * D, vr);
-        p = pn;
-        tok = nt_tok;
-        next_page = after;
+        tok = then;
+#pragma unroll
+        for (int i = 0; i < kSub; ++i) p[i] = pn[i], next[i] = after[i];
       }
-      tok += kUnit;
     }
     const int tail_end = min(end, len);
-    for (; tok < tail_end; tok += kUnit) {
-      const uint16_t* kt = c.tails + ((((int64_t)b * c.heads + h) * 2) << c.page_shift) * D + (tok - full) * D;
-      w.tail_rows(kt, kt + (int64_t)P * D, min(16, len - tok));
+    for (int tk = max(full, t0 * kUnit); tk < tail_end; tk += 16) {
+      if (tk % kUnit / (16 * kSub) != warp) continue;
+      const uint16_t* kt = c.tails + ((((int64_t)b * c.heads + h) * 2) << c.page_shift) * D + (tk - full) * D;
+      w.tail_rows(kt, kt + (int64_t)P * D, min(16, len - tk));
     }
 
     // the four warps' sums
@@ -570,17 +584,30 @@ __global__ void __launch_bounds__(D) paged_merge_kernel(const Params prm) {
     const int ctas = units < prm.ctas ? (int)units : prm.ctas;
     const int c0 = (int)(((first + 1) * ctas - 1) / units), c1 = (int)(((last + 1) * ctas - 1) / units);
     if (c0 == c1) return;  // finished by that CTA
+    const int64_t step = (int64_t)2 * prm.passes * 8 * NT * (D + 2);
+    const float* part = prm.part + (int64_t)c0 * step + ((int64_t)pass * 8 * NT + hd) * (D + 2);
+    const int64_t second = step / 2;  // the row of a range's end; c0's is its start's
     float top = -INFINITY, o = 0.0f, l = 0.0f;
-    for (int c = c0; c <= c1; ++c) {
-      const float* part =
-          prm.part + ((((int64_t)c * 2 + (c > c0 ? 0 : 1)) * prm.passes + pass) * 8 * NT + hd) * (D + 2);
-      const float pm = part[D], pl = part[D + 1], po = part[ch];
-      const float now = fmaxf(top, pm);
-      const float ref = now == -INFINITY ? 0.0f : now;
-      const float fo = exp2_fast(top - ref), fn = exp2_fast(pm - ref);
-      o = o * fo + po * fn;
-      l = l * fo + pl * fn;
-      top = now;
+    constexpr int kBatch = 8;  // partial rows in flight
+    for (int k0 = 0; k0 <= c1 - c0; k0 += kBatch) {
+      float pm[kBatch], pl[kBatch], po[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const bool live = k0 + k <= c1 - c0;
+        const float* row = part + (live ? k0 + k : 0) * step + (k0 + k == 0 || !live ? second : 0);
+        pm[k] = live ? row[D] : -INFINITY;
+        pl[k] = live ? row[D + 1] : 0.0f;
+        po[k] = live ? row[ch] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float now = fmaxf(top, pm[k]);
+        const float ref = now == -INFINITY ? 0.0f : now;
+        const float fo = exp2_fast(top - ref), fn = exp2_fast(pm[k] - ref);
+        o = o * fo + po[k] * fn;
+        l = l * fo + pl[k] * fn;
+        top = now;
+      }
     }
     r = o / l;
   }

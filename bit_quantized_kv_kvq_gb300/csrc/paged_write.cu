@@ -19,21 +19,47 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// Four codes of x / s, packed. The quotient is the IEEE one, so that a code
-// never depends on how a compiler would approximate it.
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four codes of x / s, packed, by the IEEE quotient.
 template <int CODE>
-__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, float s) {
+__device__ __forceinline__ uint32_t code4(const float* x, float s) {
   if (s == 0.0f) return 0u;
-  a = __fdiv_rn(a, s), b = __fdiv_rn(b, s), c = __fdiv_rn(c, s), d = __fdiv_rn(d, s);
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = __fdiv_rn(x[i], s);
+  if (CODE == KVQ_PAGE_E4M3) return e4m3_pair(y[0], y[1]) | (e4m3_pair(y[2], y[3]) << 16);
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r |= (uint32_t)(max(-127, min(127, __float2int_rn(y[i]))) & 255) << (8 * i);
+  return r;
+}
+
+// The same codes without a division: lo and hi are 1 / s less and more 2^-21
+// of it, so the quotient, rounded however it may be, lies between x lo and
+// x hi (1 / s and the product are within 2^-23). Rounding is monotone: where
+// the codes of both ends are the same one it is the quotient's; `differ`
+// collects where they are not (about one value in 10^5), and those take code4.
+template <int CODE>
+__device__ __forceinline__ uint32_t code4_fast(const float* x, float lo, float hi, uint32_t& differ) {
   if (CODE == KVQ_PAGE_E4M3) {
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-    return (uint32_t)lo | ((uint32_t)hi << 16);
+    const uint32_t a = e4m3_pair(x[0] * lo, x[1] * lo) | (e4m3_pair(x[2] * lo, x[3] * lo) << 16);
+    const uint32_t b = e4m3_pair(x[0] * hi, x[1] * hi) | (e4m3_pair(x[2] * hi, x[3] * hi) << 16);
+    differ |= a ^ b;
+    return a;
   }
-  const int ia = max(-127, min(127, __float2int_rn(a))), ib = max(-127, min(127, __float2int_rn(b)));
-  const int ic = max(-127, min(127, __float2int_rn(c))), id = max(-127, min(127, __float2int_rn(d)));
-  return (uint32_t)(ia & 255) | ((uint32_t)(ib & 255) << 8) | ((uint32_t)(ic & 255) << 16) | ((uint32_t)(id & 255) << 24);
+  constexpr float kInt = 12582912.0f;  // 1.5 * 2^23: the sum's last bit is 1, its low byte the rounded integer
+  uint32_t a[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = __float_as_uint(__fmaf_rn(x[i], lo, kInt));
+    differ |= a[i] ^ __float_as_uint(__fmaf_rn(x[i], hi, kInt));
+  }
+  return __byte_perm(__byte_perm(a[0], a[1], 0x0040), __byte_perm(a[2], a[3], 0x0040), 0x5410);
 }
 
 // P tokens, D channels. A granule is 16 channels of a row (32 bytes in, 16
@@ -107,15 +133,28 @@ __global__ void __launch_bounds__(WriteCfg<P, D, CODE, BF16>::kThreads)
     } else {
       const int64_t ph = ((int64_t)page * c.heads + h) * 2 + half;
       uint8_t* dst = c.pages + ph * (P * D);
+      // page-uniform: 1 / s and its products stay normal numbers
+      const bool fast = s > 0x1p-100f && s < 0x1p100f;
+      const float r = __frcp_rn(fast ? s : 1.0f), lo = r * (1.0f - 0x1p-21f), hi = r * (1.0f + 0x1p-21f);
 #pragma unroll
       for (int i = 0; i < Cfg::kGran; ++i) {
-        uint32_t o[4];
+        uint32_t o[4], differ = fast ? 0u : 1u;
+        float f[16];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const uint4 u = x[i][q];
-          const float2 f0 = unpack2<BF16>(u.x), f1 = unpack2<BF16>(u.y), f2 = unpack2<BF16>(u.z), f3 = unpack2<BF16>(u.w);
-          o[2 * q] = code4<CODE>(f0.x, f0.y, f1.x, f1.y, s);
-          o[2 * q + 1] = code4<CODE>(f2.x, f2.y, f3.x, f3.y, s);
+          const uint32_t u[4] = {x[i][q].x, x[i][q].y, x[i][q].z, x[i][q].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = unpack2<BF16>(u[k]);
+            f[8 * q + 2 * k] = v.x;
+            f[8 * q + 2 * k + 1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = code4_fast<CODE>(f + 4 * q, lo, hi, differ);
+        if (differ) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[q] = code4<CODE>(f + 4 * q, s);
         }
         *reinterpret_cast<uint4*>(dst + (i * Cfg::kHalf + tid) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
       }

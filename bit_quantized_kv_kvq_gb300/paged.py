@@ -158,11 +158,11 @@ class PagedKVCache:
             if t < 0:
                 raise ValueError("max_tokens must be >= 0")
             buf = _empty(2 * r + 2 + 2 * t, _int32, dev, stream)
-            cu, slots, positions, lo, fo = buf.split_with_sizes([r + 1, t, t, r, 1])
-            cu_p = buf.data_ptr()
-            slots_p = cu_p + 4 * (r + 1)
+            slots, positions, cu, lo, fo = buf.split_with_sizes([t, t, r + 1, r, 1])
+            slots_p = buf.data_ptr()
             positions_p = slots_p + 4 * t
-            lo_p = positions_p + 4 * t
+            cu_p = positions_p + 4 * t
+            lo_p = cu_p + 4 * (r + 1)
             fo_p = lo_p + 4 * r
             if lens_out is not None:
                 lo, lo_p = lens_out, _ints(lens_out, "lens_out", (r,), dev)

@@ -390,7 +390,7 @@ typedef struct kvq_paged_config {
   int32_t page_tokens;   /* 16, 32, 64 or 128                                      */
   int32_t num_pages;     /* pages per layer, >= 1; num_pages * page_tokens < 2^31  */
   int32_t max_pages;     /* row length of a block table, >= 1;
-                            max_pages * page_tokens < 2^31                         */
+                            max_pages * page_tokens <= 2^31 - 256                  */
   int32_t code;          /* kvq_page_code                                          */
   int32_t dtype;         /* of K, V, Q: KVQ_F16 or KVQ_BF16                        */
 } kvq_paged_config;

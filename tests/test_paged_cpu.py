@@ -41,9 +41,9 @@ def test_bytes_are_the_pages_scales_and_tails(lib, page, dim):
 
 BAD = [(dict(num_layers=0), 1), (dict(max_requests=0), 1), (dict(max_requests=4097), 1), (dict(num_kv_heads=0), 1),
        (dict(head_dim=96), 2), (dict(page_tokens=48), 2), (dict(page_tokens=256), 2), (dict(num_pages=0), 1),
-       (dict(num_pages=1 << 25), 1), (dict(max_pages=0), 1), (dict(max_pages=1 << 25), 1), (dict(code=2), 1),
+       (dict(num_pages=1 << 25), 1), (dict(max_pages=0), 1), (dict(max_pages=1 << 25), 1), (dict(max_pages=(1 << 25) - 1), 1), (dict(code=2), 1),
        (dict(dtype=0), 1), (dict(dtype=3), 1),
-       (dict(max_requests=4096, max_pages=(1 << 25) - 1), 2)]
+       (dict(max_requests=4096, max_pages=1 << 24), 2)]
 
 
 @pytest.mark.parametrize("kw,status", BAD, ids=[str(b[0]) for b in BAD])
