@@ -266,7 +266,8 @@ kvq_status kvq_paged_reserve(kvq_paged_cache* h, int32_t requests, const int32_t
   a.lens_out = lens_out;
   a.free_count_out = free_count_out;
   a.status = reinterpret_cast<uint32_t*>(h->base);
-  return done(kvq::launch_reserve(a, static_cast<cudaStream_t>(stream)), 1, "reserve launch");
+  return done(kvq::launch_reserve(a, static_cast<cudaStream_t>(stream)), kvq::reserve_launches(max_tokens),
+              "reserve launch");
 }
 
 kvq_status kvq_paged_release(kvq_paged_cache* h, int32_t requests, const int32_t* done_flags, int32_t* lens,

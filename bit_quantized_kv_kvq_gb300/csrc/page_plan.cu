@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kPer = kMaxRequests / kThreads;  // requests per thread
-constexpr int kCluster = 8;
+constexpr int kOneLaunch = 4096;  // packed tokens that one CTA plans alone
 
 // Exclusive prefix sums of (x, y) over the block; totals in *tx, *ty.
 __device__ __forceinline__ void block_scan2(long long& x, long long& y, long long* tx, long long* ty) {
@@ -55,10 +55,15 @@ __device__ __forceinline__ int last_le(const int* key, int n, int x) {
   return lo;
 }
 
-// One cluster. Every CTA makes the sums for itself (a few thousand lengths)
-// and takes its share of the tokens and pages; the cluster barrier between
-// reading the lengths and writing the state lets lens_out and free_count_out
-// be the input arrays.
+// What a reserve kernel does: the new table entries, slots and positions
+// (kPlan), the state after the step (kState), or both. Every CTA makes the
+// sums for itself (a few thousand lengths at most) and takes its share of the
+// tokens and pages. lens_out and free_count_out may be the input arrays: one
+// CTA writes them once it has read those; with several, a second launch does,
+// after all of the first have.
+constexpr int kPlan = 1, kState = 2;
+
+template <int WHAT>
 __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) {
   extern __shared__ int sm[];
   const int R = a.requests;
@@ -66,9 +71,6 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
   int* first = sm + R + 1;     // [R + 1] pages taken before the request's
   int* old = sm + 2 * (R + 1); // [R] length before
   __shared__ int bad_s;
-  uint32_t rank, ranks;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
   const int P = 1 << a.page_shift;
   if (threadIdx.x == 0) bad_s = 0;
   __syncthreads();
@@ -107,12 +109,13 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
     }
   }
   __syncthreads();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (WHAT == kPlan) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (WHAT == kState) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  const int at0 = rank * kThreads + threadIdx.x, stride = ranks * kThreads;
+  const int at0 = blockIdx.x * kThreads + threadIdx.x, stride = gridDim.x * kThreads;
   if (!fits) {
-    for (int64_t i = at0; i < a.max_tokens; i += stride) a.slots[i] = -1, a.positions[i] = -1;
-    if (rank == 0) {
+    for (int64_t i = at0; (WHAT & kPlan) && i < a.max_tokens; i += stride) a.slots[i] = -1, a.positions[i] = -1;
+    if (WHAT & kState) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int b = threadIdx.x * kPer + i;
@@ -126,13 +129,14 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
     }
     return;
   }
-  if (rank == 0) {
+  if (WHAT & kState) {
     for (int b = threadIdx.x; b <= R; b += kThreads) {
       a.cu[b] = cu[b];
       if (b < R) a.lens_out[b] = old[b] + (cu[b + 1] - cu[b]);
     }
     if (threadIdx.x == 0) *a.free_count_out = free_count - (int)pages;
   }
+  if (!(WHAT & kPlan)) return;
   for (int k = at0; k < (int)pages; k += stride) {
     const int b = last_le(first, R + 1, k);
     const int j = ((old[b] + P - 1) >> a.page_shift) + (k - first[b]);
@@ -224,28 +228,35 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseArgs a) 
 
 }  // namespace
 
+int reserve_launches(int max_tokens) { return max_tokens <= kOneLaunch ? 1 : 2; }
+
 cudaError_t launch_reserve(const ReserveArgs& a, cudaStream_t st) {
-  static SmemAttr attr;
-  const size_t smem = (size_t)(3 * a.requests + 2) * 4;
-  const cudaError_t e = attr.ensure(reserve_kernel, (3 * kMaxRequests + 2) * 4);
-  if (e != cudaSuccess) return e;
-  if (a.max_tokens <= 2 * kThreads) {
-    reserve_kernel<<<1, kThreads, smem, st>>>(a);
+  static SmemAttr one, plan, state;
+  const size_t smem = (size_t)(3 * a.requests + 2) * 4, most = (3 * kMaxRequests + 2) * 4;
+  if (a.max_tokens <= kOneLaunch) {
+    const cudaError_t e = one.ensure(reserve_kernel<kPlan | kState>, most);
+    if (e != cudaSuccess) return e;
+    reserve_kernel<kPlan | kState><<<1, kThreads, smem, st>>>(a);
     return cudaGetLastError();
   }
+  cudaError_t e = plan.ensure(reserve_kernel<kPlan>, most);
+  if (e == cudaSuccess) e = state.ensure(reserve_kernel<kState>, most);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = ((int64_t)a.max_tokens + 4 * kThreads - 1) / (4 * kThreads);
+  reserve_kernel<kPlan><<<(unsigned)(ctas < 128 ? ctas : 128), kThreads, smem, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCluster);
+  cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = kCluster;
-  at.val.clusterDim.y = 1;
-  at.val.clusterDim.z = 1;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, reserve_kernel, a);
+  return cudaLaunchKernelEx(&cfg, reserve_kernel<kState>, a);
 }
 
 cudaError_t launch_release(const ReleaseArgs& a, cudaStream_t st) {

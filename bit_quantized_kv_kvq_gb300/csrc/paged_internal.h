@@ -34,6 +34,7 @@ struct ReserveArgs {
   int32_t *table, *cu, *slots, *positions, *lens_out, *free_count_out;
   uint32_t* status;
 };
+int reserve_launches(int max_tokens);
 cudaError_t launch_reserve(const ReserveArgs& a, cudaStream_t st);
 
 struct ReleaseArgs {

@@ -443,7 +443,8 @@ KVQ_API kvq_status kvq_paged_cache_status(kvq_paged_cache* cache, void* stream, 
  * whole or not at all: where it does not fit (pages, a table row, max_tokens)
  * or a length is negative, the table stays, cu_tokens is all 0, slots and
  * positions are all -1, lens_out and free_count_out repeat the inputs, and
- * the status word is set. All arrays int32 on the device. One launch. */
+ * the status word is set. All arrays int32 on the device. One launch, two for
+ * more than 4096 packed tokens. */
 KVQ_API kvq_status kvq_paged_reserve(kvq_paged_cache* cache, int32_t requests, const int32_t* lens,
                                      const int32_t* new_tokens, int32_t* table, const int32_t* free_pages,
                                      const int32_t* free_count, int32_t max_tokens, int32_t* cu_tokens,

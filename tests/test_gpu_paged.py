@@ -58,7 +58,7 @@ def test_reserve_and_release(r, page, tokens, longest, in_place):
     kw = dict(lens_out=dl, free_count_out=dc) if in_place else {}
     launches = kvq.kernel_launches()
     plan = cache.reserve(dl, ints(new), dt, df, dc, tokens, **kw)
-    assert kvq.kernel_launches() == launches + 1
+    assert kvq.kernel_launches() == launches + (1 if tokens <= 4096 else 2)
     want = PO.reserve(lens, new, table, free, pages - at, tokens, page)
     for got, ref in zip((dt, plan.cu_tokens, plan.slots, plan.positions, plan.lens, plan.free_count), want):
         assert np.array_equal(got.cpu().numpy().reshape(np.shape(ref)), ref)
