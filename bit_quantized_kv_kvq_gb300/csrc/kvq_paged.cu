@@ -47,9 +47,12 @@ kvq_status check_config(const kvq_paged_config* c) {
   if (c->max_pages < 1 || (int64_t)c->max_pages * c->page_tokens > INT32_MAX - 255)  // tile ends stay 32-bit
     return fail(KVQ_ERR_INVALID_ARG, "max_pages %d must be >= 1 and max_pages * page_tokens at most 2^31 - 256",
                 c->max_pages);
-  if ((int64_t)c->max_requests * (((int64_t)c->max_pages * c->page_tokens + 63) / 64) > INT32_MAX)
+  if ((int64_t)c->max_requests * (((int64_t)c->max_pages * c->page_tokens + 63) / 64 + 6) > INT32_MAX)
     return fail(KVQ_ERR_UNSUPPORTED, "max_requests %d times max_pages %d is too large to plan a decode", c->max_requests,
                 c->max_pages);
+  if ((int64_t)c->num_pages * c->num_kv_heads * 2 > INT32_MAX)  // the code tiles' index
+    return fail(KVQ_ERR_UNSUPPORTED, "num_pages %d times num_kv_heads %d must be below 2^30", c->num_pages,
+                c->num_kv_heads);
   if (c->code != KVQ_PAGE_INT8 && c->code != KVQ_PAGE_E4M3)
     return fail(KVQ_ERR_INVALID_ARG, "code %d must be KVQ_PAGE_INT8 or KVQ_PAGE_E4M3", c->code);
   if (c->dtype != KVQ_F16 && c->dtype != KVQ_BF16)

@@ -3,48 +3,58 @@
 //   e_t = c <q, k_hat_t>,  o = sum_t softmax(e)_t v_hat_t,  x_hat = code * s(page, head)
 //
 // The step is bound by the bytes of codes it reads: 2 L H D per request,
-// against 4 L H_q D operations. So the codes go straight from global memory
-// into the registers that the tensor cores read them from, and nothing is
-// staged: per warp and 16 tokens,
+// against 4 L H_q D operations. Per warp and 16 tokens,
 //   S^T = K Q^T   A = K codes (16 tokens x 16 channels), B = Q (8 heads),
 //   O^T += s_v V^T P^T   A = V codes (16 channels x 16 tokens), B = P^T,
 // both m16n8k16 in fp16 with fp32 sums. Every code (int8 or e4m3) is an exact
 // fp16 number, so only P is rounded (2^-11 of each weight). Tokens and
-// channels may be summed in any order, so a lane loads 16 contiguous bytes
+// channels may be summed in any order, so a lane reads 16 contiguous bytes
 // and calls them the fragment's slots.
 //
-// The tiles (64 or 128 tokens of one request and kv-head) of all requests form one
-// line that is cut into equal ranges, one per CTA: the kernel makes the line
-// from the device lengths itself, so the grid needs no host knowledge and
-// ragged batches stay even. A CTA's four warps take 16 tokens of a tile each
-// (32 with 64 channels: as many bytes in flight) and keep their own running maximum and sums. A (request, head) that one CTA
-// covers is finished there; the others leave partial sums, which a second
-// kernel merges in the order of the CTAs.
+// The tiles (64 or 128 tokens of one request and kv-head, 16 KB of codes) of
+// all requests form one line that is cut into equal ranges, one per CTA: the
+// kernel makes the line from the device lengths itself, so the grid needs no
+// host knowledge and ragged batches stay even. A (request, head) has kExtra
+// more places on the line than tiles, for what its begin, tail and merge cost
+// (5000 to 10000 clocks against 1300 to 1600 a tile): without them a CTA that
+// got fourteen one-tile requests took three times as long as the others. A producer warp walks the
+// range and keeps a ring of tiles in flight by TMA, on into the next request
+// or head while the four consumer warps still merge the last one; these take
+// 16 or 32 tokens of a tile each and keep their own running maximum and sums.
+// A (request, head) that one CTA covers is finished there; the others leave
+// partial sums, which a second kernel merges in the order of the CTAs.
 #pragma once
 
 #include "paged_internal.h"
+#include "tensor_map.cuh"
 
 namespace kvq {
 namespace pdec {
 
 constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kThreads = kWarps * 32;  // of the consumers; the producer is a fifth warp
 constexpr unsigned kFull = 0xffffffffu;
 
 // Groups of 16 tokens that a warp takes of a tile, and the tile's tokens.
 __host__ __device__ constexpr int sub_of(int dim) { return 128 / dim; }
 __host__ __device__ constexpr int unit_of(int dim) { return kWarps * 16 * sub_of(dim); }
 
+// Places on the line before a (request, head)'s tiles.
+constexpr int kExtra = 6;
+
 // Heads of one pass over the codes: 8 NT (NT column tiles of the products).
 __host__ __device__ constexpr int nt_of(int group) { return group <= 8 ? 1 : 2; }
-// CTAs per SM that the registers allow.
-__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : 2; }
+// CTAs per SM that the registers and the rings (kTileBytes each stage) allow.
+__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
+__host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 3 : 4; }
+constexpr int kTileBytes = 16384;  // keys, then values, of kWarps * 16 * sub_of(D) tokens
 
-// Workspace: int prefix[requests + 1] of tiles (one kv-head), then partial
+// Workspace: int prefix[requests + 1] of places (of one kv-head), then partial
 // rows [ctas][2][passes][8 NT][D + 2]: o[D], m, l.
 __host__ __device__ inline size_t prefix_bytes(int requests) { return ((size_t)(requests + 1) * 4 + 255) / 256 * 256; }
 
 struct Params {
+  CUtensorMap map;  // codes as [page, head, K or V][token][channel]
   PagedDev c;
   PagedDecodeArgs a;
   int ctas, passes;
@@ -129,23 +139,32 @@ struct Warp {
   float o[NT][kSteps][4];
   float m[NT][2], l[NT][2], qs[NT][2];  // heads 2 t4, 2 t4 + 1 of the column tile
 
-  // Queries of heads [h0, h0 + heads) and the empty running state.
-  __device__ __forceinline__ void begin(const uint16_t* q, int heads, float scale_log2) {
+  // Queries of `heads` heads, as they lie; begin() makes them ready.
+  __device__ __forceinline__ void load_q(const uint16_t* q, int heads) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const bool live = nt * 8 + g < heads;
       const uint16_t* row = q + (int64_t)(live ? nt * 8 + g : 0) * D;
-      uint32_t top = 0;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         const uint2 w = *reinterpret_cast<const uint2*>(row + ((s >> 2) * 4 + t) * 16 + (s & 3) * 4);
         qf[nt][s][0] = live ? w.x : 0u;
         qf[nt][s][1] = live ? w.y : 0u;
-        top = abs_max2(abs_max2(top, qf[nt][s][0]), qf[nt][s][1]);
       }
+    }
+  }
+
+  // The loaded queries' factors, and the empty running state.
+  __device__ __forceinline__ void begin(float scale_log2) {
+    const int t = threadIdx.x & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       float f = scale_log2;
       if (BF16) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) top = abs_max2(abs_max2(top, qf[nt][s][0]), qf[nt][s][1]);
         top = both_halves(top);
         top = max(top, __shfl_xor_sync(kFull, top, 1));
         top = max(top, __shfl_xor_sync(kFull, top, 2));
@@ -230,24 +249,26 @@ struct Warp {
     }
   }
 
+  // 16 tokens' codes from the swizzled tile (16-byte chunk index XOR address
+  // bits 7 to 9); k, v: the group's first row, at a multiple of 1024 bytes.
   __device__ __forceinline__ void load_k(const uint8_t* k, uint4 (&kr)[2][kChunks]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int c = 0; c < kChunks; ++c)
-        kr[r][c] = __ldcs(reinterpret_cast<const uint4*>(k + (g + 8 * r) * D + (c * 4 + t) * 16));
+        kr[r][c] = *reinterpret_cast<const uint4*>(k + swz<D>((g + 8 * r) * D + (c * 4 + t) * 16));
   }
   __device__ __forceinline__ void load_v(const uint8_t* v, uint32_t (&vr)[4][kVw]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const uint8_t* src = v + (2 * t + (r & 1) + (r >> 1) * 8) * D + g * (D / 8);
+      const uint8_t* src = v + swz<D>((2 * t + (r & 1) + (r >> 1) * 8) * D + g * (D / 8));
       if (D == 128) {
-        const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src));
+        const uint4 w = *reinterpret_cast<const uint4*>(src);
         vr[r][0] = w.x, vr[r][1] = w.y, vr[r][2 % kVw] = w.z, vr[r][3 % kVw] = w.w;
       } else {
-        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(src));
+        const uint2 w = *reinterpret_cast<const uint2*>(src);
         vr[r][0] = w.x, vr[r][1] = w.y;
       }
     }
@@ -300,17 +321,22 @@ struct Warp {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = g + 8 * r;
-      uint32_t top = 0;
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         const uint4* src = reinterpret_cast<const uint4*>(k + row * D + (c * 4 + t) * 16);
         const uint4 x = row < live ? src[0] : zero, y = row < live ? src[1] : zero;
         kw[r][c][0] = x.x, kw[r][c][1] = x.y, kw[r][c][2] = x.z, kw[r][c][3] = x.w;
         kw[r][c][4] = y.x, kw[r][c][5] = y.y, kw[r][c][6] = y.z, kw[r][c][7] = y.w;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = abs_max2(top, kw[r][c][i]);
       }
-      if (BF16) {
+    }
+    if (BF16) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = abs_max2(top, kw[r][c][i]);
         top = both_halves(top);
         top = max(top, __shfl_xor_sync(kFull, top, 1));
         top = max(top, __shfl_xor_sync(kFull, top, 2));
@@ -338,7 +364,6 @@ struct Warp {
     uint32_t p[NT][2];
     weights(s, f[0], f[1], g < live, g + 8 < live, p);
     uint32_t vw[4][D / 16];
-    uint32_t top = 0;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 2 * t + (r & 1) + (r >> 1) * 8;
@@ -346,10 +371,13 @@ struct Warp {
       for (int c = 0; c < D / 64; ++c) {
         const uint4 x = row < live ? reinterpret_cast<const uint4*>(v + row * D + g * (D / 8))[c] : zero;
         vw[r][4 * c] = x.x, vw[r][4 * c + 1] = x.y, vw[r][4 * c + 2] = x.z, vw[r][4 * c + 3] = x.w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = abs_max2(top, vw[r][4 * c + i]);
       }
     }
+    uint32_t top = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) top = abs_max2(top, vw[r][i]);
     float sv = 1.0f;
     if (BF16) {  // one power of two for the 16 rows
       const int e = bf16_shift(__reduce_max_sync(kFull, both_halves(top)));
@@ -367,192 +395,300 @@ struct Warp {
   }
 };
 
-// A tile's codes of one head, and its scales.
-struct TilePtr {
-  const uint8_t* k;
-  float ks, vs;
+// A part of one (request, kv-head): its tiles [t0, t1), and the place on the
+// line after the (request, head).
+struct Part {
+  int b, h, t0, t1, tiles;
+  long long end;
+  // the range's share of it
+  __device__ __forceinline__ void cut(long long v0, long long v1) {
+    const long long first = end - tiles;  // the place of tile 0
+    t0 = v0 > first ? (int)(v0 - first) : 0;
+    t1 = v1 < end ? (int)(v1 - first) : tiles;
+  }
 };
 
+// The first part of the range [v0, v1) of places; it may hold no tile
+// (t1 <= t0: only places before tile 0, or beyond).
+__device__ __forceinline__ Part first_part(const int* prefix, int requests, int heads, long long v0, long long v1) {
+  Part x;
+  x.b = 0;
+  for (int n = requests; n > 1;) {  // last b with prefix[b] * heads <= v0 (equal ones: empty requests before it)
+    const int half = n >> 1;
+    if ((long long)prefix[x.b + half] * heads <= v0) x.b += half, n -= half;
+    else n = half;
+  }
+  const int places = prefix[x.b + 1] - prefix[x.b];
+  const long long at = v0 - (long long)prefix[x.b] * heads;
+  x.h = (unsigned long long)at >> 32 ? (int)(at / places) : (int)((uint32_t)at / (uint32_t)places);
+  x.tiles = places - kExtra;
+  x.end = (long long)prefix[x.b] * heads + (long long)(x.h + 1) * places;
+  x.cut(v0, v1);
+  return x;
+}
+
+// The next part, or false where the range ends before it has a tile.
+__device__ __forceinline__ bool next_part(Part& x, const int* prefix, int requests, int heads, long long v0,
+                                          long long v1) {
+  do {
+    if (x.end >= v1) return false;
+    if (++x.h == heads) {
+      x.h = 0;
+      do ++x.b;
+      while (prefix[x.b + 1] == prefix[x.b]);  // ends: there are places before v1
+      x.tiles = prefix[x.b + 1] - prefix[x.b] - kExtra;
+    }
+    x.end += x.tiles + kExtra;
+    x.cut(v0, v1);
+  } while (x.t1 <= x.t0);
+  return true;
+}
+
+template <int NT>
+struct Ring {
+  uint64_t full[stages_of(NT)], empty[stages_of(NT)];
+  uint32_t live[stages_of(NT)];     // bit i: box i of the tile is there
+  float2 scale[stages_of(NT)][8];   // its scales of keys and values
+};
+
+// Whole warp: false where the wait gave up.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  const bool done = mbar_wait_bounded(bar, parity);
+  if (!done) raise_status(status, kStatusTimeout);
+  return __all_sync(kFull, done);
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// The producer: per tile, boxes of min(P, 64) tokens of complete pages.
+template <int D, int NT>
+__device__ __forceinline__ void produce(const Params& prm, Ring<NT>& ring, unsigned char* tiles, const int* prefix,
+                                        Part x, const long long v0, const long long v1) {
+  constexpr int kStages = stages_of(NT), kUnit = unit_of(D);
+  const PagedDev& c = prm.c;
+  const int lane = threadIdx.x & 31, P = 1 << c.page_shift;
+  const int box = P < 64 ? P : 64, boxes = kUnit / box;
+  int i = 0;
+  bool ok = true;
+  do {
+    const int full = prm.a.lens[x.b] & ~(P - 1);  // tokens in complete pages
+    const int32_t* row = prm.a.table + (int64_t)x.b * c.max_pages;
+    auto page_at = [&](int tile) {
+      const int tk = tile * kUnit + lane * box;
+      return lane < boxes && tk < full ? row[tk >> c.page_shift] : -1;
+    };
+    int page = page_at(x.t0);
+    for (int tile = x.t0; tile < x.t1; ++tile, ++i) {
+      const int st = i % kStages, tk = tile * kUnit + lane * box;
+      const int next = tile + 1 < x.t1 ? page_at(tile + 1) : -1;
+      const bool wanted = lane < boxes && tk < full, there = wanted && page >= 0 && page < c.num_pages;
+      if (wanted && !there) raise_status(c.status, kStatusBadIndex);
+      const uint32_t live = __ballot_sync(kFull, there);
+      ok = wait(&ring.empty[st], ((i / kStages) & 1) ^ 1, c.status);
+      if (!ok) break;
+      if (lane == 0) {
+        ring.live[st] = live;
+        expect_tx(&ring.full[st], (uint32_t)__popc(live) * box * D * 2);
+      }
+      __syncwarp();
+      if (there) {
+        const int64_t ph = ((int64_t)page * c.heads + x.h) * 2;
+        unsigned char* dst = tiles + st * kTileBytes + lane * box * D;
+        tma_rows(dst, &prm.map, tk & (P - 1), (int)ph, &ring.full[st]);
+        tma_rows(dst + kTileBytes / 2, &prm.map, tk & (P - 1), (int)ph + 1, &ring.full[st]);
+        ring.scale[st][lane] = *reinterpret_cast<const float2*>(c.scales + ph);
+      }
+      __syncwarp();
+      if (lane == 0) arrive(&ring.full[st]);
+      page = next;
+    }
+  } while (ok && next_part(x, prefix, prm.a.requests, c.heads, v0, v1));
+  // nothing is in flight into this CTA's shared memory when it ends
+  for (int k = max(0, i - kStages); k < i; ++k) wait(&ring.full[k % kStages], (k / kStages) & 1, c.status);
+}
+
 template <int D, int CODE, bool BF16, int NT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) paged_decode_kernel(const Params prm) {
+__global__ void __launch_bounds__(kThreads + 32, ctas_per_sm(NT))
+    paged_decode_kernel(const __grid_constant__ Params prm) {
   using W = Warp<D, CODE, BF16, NT>;
-  constexpr int kSub = sub_of(D), kUnit = unit_of(D);
+  constexpr int kSub = sub_of(D), kUnit = unit_of(D), kStages = stages_of(NT);
   const PagedDev& c = prm.c;
   const PagedDecodeArgs& a = prm.a;
-  extern __shared__ int prefix[];  // [requests + 1]
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* tiles = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  int* prefix = reinterpret_cast<int*>(tiles + kStages * kTileBytes);  // [requests + 1]
   __shared__ float so[kWarps][8 * NT][D + 1];
   __shared__ float sml[kWarps][8 * NT][2];
   __shared__ int wsum[kWarps];
+  __shared__ Ring<NT> ring;
+  __shared__ int failed;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int R = a.requests, P = 1 << c.page_shift;
   const int most = c.max_pages << c.page_shift;
 
-  // prefix sums of the requests' tiles
+  if (threadIdx.x == kThreads) {
+    prefetch_map(&prm.map);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&ring.full[i], 1);
+      mbar_init(&ring.empty[i], kWarps);
+    }
+    mbar_fence_init();
+    failed = 0;
+  }
+  // prefix sums of the requests' places
+  auto places_of = [&](int n) { return n > 0 ? (n + kUnit - 1) / kUnit + kExtra : 0; };
   const int per = (R + kThreads - 1) / kThreads;
-  int sum = 0;
-  bool bad = false;
-  for (int i = 0; i < per; ++i) {
-    const int b = threadIdx.x * per + i;
-    int n = b < R ? a.lens[b] : 0;
-    if (n < 0 || n > most) bad = true, n = 0;
-    sum += (n + kUnit - 1) / kUnit;
-  }
-  if (bad && blockIdx.x == 0 && blockIdx.y == 0) raise_status(c.status, kStatusBadIndex);
-  int incl = sum;
+  int sum = 0, incl = 0;
+  if (warp < kWarps) {
+    bool bad = false;
+    for (int i = 0; i < per; ++i) {
+      const int b = threadIdx.x * per + i;
+      int n = b < R ? a.lens[b] : 0;
+      if (n < 0 || n > most) bad = true, n = 0;
+      sum += places_of(n);
+    }
+    if (bad && blockIdx.x == 0 && blockIdx.y == 0) raise_status(c.status, kStatusBadIndex);
+    incl = sum;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int u = __shfl_up_sync(kFull, incl, d);
-    if (lane >= d) incl += u;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(kFull, incl, d);
+      if (lane >= d) incl += u;
+    }
+    if (lane == 31) wsum[warp] = incl;
   }
-  if (lane == 31) wsum[warp] = incl;
   __syncthreads();
-  int at = incl - sum;
-  for (int i = 0; i < warp; ++i) at += wsum[i];
-  for (int i = 0; i < per; ++i) {
-    const int b = threadIdx.x * per + i;
-    if (b < R) {
-      prefix[b] = at;
-      int n = a.lens[b];
-      if (n < 0 || n > most) n = 0;
-      at += (n + kUnit - 1) / kUnit;
-      if (b == R - 1) prefix[R] = at;
+  if (warp < kWarps) {
+    int at = incl - sum;
+    for (int i = 0; i < warp; ++i) at += wsum[i];
+    for (int i = 0; i < per; ++i) {
+      const int b = threadIdx.x * per + i;
+      if (b < R) {
+        prefix[b] = at;
+        int n = a.lens[b];
+        if (n < 0 || n > most) n = 0;
+        at += places_of(n);
+        if (b == R - 1) prefix[R] = at;
+      }
     }
   }
   __syncthreads();
   if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int b = threadIdx.x; b <= R; b += kThreads) prm.prefix[b] = prefix[b];
+    for (int b = threadIdx.x; b <= R; b += kThreads + 32) prm.prefix[b] = prefix[b];
 
-  const long long units = (long long)prefix[R] * c.heads;
-  const int ctas = units < prm.ctas ? (int)units : prm.ctas;  // each of these has a tile at least
+  const long long places = (long long)prefix[R] * c.heads;
+  const int ctas = places < prm.ctas ? (int)places : prm.ctas;  // each of these has a place at least
   if ((int)blockIdx.x >= ctas) return;
-  const long long u1 = units * (blockIdx.x + 1) / ctas;
-  long long u = units * blockIdx.x / ctas;
-  while (u < u1) {
-    // the request, head and tiles [t0, t1) that start at unit u
-    int b = 0;
-    {
-      int n = R;
-      while (n > 1) {  // last b with prefix[b] * heads <= u (equal ones: empty requests before it)
-        const int half = n >> 1;
-        if ((long long)prefix[b + half] * c.heads <= u) b += half, n -= half;
-        else n = half;
-      }
-    }
-    const int tiles = prefix[b + 1] - prefix[b];
-    const long long in_b = u - (long long)prefix[b] * c.heads;
-    const int h = (int)(in_b / tiles), t0 = (int)(in_b % tiles);
-    const int t1 = (int)(u1 - u < tiles - t0 ? t0 + (u1 - u) : tiles);
-    const int len = a.lens[b];
+  const long long v0 = places * blockIdx.x / ctas, v1 = places * (blockIdx.x + 1) / ctas;
+  Part cur = first_part(prefix, R, c.heads, v0, v1);
+  if (cur.t1 <= cur.t0 && !next_part(cur, prefix, R, c.heads, v0, v1)) return;  // no tile: all of the CTA
+  if (warp == kWarps) {
+    produce<D, NT>(prm, ring, tiles, prefix, cur, v0, v1);
+    return;
+  }
+
+  const int box_shift = c.page_shift < 6 ? c.page_shift : 6;
+  const int pass0 = blockIdx.y * 8 * NT, heads = min(8 * NT, a.group - pass0);
+  W w;
+  auto load_q = [&](const Part& x) {
+    w.load_q(a.q + x.b * a.q_stride + (int64_t)(x.h * a.group + pass0) * D, heads);
+  };
+  load_q(cur);
+  bool ok = true;
+  int len = a.lens[cur.b];
+  for (int i = 0;;) {
     const int full = len & ~(P - 1);  // tokens in complete pages
-    const int head0 = h * a.group + blockIdx.y * 8 * NT;
-    const int heads = min(8 * NT, a.group - (int)blockIdx.y * 8 * NT);
-
-    W w;
-    w.begin(a.q + b * a.q_stride + (int64_t)head0 * D, heads, a.scale_log2);
-    const int32_t* row = a.table + (int64_t)b * c.max_pages;
-
-    auto tile_of = [&](int page, int tok, bool live) {
-      TilePtr p;
-      const bool ok = page >= 0 && page < c.num_pages;
-      if (!ok && live && lane == 0) raise_status(c.status, kStatusBadIndex);
-      const int64_t ph = ((int64_t)(ok ? page : 0) * c.heads + h) * 2;
-      p.k = c.pages + (ph << c.page_shift) * D + (tok & (P - 1)) * D;
-      const float2 s = *reinterpret_cast<const float2*>(c.scales + ph);
-      p.ks = s.x;
-      p.vs = s.y;
-      if (!ok) p.k = nullptr;
-      return p;
-    };
-    const int end = t1 * kUnit, page_end = min(end, full);
-    int tok = t0 * kUnit + warp * 16 * kSub;
-    if (tok < page_end) {
+    const uint16_t* tail = c.tails + ((((int64_t)cur.b * c.heads + cur.h) * 2) << c.page_shift) * D;
+    const int tail0 = max(full, cur.t0 * kUnit), tail_end = min(cur.t1 * kUnit, len);
+    for (int tk = tail0 + (threadIdx.x >> 1); tk < tail_end; tk += kThreads / 2) {  // half a row a thread, keys and values
+      const uint16_t* at = tail + (tk - full) * D + (threadIdx.x & 1) * (D / 2);
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(at + (int64_t)P * D));
+    }
+    w.begin(a.scale_log2);
+    for (int tile = cur.t0; tile < cur.t1; ++tile, ++i) {
+      const int st = i % kStages;
+      ok = ok && wait(&ring.full[st], (i / kStages) & 1, c.status);
+      if (!ok) break;
+      const unsigned char* k = tiles + st * kTileBytes + warp * 16 * kSub * D;
       uint4 kr[kSub][2][W::kChunks];
       uint32_t vr[kSub][4][W::kVw];
-      TilePtr p[kSub];
-      int next[kSub];
-      // a group past the complete pages, or of a page out of range, takes no part
-      auto page_at = [&](int tk) { return tk < page_end ? row[tk >> c.page_shift] : -1; };
-      auto base_of = [&](const TilePtr& q) { return q.k ? q.k : c.pages; };
+      float2 sc[kSub];
+      const uint32_t live = ring.live[st];
+      bool there[kSub];
 #pragma unroll
-      for (int i = 0; i < kSub; ++i) {
-        p[i] = tile_of(page_at(tok + 16 * i), tok + 16 * i, tok + 16 * i < page_end);
-        w.load_k(base_of(p[i]), kr[i]);
-        w.load_v(base_of(p[i]) + (size_t)P * D, vr[i]);
-        next[i] = page_at(tok + kUnit + 16 * i);
+      for (int j = 0; j < kSub; ++j) {
+        const int box = (warp * 16 * kSub + 16 * j) >> box_shift;
+        there[j] = (live >> box) & 1;
+        sc[j] = ring.scale[st][box];
+        w.load_k(k + 16 * j * D, kr[j]);
+        w.load_v(k + kTileBytes / 2 + 16 * j * D, vr[j]);
       }
-      for (;;) {
-        const int then = tok + kUnit;
-        const bool more = then < page_end;
-        TilePtr pn[kSub];
-        int after[kSub];
+      __syncwarp();
+      if (lane == 0) arrive(&ring.empty[st]);
 #pragma unroll
-        for (int i = 0; i < kSub; ++i) after[i] = page_at(then + kUnit + 16 * i);
-#pragma unroll
-        for (int i = 0; i < kSub; ++i) {
-          float s[NT][4];
-          w.scores(kr[i], s);
-          pn[i] = p[i];
-          if (more) {
-            pn[i] = tile_of(next[i], then + 16 * i, then + 16 * i < page_end);
-            w.load_k(base_of(pn[i]), kr[i]);
-          }
-          if (p[i].k) {
-            uint32_t pb[NT][2];
-            w.weights(s, p[i].ks, p[i].ks, true, true, pb);
-            w.values(vr[i], p[i].vs, pb);
-          }
-          if (more) w.load_v(base_of(pn[i]) + (size_t)P * D, vr[i]);
-        }
-        if (!more) break;
-        tok = then;
-#pragma unroll
-        for (int i = 0; i < kSub; ++i) p[i] = pn[i], next[i] = after[i];
+      for (int j = 0; j < kSub; ++j) {
+        if (!there[j]) continue;
+        float s[NT][4];
+        uint32_t pb[NT][2];
+        w.scores(kr[j], s);
+        w.weights(s, sc[j].x, sc[j].x, true, true, pb);
+        w.values(vr[j], sc[j].y, pb);
       }
     }
-    const int tail_end = min(end, len);
-    for (int tk = max(full, t0 * kUnit); tk < tail_end; tk += 16) {
-      if (tk % kUnit / (16 * kSub) != warp) continue;
-      const uint16_t* kt = c.tails + ((((int64_t)b * c.heads + h) * 2) << c.page_shift) * D + (tk - full) * D;
-      w.tail_rows(kt, kt + (int64_t)P * D, min(16, len - tk));
-    }
+    for (int tk = tail0; tk < tail_end; tk += 16)
+      if (tk % kUnit / (16 * kSub) == warp)
+        w.tail_rows(tail + (tk - full) * D, tail + (tk - full + P) * D, min(16, len - tk));
 
-    // the four warps' sums
-    __syncthreads();  // the last segment's readers are done
+    // the four warps' sums; the next part's queries are on their way meanwhile
+    const Part done = cur;
+    if (!ok) failed = 1;
+    const bool go_on = next_part(cur, prefix, R, c.heads, v0, v1);
+    if (go_on) {
+      len = a.lens[cur.b];
+      load_q(cur);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = w.l[nt][i];
+      for (int i2 = 0; i2 < 2; ++i2) {
+        float x = w.l[nt][i2];
         x += __shfl_xor_sync(kFull, x, 4);
         x += __shfl_xor_sync(kFull, x, 8);
         x += __shfl_xor_sync(kFull, x, 16);
-        const int hd = nt * 8 + 2 * t + i;
-        if (g == 0) sml[warp][hd][0] = w.m[nt][i], sml[warp][hd][1] = x;
+        const int hd = nt * 8 + 2 * t + i2;
+        if (g == 0) sml[warp][hd][0] = w.m[nt][i2], sml[warp][hd][1] = x;
 #pragma unroll
         for (int j = 0; j < W::kSteps; ++j) {
-          so[warp][hd][g * (D / 8) + 2 * j] = w.o[nt][j][i];
-          so[warp][hd][g * (D / 8) + 2 * j + 1] = w.o[nt][j][2 + i];
+          so[warp][hd][g * (D / 8) + 2 * j] = w.o[nt][j][i2];
+          so[warp][hd][g * (D / 8) + 2 * j + 1] = w.o[nt][j][2 + i2];
         }
       }
-    __syncthreads();
-    const bool whole = t0 == 0 && t1 == tiles;
-    float* part = prm.part + ((((int64_t)blockIdx.x * 2 + (t0 > 0 ? 0 : 1)) * prm.passes + blockIdx.y) * 8 * NT) * (D + 2);
-    for (int i = threadIdx.x; i < heads * D; i += kThreads) {
-      const int hd = i / D, ch = i % D;
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (failed) return;  // all four warps: a wait gave up
+    const bool whole = done.t0 == 0 && done.t1 == done.tiles;
+    const int head0 = done.h * a.group + pass0;
+    float* part =
+        prm.part + ((((int64_t)blockIdx.x * 2 + (done.t0 > 0 ? 0 : 1)) * prm.passes + blockIdx.y) * 8 * NT) * (D + 2);
+    for (int k = threadIdx.x; k < heads * D; k += kThreads) {
+      const int hd = k / D, ch = k % D;
       float top = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) top = fmaxf(top, sml[k][hd][0]);
+      for (int v = 0; v < kWarps; ++v) top = fmaxf(top, sml[v][hd][0]);
       const float ref = top == -INFINITY ? 0.0f : top;
       float o = 0.0f, l = 0.0f;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        const float f = exp2_fast(sml[k][hd][0] - ref);
-        o = fmaf(f, so[k][hd][ch], o);
-        l = fmaf(f, sml[k][hd][1], l);
+      for (int v = 0; v < kWarps; ++v) {
+        const float f = exp2_fast(sml[v][hd][0] - ref);
+        o = fmaf(f, so[v][hd][ch], o);
+        l = fmaf(f, sml[v][hd][1], l);
       }
       if (whole) {
-        const int64_t to = ((int64_t)b * a.q_heads + head0 + hd) * D + ch;
+        const int64_t to = ((int64_t)done.b * a.q_heads + head0 + hd) * D + ch;
         const float r = o / l;
         if (a.out_f32) static_cast<float*>(a.out)[to] = r;
         else if (BF16) static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16(r);
@@ -562,27 +698,32 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) paged_decode_kernel
         if (ch == 0) part[hd * (D + 2) + D] = top, part[hd * (D + 2) + D + 1] = l;
       }
     }
-    u += t1 - t0;
+    if (!go_on) return;
+    asm volatile("bar.sync 1, 128;" ::: "memory");  // so and sml may be written again
   }
 }
 
 // Merges the partial sums of each (request, query head) that several CTAs
 // share, in the order of the CTAs; zeros for a request without tokens.
 template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(D) paged_merge_kernel(const Params prm) {
+__global__ void __launch_bounds__(D) paged_merge_kernel(const __grid_constant__ Params prm) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PagedDecodeArgs& a = prm.a;
   const int b = blockIdx.x, hq = blockIdx.y, ch = threadIdx.x;
   const int h = hq / a.group, in_group = hq % a.group, pass = in_group / (8 * NT), hd = in_group % (8 * NT);
-  const int p0 = prm.prefix[b], tiles = prm.prefix[b + 1] - p0;
+  const int p0 = prm.prefix[b], own = prm.prefix[b + 1] - p0;
   const int64_t to = ((int64_t)b * a.q_heads + hq) * D + ch;
   float r = 0.0f;
-  if (tiles > 0) {
-    const long long units = (long long)prm.prefix[a.requests] * prm.c.heads;
-    const long long first = (long long)p0 * prm.c.heads + (long long)h * tiles, last = first + tiles - 1;
-    // the CTA of unit u is the last c with floor(units c / ctas) <= u
-    const int ctas = units < prm.ctas ? (int)units : prm.ctas;
-    const int c0 = (int)(((first + 1) * ctas - 1) / units), c1 = (int)(((last + 1) * ctas - 1) / units);
+  if (own > 0) {
+    const long long places = (long long)prm.prefix[a.requests] * prm.c.heads;
+    const long long end = (long long)p0 * prm.c.heads + (long long)(h + 1) * own, first = end - (own - kExtra);
+    // the CTA of a place v is the last c with floor(places c / ctas) <= v
+    const int ctas = places < prm.ctas ? (int)places : prm.ctas;
+    auto cta_of = [&](long long v) {
+      const unsigned long long n = (unsigned long long)(v + 1) * ctas - 1;
+      return (n | places) >> 32 ? (int)(n / places) : (int)((uint32_t)n / (uint32_t)places);
+    };
+    const int c0 = cta_of(first), c1 = cta_of(end - 1);
     if (c0 == c1) return;  // finished by that CTA
     const int64_t step = (int64_t)2 * prm.passes * 8 * NT * (D + 2);
     const float* part = prm.part + (int64_t)c0 * step + ((int64_t)pass * 8 * NT + hd) * (D + 2);
@@ -625,11 +766,23 @@ cudaError_t launch(const PagedDev& c, const PagedDecodeArgs& a, cudaStream_t st)
   p.passes = (a.group + 8 * NT - 1) / (8 * NT);
   p.prefix = static_cast<int*>(a.ws);
   p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + prefix_bytes(a.requests));
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const int page = 1 << c.page_shift;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)c.num_pages * c.heads * 2};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * page};
+  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)(page < 64 ? page : 64), 1u};
+  const cuuint32_t es[3] = {1u, 1u, 1u};
+  if (fn(&p.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.pages, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   static SmemAttr attr;
-  const size_t smem = (size_t)(a.requests + 1) * 4;
-  cudaError_t e = attr.ensure(paged_decode_kernel<D, CODE, BF16, NT>, (kMaxRequests + 1) * 4);
+  const size_t ring = 1024 + stages_of(NT) * kTileBytes;
+  cudaError_t e = attr.ensure(paged_decode_kernel<D, CODE, BF16, NT>, ring + (kMaxRequests + 1) * 4);
   if (e != cudaSuccess) return e;
-  paged_decode_kernel<D, CODE, BF16, NT><<<dim3(p.ctas, p.passes), kThreads, smem, st>>>(p);
+  paged_decode_kernel<D, CODE, BF16, NT>
+      <<<dim3(p.ctas, p.passes), kThreads + 32, ring + (size_t)(a.requests + 1) * 4, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
