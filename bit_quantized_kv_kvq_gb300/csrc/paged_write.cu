@@ -72,15 +72,17 @@ struct WriteCfg {
   static constexpr int kThreads = 2 * kHalf;
 };
 
+// 64 registers a thread: 1024 threads of an SM, 128 KB of rows on their way.
 template <int P, int D, int CODE, bool BF16>
-__global__ void __launch_bounds__(WriteCfg<P, D, CODE, BF16>::kThreads)
+__global__ void __launch_bounds__(WriteCfg<P, D, CODE, BF16>::kThreads, 1024 / WriteCfg<P, D, CODE, BF16>::kThreads)
     paged_write_kernel(const PagedDev c, const PagedWriteArgs a) {
   using Cfg = WriteCfg<P, D, CODE, BF16>;
   constexpr int kRowGran = D / 16;
-  const int h = blockIdx.y;
+  // heads run fastest: CTAs that run together read whole token rows
+  const int h = blockIdx.x % c.heads;
   const int32_t* cu = a.cu;
   // items of request b start at floor(cu[b] / P) + b: room for ceil(m / P) of them
-  const int w = blockIdx.x;
+  const int w = blockIdx.x / c.heads;
   const int b = warp_last_le(a.requests, w, [&](int i) { return (int)((uint32_t)cu[i] / P) + i; });
   const int c0 = cu[b], m = cu[b + 1] - c0;
   if (m <= 0) return;
@@ -102,6 +104,7 @@ __global__ void __launch_bounds__(WriteCfg<P, D, CODE, BF16>::kThreads)
     uint4 x[Cfg::kGran][2];
     uint32_t top = 0;
     const int start = (page0 + j) * P;  // position of the page's first token
+    const int slot = a.slots[c0 + start + P - 1 - old];  // of the page's last token
 #pragma unroll
     for (int i = 0; i < Cfg::kGran; ++i) {
       const int gr = i * Cfg::kHalf + tid, row = gr / kRowGran, ch = (gr % kRowGran) * 16;
@@ -126,7 +129,6 @@ __global__ void __launch_bounds__(WriteCfg<P, D, CODE, BF16>::kThreads)
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) top = max(top, wtop[half * kWarps + i]);
     const float s = __fdiv_rn(unpack2<BF16>(top).x, CODE == KVQ_PAGE_INT8 ? 127.0f : 448.0f);
-    const int slot = a.slots[c0 + start + P - 1 - old];  // of the page's last token
     const int page = slot >> c.page_shift;
     if (slot < 0 || page >= c.num_pages || (slot & (P - 1)) != P - 1) {
       if (threadIdx.x == 0) raise_status(c.status, kStatusBadIndex);
@@ -174,8 +176,9 @@ __global__ void __launch_bounds__(WriteCfg<P, D, CODE, BF16>::kThreads)
 
 template <int P, int D, int CODE, bool BF16>
 cudaError_t launch(const PagedDev& c, const PagedWriteArgs& a, cudaStream_t st) {
-  const dim3 grid(a.max_tokens / P + a.requests, c.heads);
-  paged_write_kernel<P, D, CODE, BF16><<<grid, WriteCfg<P, D, CODE, BF16>::kThreads, 0, st>>>(c, a);
+  const int64_t grid = (int64_t)(a.max_tokens / P + a.requests) * c.heads;
+  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+  paged_write_kernel<P, D, CODE, BF16><<<(unsigned)grid, WriteCfg<P, D, CODE, BF16>::kThreads, 0, st>>>(c, a);
   return cudaGetLastError();
 }
 
