@@ -376,6 +376,12 @@ KVQ_API kvq_status kvq_cache_status(kvq_cache* cache, void* stream, uint32_t* wo
  * they hold is checked on the device: a value out of range sets the status
  * word (kvq_paged_cache_status) and the work that it belongs to is left out.
  *
+ * Outputs must not overlap inputs unless a call says so. Pages may be read by
+ * several requests (a shared prefix) but are written for one. Calls that write
+ * and calls that read the same layer, and reserves and releases of the same
+ * arrays, must be ordered on the GPU; decodes of one layer may overlap, each
+ * with a workspace of its own.
+ *
  * A step: kvq_paged_reserve once; then per layer kvq_paged_write, and
  * kvq_prompt_attention for prompts or kvq_paged_decode_attention for single
  * tokens; kvq_paged_release when requests end.

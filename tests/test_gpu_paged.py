@@ -454,3 +454,58 @@ def test_pages_past_four_gibibytes():
     assert table.tolist() == [[pages - 2, pages - 1, 5, -1]]
     assert torch.equal(small.decode(0, q, t2, p2.lens, 0.1, out_dtype=torch.float32), o)
     assert cache.status() == 0
+
+
+def test_many_requests():
+    """4096 slots, most of them idle or short: the plan, the write and the decode."""
+    r, page = 4096, 16
+    rs = np.random.RandomState(5)
+    new = rs.randint(0, 3, r)
+    new[[3, 4095]] = [700, 90]
+    t = int(new.sum())
+    pages = int((-(-new // page)).sum())
+    cache = kvq.PagedKVCache(1, r, 1, 64, page, pages, 48)
+    table, free = ints(np.full((r, 48), -1)), ints(rs.permutation(pages))
+    gen = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(t, 1, 64, generator=gen).half() for _ in range(2))
+    q = torch.randn(r, 2, 64, generator=gen).half()
+    lens, count = ints(np.zeros(r)), ints([pages])
+    plan = cache.reserve(lens, ints(new), table, free, count, t, lens_out=lens, free_count_out=count)
+    cache.write(0, k.cuda(), v.cuda(), plan.cu_tokens, plan.slots, lens)
+    o = cache.decode(0, q.cuda(), table, lens, 0.125).double().cpu().numpy()
+    assert count.item() == 0 and np.array_equal(lens.cpu().numpy(), new) and cache.status() == 0
+    cu, tab = plan.cu_tokens.tolist(), table.cpu().numpy()
+    assert not o[new == 0].any()
+    for b in list(np.flatnonzero(new)[:20]) + [3, 4095]:
+        oracle = PO.PagedOracle(1, 1, 64, page, "int8")
+        oracle.write(0, k[cu[b]:cu[b + 1]].double().numpy(), v[cu[b]:cu[b + 1]].double().numpy(), tab[b])
+        kv = oracle.values(0, tab[b])
+        for h in range(2):
+            ref, w, size = PO.attend(q[b, h].double().numpy(), kv[0, 0], kv[1, 0], 0.125)
+            tol = decode_bound(w, size, np.abs(kv[1]).max(), int(new[b]), 2.0 ** -11, ref)
+            assert (np.abs(o[b, h] - ref) <= tol).all(), b
+
+
+def test_shared_pages_are_read_by_both():
+    """Two requests whose tables name the same complete pages (a shared prefix)."""
+    s = Served(2, 2, 128, 32, "e4m3", F16, 256, seed=3)
+    s.step([200, 0])
+    table = s.table.clone()
+    table[1] = table[0]
+    lens = ints([192, 192])
+    q = s.rows(1, 8).cuda().repeat(2, 1, 1)
+    o = s.cache.decode(0, q, table, lens, 0.1)
+    assert torch.equal(o[0], o[1]) and o.any()
+    assert s.cache.status() == 0
+
+
+def test_write_takes_the_rows_after_others():
+    """cu_tokens that starts inside the packed rows: the ones before it are not read."""
+    cache = kvq.PagedKVCache(1, 1, 1, 64, 16, 4, 4)
+    x = torch.randn(100, 1, 64, generator=torch.Generator().manual_seed(2)).half().cuda()
+    x[:60] = float("nan")
+    slots = ints(np.concatenate([np.full(60, -1), np.arange(40)]))
+    cache.write(0, x, x, ints([60, 100]), slots, ints([40]))
+    other = kvq.PagedKVCache(1, 1, 1, 64, 16, 4, 4)
+    other.write(0, x[60:], x[60:], ints([0, 40]), ints(np.arange(40)), ints([40]))
+    assert torch.equal(cache.buffer, other.buffer) and cache.status() == 0

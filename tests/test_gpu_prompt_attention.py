@@ -2,6 +2,7 @@
 from its roundings: lengths around the tile borders, head groups, strides,
 sequences of no tokens, rows outside every sequence, infinities and NaN."""
 import math
+import os
 
 import numpy as np
 import pytest
@@ -213,3 +214,75 @@ def test_arguments_are_checked():
                                              x[..., :32].contiguous()[:, 6:], cu, 0.1)):
         with pytest.raises(kvq.KVQError):
             bad()
+
+
+def test_pack_does_not_change_a_sequence():
+    """A sequence's rows have the same bits alone, anywhere in a pack, and every time."""
+    x = rows(1500, 4, 2, 128, BF16, seed=12).cuda()
+    cu = [0, 1, 700, 701, 701, 1100, 1500]
+    def run(lo, hi, c):
+        y = x[lo:hi]
+        return kvq.prompt_attention(y[:, :4], y[:, 4:6], y[:, 6:], ints(c), 0.09)
+    whole = run(0, 1500, cu)
+    for _ in range(3):
+        assert torch.equal(run(0, 1500, cu), whole)
+    for lo, hi in zip(cu[:-1], cu[1:]):
+        if hi > lo:
+            assert torch.equal(run(lo, hi, [0, hi - lo]), whole[lo:hi])
+
+
+def test_rows_before_the_first_sequence_and_unaligned_output():
+    """cu_tokens that starts far in; an output on a 16-byte, not a 32-byte border."""
+    x = rows(700, 3, 3, 64, F16, seed=13).cuda()
+    q, k, v = x[:, :3], x[:, 3:6], x[:, 6:]
+    want = kvq.prompt_attention(q[300:], k[300:], v[300:], ints([0, 150, 400]), 0.125)
+    flat = torch.full((700 * 3 * 64 + 8,), 5.0, dtype=F16, device="cuda")
+    out = flat[8:].view(700, 3, 64)
+    assert out.data_ptr() % 32 == 16
+    kvq.prompt_attention(q, k, v, ints([300, 450, 700]), 0.125, out=out)
+    assert torch.equal(out[300:], want) and (out[:300] == 5).all() and (flat[:8] == 5).all()
+
+
+def test_many_sequences():
+    lens = np.random.RandomState(3).randint(0, 9, 4096)
+    lens[[7, 2000]] = [300, 140]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    x = rows(int(cu[-1]), 2, 1, 64, F16, seed=14).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = kvq.prompt_attention(x[:, :2], x[:, 2:3], x[:, 3:], ints(cu), 0.125, status=status)
+    assert status.item() == 0
+    picks = [0, 1, 7, 8, 1999, 2000, 2001, 4095]
+    for s in picks:
+        lo, hi = int(cu[s]), int(cu[s + 1])
+        if hi > lo:
+            y = x[lo:hi]
+            assert torch.equal(o[lo:hi], kvq.prompt_attention(y[:, :2], y[:, 2:3], y[:, 3:], ints([0, hi - lo]), 0.125))
+    check(x[:int(cu[40])], 2, 1, cu[:41].tolist(), 0.125)
+
+
+def test_first_call_of_a_process_in_a_capture():
+    """Kernels that load while a stream is captured (a fresh process)."""
+    import subprocess
+    import sys
+    code = """
+import sys, torch
+sys.path.insert(0, %r)
+import bit_quantized_kv_kvq_gb300 as kvq
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+x = torch.randn(80, 6, 64, device="cuda").half()
+cache = kvq.PagedKVCache(1, 2, 1, 64, 16, 8, 4)
+lens, new, table, free, count = i([0, 0]), i([40, 40]), i([[-1] * 4] * 2), i(list(range(8))), i([8])
+out = torch.zeros(80, 4, 64, dtype=torch.float16, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    plan = cache.reserve(lens, new, table, free, count, 80)
+    cache.write(0, x[:, 4:5], x[:, 5:], plan.cu_tokens, plan.slots, plan.lens)
+    kvq.prompt_attention(x[:, :4], x[:, 4:5], x[:, 5:], plan.cu_tokens, 0.1, out=out)
+    dec = cache.decode(0, x[:2, :4], table, plan.lens, 0.1)
+g.replay()
+torch.cuda.synchronize()
+assert cache.status() == 0 and plan.lens.tolist() == [40, 40] and count.item() == 8 and out.any() and dec.any()
+""" % os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]
