@@ -17,8 +17,9 @@
 // One persistent CTA per SM runs through blocks, and every role runs ahead of
 // the slower ones as far as its buffers go, so that a block's loads and first
 // scores overlap the end of the one before. Warps 0-3 and 4-7: softmax of the
-// units; 8: TMA; 9: tensor core issue; 10: the values of the tiles that the
-// diagonal cuts (check_values); 11: the order of the blocks (Order).
+// units; 8: TMA; 9: tensor core issue; 10: the gate, which follows the loads and
+// checks the values of the tiles that the diagonal cuts (check_values); 11: the
+// order of the blocks (Order).
 #include "paged_internal.h"
 #include "tcgen05.cuh"
 #include "tensor_map.cuh"
@@ -45,7 +46,7 @@ struct Block {
 struct Shared {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], drain;
   uint64_t kv_full[8], kv_empty[8];    // by ring stage
-  uint64_t v_full[8], v_checked[8];    // by ring stage: values of a tile that the diagonal cuts
+  uint64_t v_full[8];                  // by ring stage: values of a tile that the diagonal cuts
   uint64_t block_full[2], block_empty[2];
   uint64_t fix_ready[2], fix_free[2];  // by parity of the block: `first` written, read
   uint64_t* last_load[8];              // the barrier of the last load into each stage, and its phase
@@ -88,13 +89,6 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* s
   const bool done = mbar_wait_bounded(bar, parity);
   if (!done) raise_status(status, kStatusTimeout);
   return __all_sync(0xffffffffu, done);
-}
-
-// Two barriers at once (the second may be NULL): one latency where both are done.
-__device__ __forceinline__ bool wait2(uint64_t* x, uint32_t px, uint64_t* y, uint32_t py, uint32_t* status) {
-  const bool dx = mbar_try_wait(x, px), dy = y == nullptr || mbar_try_wait(y, py);
-  if (__all_sync(0xffffffffu, dx && dy)) return true;
-  return wait(x, px, status) && (y == nullptr || wait(y, py, status));
 }
 
 // What all warps follow: the block's units and their key tiles.
@@ -470,7 +464,7 @@ __device__ __forceinline__ void mma_role(const PromptArgs& a, Shared* sh, unsign
   const unsigned char* ring = smem + 2 * C::kTile;
   const uint64_t dq = t5::smem_desc(smem_u32(smem), 16), dk = t5::smem_desc(smem_u32(ring), 16);
   const uint64_t dv = t5::smem_desc(smem_u32(ring), kRows * 128);
-  uint32_t q_phase = 0, p_phase[2] = {0, 0}, full_phase = 0, cut_phase = 0;
+  uint32_t q_phase = 0, p_phase[2] = {0, 0}, full_phase = 0;
   // S of unit u from the key tile in stage st
   auto scores = [&](int u, int st) {
     const uint64_t q = dq + (uint32_t)(u * C::kTile >> 4), k = dk + (uint32_t)(st * C::kTile >> 4);
@@ -506,13 +500,10 @@ __device__ __forceinline__ void mma_role(const PromptArgs& a, Shared* sh, unsign
     }
     for (int j = 0; j < un.most && ok; ++j) {
       const int sv = (i + 2 * j + 1) % C::kStages, sk = (i + 2 * j + 2) % C::kStages;
-      const bool more = j + 1 < un.most, cut = un.cut(j);
-      // this tile's values and the next one's keys
-      const uint32_t vp = ((cut ? cut_phase : full_phase) >> sv) & 1;
-      ok = wait2(cut ? &sh->v_checked[sv] : &sh->kv_full[sv], vp, more ? &sh->kv_full[sk] : nullptr,
-                 (full_phase >> sk) & 1, a.status);
-      if (cut) cut_phase ^= 1u << sv;
-      else full_phase ^= 1u << sv;
+      const bool more = j + 1 < un.most;
+      // p_full also says that this tile's values and the next one's keys are
+      // there (gate_role): their waits would cost the products' queue
+      if (!un.cut(j)) full_phase ^= 1u << sv;
       if (more) full_phase ^= 1u << sk;
       const uint64_t v = dv + (uint32_t)(sv * C::kTile >> 4);
 #pragma unroll
@@ -563,11 +554,13 @@ __device__ __forceinline__ void order_role(const PromptArgs& a, Shared* sh, Orde
   }
 }
 
+// Follows the loads and lets the products of each tile go on: its values and
+// the next tile's keys are there, and checked where the diagonal cuts the tile.
 template <int D, bool BF16>
-__device__ __forceinline__ void check_role(const PromptArgs& a, Shared* sh, unsigned char* ring, bool pair) {
+__device__ __forceinline__ void gate_role(const PromptArgs& a, Shared* sh, unsigned char* ring, bool pair) {
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
-  uint32_t cut_phase = 0;
+  uint32_t full_phase = 0, cut_phase = 0, p_phase[2] = {0, 0}, opened[2] = {0, 0};
   int i = 0;
   Block b;
   for (int it = 0; take_block(sh, it, a.status, b); ++it) {
@@ -581,13 +574,35 @@ __device__ __forceinline__ void check_role(const PromptArgs& a, Shared* sh, unsi
       if (lane == 0) sh->any_nonfinite[par] = 0;
     }
     __syncwarp();
-    for (int j = un.tiles[0] - 1; j < un.most; ++j) {
-      const int st = (i + 2 * j + 1) % C::kStages;
-      if (!wait(&sh->v_full[st], (cut_phase >> st) & 1, a.status)) return;
-      cut_phase ^= 1u << st;
-      check_values<D, BF16>(ring + st * C::kTile, j * kRows, sh->first[par], &sh->any_nonfinite[par]);
-      fence_proxy_async_smem();  // the tensor cores read what was written here
-      arrive(&sh->v_checked[st]);
+    // every phase of the ring is waited for, in order: a parity says no more
+    if (!wait(&sh->kv_full[i % C::kStages], (full_phase >> (i % C::kStages)) & 1, a.status)) return;
+    full_phase ^= 1u << (i % C::kStages);
+    for (int j = 0; j < un.most; ++j) {
+      const int sv = (i + 2 * j + 1) % C::kStages, sk = (i + 2 * j + 2) % C::kStages;
+      const bool cut = un.cut(j), more = j + 1 < un.most;
+      if (more) {
+        if (!wait(&sh->kv_full[sk], (full_phase >> sk) & 1, a.status)) return;
+        full_phase ^= 1u << sk;
+      }
+      if (cut) {
+        if (!wait(&sh->v_full[sv], (cut_phase >> sv) & 1, a.status)) return;
+        cut_phase ^= 1u << sv;
+        check_values<D, BF16>(ring + sv * C::kTile, j * kRows, sh->first[par], &sh->any_nonfinite[par]);
+        fence_proxy_async_smem();  // the tensor cores read what was written here
+      } else {
+        if (!wait(&sh->kv_full[sv], (full_phase >> sv) & 1, a.status)) return;
+        full_phase ^= 1u << sv;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (j >= un.tiles[u]) continue;
+        // one arrival a phase: the one before is complete
+        if (opened[u] && !wait(&sh->p_full[u], p_phase[u] ^ 1, a.status)) return;
+        opened[u] = 1;
+        p_phase[u] ^= 1;
+        if (lane == 0) arrive(&sh->p_full[u]);
+      }
     }
     arrive(&sh->fix_ready[par]);
     i += 2 * un.most;
@@ -617,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 128);
+      mbar_init(&sh.p_full[i], 129);  // the unit's threads, and the gate
       mbar_init(&sh.o_done[i], 1);
       mbar_init(&sh.block_full[i], 1);
       mbar_init(&sh.block_empty[i], 11);  // every warp but the one that fills it
@@ -629,7 +644,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.kv_full[i], 1);
       mbar_init(&sh.kv_empty[i], 1);
       mbar_init(&sh.v_full[i], 1);
-      mbar_init(&sh.v_checked[i], 32);
     }
     mbar_fence_init();
   }
@@ -652,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) load_role<D>(mq, mk, mv, a, &sh, smem, pair);
     else if (warp == 9) mma_role<D, BF16>(a, &sh, smem, pair);
-    else if (warp == 10) check_role<D, BF16>(a, &sh, smem + 2 * C::kTile, pair);
+    else if (warp == 10) gate_role<D, BF16>(a, &sh, smem + 2 * C::kTile, pair);
     else order_role(a, &sh, Order(nb, a.seqs, lots), span, pair);
   }
   __syncwarp();
