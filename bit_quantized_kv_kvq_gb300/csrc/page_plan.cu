@@ -7,6 +7,11 @@
 // requests, of m and of the growth, give every packed token its request and
 // position and every new page its place on the free stack, so everything after
 // the sums is independent per token and per page.
+//
+// A decode step reads and writes a few hundred bytes: latency, 5.4 us in a
+// graph for 16 requests. Many packed tokens go over the GPU (8 bytes written a
+// token, searched for four at a time): 262144 tokens of 1024 requests 7.3 us;
+// one cluster of eight CTAs took 20.5 us.
 #include "paged_internal.h"
 
 namespace kvq {

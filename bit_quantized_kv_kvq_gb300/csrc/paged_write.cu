@@ -8,6 +8,10 @@
 // every code written once. Rows of the page that came in earlier steps are in
 // the request's tail; the rows of the new open page go there, by the CTA of
 // the request's first item, which is the only one that reads that tail.
+//
+// Bound by bytes: 131072 fp16 tokens of 8 heads x 128 channels (805 MB) take
+// 128 us, 6.27 TB/s, 0.92 of the measured copy rate. With an IEEE division a
+// value it was bound by those (193 us); with 20 warps an SM by latency (151 us).
 #include "paged_internal.h"
 
 namespace kvq {
