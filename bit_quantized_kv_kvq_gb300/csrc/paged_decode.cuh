@@ -24,11 +24,11 @@
 // A (request, head) that one CTA covers is finished there; the others leave
 // partial sums, which a second kernel merges in the order of the CTAs.
 //
-// 16 requests of up to 131072 tokens, 8 kv-heads, 64 query heads (2.05 GB):
-// 275 us, the copy rate. 64 ragged requests up to 8192 tokens (0.54 GB): 96 us,
-// 0.83 of it; what is left are the ends of requests (tail, merge, the next
-// queries). 24 requests up to 2500 tokens, 32 heads of 64 channels (0.12 GB):
-// 32 us, 0.56. One request of 777 tokens: 8.7 us, latency of two launches.
+// 16 requests of up to 131072 tokens, 8 kv-heads, 64 query heads (1.84 GB):
+// 275 us, 0.98 of the copy rate. 64 ragged requests up to 8192 tokens (0.51
+// GB): 96 us, 0.78 of it; what is left are the ends of requests (tail, merge,
+// the next queries). 24 requests up to 2500 tokens, 32 heads of 64 channels
+// (0.115 GB): 32 us, 0.53. One request of 777 tokens: 8.7 us, latency of two launches.
 // Loads straight into the fragments' registers, without a ring, took 292, 101,
 // 39 and 8.5 us.
 #pragma once
