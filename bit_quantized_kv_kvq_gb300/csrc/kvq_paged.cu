@@ -47,7 +47,7 @@ kvq_status check_config(const kvq_paged_config* c) {
   if (c->max_pages < 1 || (int64_t)c->max_pages * c->page_tokens > INT32_MAX - 255)  // tile ends stay 32-bit
     return fail(KVQ_ERR_INVALID_ARG, "max_pages %d must be >= 1 and max_pages * page_tokens at most 2^31 - 256",
                 c->max_pages);
-  if ((int64_t)c->max_requests * (((int64_t)c->max_pages * c->page_tokens + 63) / 64 + 6) > INT32_MAX)
+  if ((int64_t)c->max_requests * (((int64_t)c->max_pages * c->page_tokens + 63) / 64 + 5) > INT32_MAX)
     return fail(KVQ_ERR_UNSUPPORTED, "max_requests %d times max_pages %d is too large to plan a decode", c->max_requests,
                 c->max_pages);
   if ((int64_t)c->num_pages * c->num_kv_heads * 2 > INT32_MAX)  // the code tiles' index

@@ -16,7 +16,7 @@
 // kernel makes the line from the device lengths itself, so the grid needs no
 // host knowledge and ragged batches stay even. A (request, head) has kExtra
 // more places on the line than tiles, for what its begin, tail and merge cost
-// (5000 to 10000 clocks against 1300 to 1600 a tile): without them a CTA that
+// (4000 to 8000 clocks against 1300 to 1600 a tile): without them a CTA that
 // got fourteen one-tile requests took three times as long as the others. A producer warp walks the
 // range and keeps a ring of tiles in flight by TMA, on into the next request
 // or head while the four consumer warps still merge the last one; these take
@@ -26,7 +26,7 @@
 //
 // 16 requests of up to 131072 tokens, 8 kv-heads, 64 query heads (1.84 GB):
 // 275 us, 0.98 of the copy rate. 64 ragged requests up to 8192 tokens (0.51
-// GB): 96 us, 0.78 of it; what is left are the ends of requests (tail, merge,
+// GB): 91 us, 0.82 of it; what is left are the ends of requests (tail, merge,
 // the next queries). 24 requests up to 2500 tokens, 32 heads of 64 channels
 // (0.115 GB): 32 us, 0.53. One request of 777 tokens: 8.7 us, latency of two launches.
 // Loads straight into the fragments' registers, without a ring, took 292, 101,
@@ -48,7 +48,7 @@ __host__ __device__ constexpr int sub_of(int dim) { return 128 / dim; }
 __host__ __device__ constexpr int unit_of(int dim) { return kWarps * 16 * sub_of(dim); }
 
 // Places on the line before a (request, head)'s tiles.
-constexpr int kExtra = 6;
+constexpr int kExtra = 5;
 
 // Heads of one pass over the codes: 8 NT (NT column tiles of the products).
 __host__ __device__ constexpr int nt_of(int group) { return group <= 8 ? 1 : 2; }
@@ -74,6 +74,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                                          uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma16816_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -118,10 +126,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Exponent k with max |x| * 2^k in [2^14, 2^15), from the bits of max |x| in
-// bf16: rows in bf16 go to the fp16 products scaled by 2^k. That is exact but
-// for elements below 2^-29 of the row's largest, whose rounding (2^-40 of it)
-// is far below the fp32 sums' own.
+// bf16: bf16 queries go to the fp16 products with the codes scaled by 2^k. That
+// is exact but for elements below 2^-29 of the query's largest, whose rounding
+// (2^-40 of it) is far below the fp32 sums' own.
 __device__ __forceinline__ int bf16_shift(uint32_t top_bits) {
   const int k = 14 - ((int)(top_bits >> 7) - 127);
   return k > 100 ? 100 : k;
@@ -198,17 +212,16 @@ struct Warp {
     }
   }
 
-  // Weights of 16 tokens from their scores s (c0, c1: token g; c2, c3: token
-  // g + 8), as the B operand of P^T. fa, fb: factors of the two token rows.
-  __device__ __forceinline__ void weights(float (&s)[NT][4], float fa, float fb, bool va, bool vb,
-                                          uint32_t (&p)[NT][2]) {
+  // Scores s of 16 tokens (c0, c1: token g; c2, c3: token g + 8) to their
+  // weights; q f: the heads' factors. va, vb: whether the two tokens count.
+  __device__ __forceinline__ void weights(float (&s)[NT][4], const float (&q)[NT][2], float f0, bool va, bool vb) {
     bool up = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        s[nt][i] = va ? s[nt][i] * (qs[nt][i] * fa) : -INFINITY;
-        s[nt][2 + i] = vb ? s[nt][2 + i] * (qs[nt][i] * fb) : -INFINITY;
+        s[nt][i] = va ? s[nt][i] * (q[nt][i] * f0) : -INFINITY;
+        s[nt][2 + i] = vb ? s[nt][2 + i] * (q[nt][i] * f0) : -INFINITY;
         up |= fmaxf(s[nt][i], s[nt][2 + i]) > m[nt][i] + 8.0f;
       }
     }
@@ -240,6 +253,12 @@ struct Warp {
         s[nt][2 + i] = exp2_fast(s[nt][2 + i] - ref);
         l[nt][i] += s[nt][i] + s[nt][2 + i];
       }
+    }
+  }
+  // ... as the B operand of P^T in fp16.
+  __device__ __forceinline__ void half_weights(const float (&s)[NT][4], uint32_t (&p)[NT][2]) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       p[nt][0] = movmatrix(pack_h2(s[nt][0], s[nt][1]));
       p[nt][1] = movmatrix(pack_h2(s[nt][2], s[nt][3]));
     }
@@ -318,88 +337,83 @@ struct Warp {
     }
   }
 
-  // 16 rows of the tail, `live` of them cached: the same products on the
-  // input type's rows. k, v: the tail's rows at the first of them.
-  __device__ __forceinline__ void tail_rows(const uint16_t* k, const uint16_t* v, int live) {
+  // 16 rows of the tail, `live` of them cached: the same products on the input
+  // type's rows (qf: the queries as they lie). In bf16 a weight goes as the sum
+  // of two bf16 numbers, 2^-16 of it off. k, v: the tail's rows at the first.
+  __device__ __forceinline__ void tail_rows(const uint16_t* k, const uint16_t* v, int live, float scale_log2) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    float s[NT][4];
-    float f[2] = {1.0f, 1.0f};
-    uint32_t kw[2][kChunks][8];
+    float s[NT][4], q[NT][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = g + 8 * r;
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const uint4* src = reinterpret_cast<const uint4*>(k + row * D + (c * 4 + t) * 16);
-        const uint4 x = row < live ? src[0] : zero, y = row < live ? src[1] : zero;
-        kw[r][c][0] = x.x, kw[r][c][1] = x.y, kw[r][c][2] = x.z, kw[r][c][3] = x.w;
-        kw[r][c][4] = y.x, kw[r][c][5] = y.y, kw[r][c][6] = y.z, kw[r][c][7] = y.w;
-      }
-    }
-    if (BF16) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) top = abs_max2(top, kw[r][c][i]);
-        top = both_halves(top);
-        top = max(top, __shfl_xor_sync(kFull, top, 1));
-        top = max(top, __shfl_xor_sync(kFull, top, 2));
-        const int e = bf16_shift(top);
-        const float up = exp2i(e);
-        f[r] = exp2i(-e);
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) kw[r][c][i] = bf2_to_h2(kw[r][c][i], up);
-      }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      q[nt][0] = q[nt][1] = scale_log2;
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[nt][r] = 0.0f;
+    }
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
+    for (int c = 0; c < kChunks; ++c) {
+      uint4 x[2][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int r = 0; r < 2; ++r) {
+        const uint4* src = reinterpret_cast<const uint4*>(k + (g + 8 * r) * D + (c * 4 + t) * 16);
+        x[r][0] = g + 8 * r < live ? src[0] : zero;
+        x[r][1] = g + 8 * r < live ? src[1] : zero;
+      }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma16816(s[nt], kw[0][c][2 * i], kw[1][c][2 * i], kw[0][c][2 * i + 1], kw[1][c][2 * i + 1],
-                   qf[nt][c * 4 + i][0], qf[nt][c * 4 + i][1]);
-    uint32_t p[NT][2];
-    weights(s, f[0], f[1], g < live, g + 8 < live, p);
-    uint32_t vw[4][D / 16];
+      for (int i = 0; i < 4; ++i) {
+        const uint4 a = x[0][i >> 1], b = x[1][i >> 1];
+        const uint32_t a0 = i & 1 ? a.z : a.x, a2 = i & 1 ? a.w : a.y, a1 = i & 1 ? b.z : b.x, a3 = i & 1 ? b.w : b.y;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 2 * t + (r & 1) + (r >> 1) * 8;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const uint4 x = row < live ? reinterpret_cast<const uint4*>(v + row * D + g * (D / 8))[c] : zero;
-        vw[r][4 * c] = x.x, vw[r][4 * c + 1] = x.y, vw[r][4 * c + 2] = x.z, vw[r][4 * c + 3] = x.w;
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t b0 = qf[nt][c * 4 + i][0], b1 = qf[nt][c * 4 + i][1];
+          if (BF16) mma16816_bf16(s[nt], a0, a1, a2, a3, b0, b1);
+          else mma16816(s[nt], a0, a1, a2, a3, b0, b1);
+        }
       }
     }
-    uint32_t top = 0;
+    weights(s, q, 1.0f, g < live, g + 8 < live);
+    uint32_t p[NT][2], pl[NT][2];
+    if (BF16) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) top = abs_max2(top, vw[r][i]);
-    float sv = 1.0f;
-    if (BF16) {  // one power of two for the 16 rows
-      const int e = bf16_shift(__reduce_max_sync(kFull, both_halves(top)));
-      const float up = exp2i(e);
-      sv = exp2i(-e);
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) vw[r][i] = bf2_to_h2(vw[r][i], up);
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t hi = pack_bf2(s[nt][2 * r], s[nt][2 * r + 1]);
+          p[nt][r] = movmatrix(hi);
+          pl[nt][r] = movmatrix(pack_bf2(s[nt][2 * r] - __uint_as_float(hi << 16),
+                                         s[nt][2 * r + 1] - __uint_as_float(hi & 0xffff0000u)));
+        }
+    } else {
+      half_weights(s, p);
     }
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j)  // channels 2 j and 2 j + 1 of the lane's D / 8
-      add_pv(j, sv, __byte_perm(vw[0][j], vw[1][j], 0x5410), __byte_perm(vw[0][j], vw[1][j], 0x7632),
-             __byte_perm(vw[2][j], vw[3][j], 0x5410), __byte_perm(vw[2][j], vw[3][j], 0x7632), p);
+    for (int c = 0; c < D / 64; ++c) {
+      uint4 x[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 2 * t + (r & 1) + (r >> 1) * 8;
+        x[r] = row < live ? reinterpret_cast<const uint4*>(v + row * D + g * (D / 8))[c] : zero;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // channels 2 j and 2 j + 1 of the lane's D / 8
+        const int j = 4 * c + i;
+        const uint32_t w0 = i == 0 ? x[0].x : i == 1 ? x[0].y : i == 2 ? x[0].z : x[0].w;
+        const uint32_t w1 = i == 0 ? x[1].x : i == 1 ? x[1].y : i == 2 ? x[1].z : x[1].w;
+        const uint32_t w2 = i == 0 ? x[2].x : i == 1 ? x[2].y : i == 2 ? x[2].z : x[2].w;
+        const uint32_t w3 = i == 0 ? x[3].x : i == 1 ? x[3].y : i == 2 ? x[3].z : x[3].w;
+        const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
+        const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (BF16) {
+            mma16816_bf16(o[nt][j], a0, a1, a2, a3, p[nt][0], p[nt][1]);
+            mma16816_bf16(o[nt][j], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+          } else {
+            mma16816(o[nt][j], a0, a1, a2, a3, p[nt][0], p[nt][1]);
+          }
+        }
+      }
+    }
   }
 };
 
@@ -649,13 +663,15 @@ __global__ void __launch_bounds__(kThreads + 32, ctas_per_sm(NT))
         float s[NT][4];
         uint32_t pb[NT][2];
         w.scores(kr[j], s);
-        w.weights(s, sc[j].x, sc[j].x, true, true, pb);
+        w.weights(s, w.qs, sc[j].x, true, true);
+        w.half_weights(s, pb);
         w.values(vr[j], sc[j].y, pb);
       }
     }
+    if (BF16 && tail0 < tail_end) load_q(cur);  // the products with the codes had them scaled
     for (int tk = tail0; tk < tail_end; tk += 16)
       if (tk % kUnit / (16 * kSub) == warp)
-        w.tail_rows(tail + (tk - full) * D, tail + (tk - full + P) * D, min(16, len - tk));
+        w.tail_rows(tail + (tk - full) * D, tail + (tk - full + P) * D, min(16, len - tk), a.scale_log2);
 
     // the four warps' sums; the next part's queries are on their way meanwhile
     const Part done = cur;
