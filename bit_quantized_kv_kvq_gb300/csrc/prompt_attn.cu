@@ -27,7 +27,7 @@
 // softmax, weights to the products, 500 of hand-overs) is as long. Eight
 // prompts of 1024 tokens: 74 us (930 TFLOP/s): the ends of blocks, where both
 // units write their rows, and half of every tile on the diagonal. With 64
-// channels per head the softmax is the longer part: 8192 tokens 285 us (970).
+// channels per head the softmax is the longer part: 8192 tokens 290 us (950).
 #include "paged_internal.h"
 #include "tcgen05.cuh"
 #include "tensor_map.cuh"

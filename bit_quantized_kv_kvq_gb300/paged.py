@@ -238,7 +238,12 @@ class PagedKVCache:
         elif tuple(out.shape) != (r, hq, d) or out.device != dev or not out.is_contiguous() or out.dtype not in _DTYPES:
             raise ValueError("out must be a contiguous tensor of shape %s on %s" % ((r, hq, d), dev))
         raw = _raw_stream(stream, dev)
-        ws = self._workspace(hq, raw, stream) if workspace is None else workspace
+        if workspace is None:
+            ws = self._workspace(hq, raw, stream)
+        else:
+            ws = workspace
+            if not isinstance(ws, _Tensor) or ws.device != dev or not ws.is_contiguous():
+                raise TypeError("workspace must be a contiguous tensor on %s" % dev)
         _check(lib.kvq_paged_decode_attention(
             self.handle, layer, r, qp, qs, hq, _ints(table, "table", (r, self._table_pages), dev),
             _ints(lens, "lens", (r,), dev), softmax_scale, out.data_ptr(), _DTYPES[out.dtype], ws.data_ptr(), ws.nbytes,

@@ -315,13 +315,27 @@ def test_arguments_are_checked():
         with pytest.raises(kvq.KVQError):
             bad()
     for bad in (lambda: c.decode(0, q.float(), s.table, s.lens, 0.1), lambda: c.decode(0, q, s.table.long(), s.lens, 0.1),
-                lambda: c.decode(0, q.cpu(), s.table, s.lens, 0.1)):
+                lambda: c.decode(0, q.cpu(), s.table, s.lens, 0.1),
+                lambda: c.decode(0, q, s.table, s.lens, 0.1, workspace=torch.empty(1 << 24, dtype=torch.uint8))):
         with pytest.raises(TypeError):
             bad()
     for bad in (lambda: c.decode(0, q, s.table[:, :2], s.lens, 0.1), lambda: c.decode(0, q, s.table, s.lens[:1], 0.1),
                 lambda: c.decode(0, q.transpose(0, 1), s.table, s.lens, 0.1)):
         with pytest.raises(ValueError):
             bad()
+    k, ok = s.rows(4, 2).cuda(), lambda *n: ints(np.zeros(n))
+    for bad in (lambda: c.write(1, k, k, ok(3), ok(4), s.lens), lambda: c.write(-1, k, k, ok(3), ok(4), s.lens),
+                lambda: c.reserve(ok(3), ok(3), ok(3, 4), ok(9), ok(1), 4),       # more requests than slots
+                lambda: c.release(ok(3), ok(3), ok(3, 4), ok(9), ok(1))):
+        with pytest.raises(kvq.KVQError):
+            bad()
+    for bad in (lambda: c.write(0, k, k[:3], ok(3), ok(4), s.lens), lambda: c.write(0, k, k, ok(3), ok(3), s.lens),
+                lambda: c.reserve(ok(2), ok(3), ok(2, 4), ok(9), ok(1), 4), lambda: c.reserve(ok(2), ok(2), ok(2, 5), ok(9), ok(1), 4),
+                lambda: c.reserve(ok(2), ok(2), ok(2, 4), ok(8), ok(1), 4), lambda: c.reserve(ok(2), ok(2), ok(2, 4), ok(9), ok(1), -1)):
+        with pytest.raises(ValueError):
+            bad()
+    c.write(0, k[:0], k[:0], ok(3), ok(0), s.lens)  # nothing to write
+    c.reserve(s.lens, ok(2), s.table, s.free, s.count, 0)
     assert c.status() == 0
 
 
