@@ -157,6 +157,7 @@ struct Warp {
   static constexpr int kSteps = D / 16;   // k-steps of S, row tiles of O
   static constexpr int kChunks = D / 64;  // 16-byte chunks of a key row per lane
   static constexpr int kVw = D / 32;      // words of a value row per lane
+  static constexpr float kLift = 7.0f;
   uint32_t qf[NT][kSteps][2];
   float o[NT][kSteps][4];
   float m[NT][2], l[NT][2], qs[NT][2];  // heads 2 t4, 2 t4 + 1 of the column tile
@@ -222,11 +223,13 @@ struct Warp {
       for (int i = 0; i < 2; ++i) {
         s[nt][i] = va ? s[nt][i] * (q[nt][i] * f0) : -INFINITY;
         s[nt][2 + i] = vb ? s[nt][2 + i] * (q[nt][i] * f0) : -INFINITY;
-        up |= fmaxf(s[nt][i], s[nt][2 + i]) > m[nt][i] + 8.0f;
+        up |= fmaxf(s[nt][i], s[nt][2 + i]) - m[nt][i] > kLift + 8.0f;
       }
     }
-    // The reference of the exponentials moves only when a score passes it by
-    // 8: weights stay below 2^8, and most tiles skip the reduction.
+    // The reference of the exponentials lies kLift below a score and moves only
+    // when one passes that by 8: most tiles skip the reduction, weights stay
+    // below 2^15, and those of 2^-21 of it and more above fp16's subnormal numbers
+    // (below, many small weights beside a large one would be off to one side).
     if (__any_sync(kFull, up)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -236,9 +239,10 @@ struct Warp {
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-          const bool mine = x > m[nt][i] + 8.0f;  // each head by its own scores
-          const float f = mine ? exp2_fast(m[nt][i] - x) : 1.0f;
-          m[nt][i] = mine ? x : m[nt][i];
+          const bool mine = x - m[nt][i] > kLift + 8.0f;  // each head by its own scores
+          const float now = mine ? x - kLift : m[nt][i];
+          const float f = mine ? exp2_fast(m[nt][i] - now) : 1.0f;
+          m[nt][i] = now;
           l[nt][i] *= f;
 #pragma unroll
           for (int j = 0; j < kSteps; ++j) o[nt][j][i] *= f, o[nt][j][2 + i] *= f;

@@ -487,8 +487,8 @@ KVQ_API kvq_status kvq_paged_decode_workspace_bytes(const kvq_paged_cache* cache
  * q: [requests][H_q][D] in the config's dtype, rows q_stride elements apart (a
  * multiple of 8, >= H_q * D); H_q any multiple of H_kv. out: [requests][H_q][D] in
  * out_dtype (KVQ_F32 or the config's dtype); a request with lens[b] == 0 gets
- * zeros. The sums are fp32 and normalised at the end: tokens * 256 * |v| must stay
- * below 3e38 (here and in kvq_prompt_attention). The tiles of all requests are cut into equal ranges by the kernel
+ * zeros. The sums are fp32 and normalised at the end: tokens * 2^15 * |v| must stay
+ * below 3e38 (tokens * 2^8 * |v| in kvq_prompt_attention). The tiles of all requests are cut into equal ranges by the kernel
  * from lens, so the grid does not depend on the lengths. workspace: 16-byte
  * aligned, any content, not shared with calls that overlap on the GPU. Two
  * launches (the second merges the ranges' partial sums in a fixed order). */

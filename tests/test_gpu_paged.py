@@ -523,3 +523,41 @@ def test_write_takes_the_rows_after_others():
     other = kvq.PagedKVCache(1, 1, 1, 64, 16, 4, 4)
     other.write(0, x[60:], x[60:], ints([0, 40]), ints(np.arange(40)), ints([40]))
     assert torch.equal(cache.buffer, other.buffer) and cache.status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+def test_many_small_weights_beside_a_large_one(dtype, d, code):
+    """A first token of e^14.125 times the weight of each other one, which hold
+    the values: in pages and in the tail their weights keep 11 bits."""
+    for t in (3000, 50):  # tokens in pages and a tail, in the tail alone
+        s = Served(1, 1, d, 64, code, dtype, 3100)
+        k, v = torch.zeros(t, 1, d, dtype=dtype), torch.ones(t, 1, d, dtype=dtype)
+        k[0, 0, 0], v[0] = 14.125, 0
+        s.step([t], k=k, v=v)
+        q = torch.zeros(1, 1, d, dtype=dtype)
+        q[0, 0, 0] = 1
+        o = s.cache.decode(0, q.cuda(), s.table, s.lens, 1.0, out_dtype=torch.float32).double()
+        n = (t - 1) * math.exp(-14.125)
+        # half a step of fp16, and what the codes' scales, exponentials and fp32 sums add
+        assert ((o - n / (1 + n)).abs() <= (2.0 ** -11 + 2.0 ** -14) * 1.01 * n).all(), t
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,top", [(F16, 61440.0), (BF16, 2.0 ** 55)])
+def test_scores_of_any_size(dtype, top, d):
+    """Equal scores far past where a last place of theirs is worth a weight."""
+    t = 333
+    s = Served(1, 1, d, 64, "int8", dtype, 400)
+    s.step([t], k=torch.full((t, 1, d), top, dtype=dtype), v=s.rows(t, 1))
+    kv = s.oracle.values(0, s.table.cpu().numpy()[0])[1, 0]
+    for sign in (1, -1):
+        q = torch.full((1, 1, d), sign * top, dtype=dtype)
+        o = s.cache.decode(0, q.cuda(), s.table, s.lens, 0.1, out_dtype=torch.float32)[0, 0].double().cpu().numpy()
+        assert np.isfinite(o).all()
+        # the pages' keys read back as code * scale, within 2^-23 of the tail's:
+        # at these sizes one or the other has all the weight
+        near = [kv[:t // 64 * 64].mean(0), kv[t // 64 * 64:].mean(0), kv.mean(0)]
+        tol = (2.0 ** -11 + 2.0 ** -14) * np.abs(kv).mean(0) * 2
+        assert any((np.abs(o - x) <= tol).all() for x in near)
