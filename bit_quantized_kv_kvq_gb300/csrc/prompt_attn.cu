@@ -222,15 +222,15 @@ __device__ __forceinline__ void check_values(unsigned char* tile, int k0, int (*
   }
 }
 
-// 2 N scores of a row to weights: p = 2^(s sc - ref), packed, and their sum.
+// 2 N scores of a row to weights: p = 2^(s sc - off), packed, and their sum.
 template <bool BF16, int N>
-__device__ __forceinline__ uint64_t to_weights(const uint32_t* s, uint64_t sc2, float ref, uint32_t* p) {
-  const uint64_t ref2 = f2_pack(-ref, -ref);
+__device__ __forceinline__ uint64_t to_weights(const uint32_t* s, uint64_t sc2, float off, uint32_t* p) {
+  const uint64_t off2 = f2_pack(-off, -off);
   uint64_t sum0 = f2_pack(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     float x, y;
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, ref2), x, y);
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, off2), x, y);
     x = exp2_fast(x);
     y = exp2_fast(y);
     if (i & 1) sum1 = f2_add(sum1, f2_pack(x, y));
@@ -253,27 +253,65 @@ __device__ __forceinline__ float max_of(const uint32_t* s) {
   return fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
 }
 
-// The reference m of a row's exponentials moves only when a score passes it by
-// 8 (weights stay below 2^8), so that few tiles scale O (o: it has a value).
-// Each row goes by its own scores: its bits do not depend on its neighbours.
-template <int D>
-__device__ __forceinline__ void raise_reference(float top, float& m, float& l, uint32_t tO, bool o) {
-  const bool up = top > m + 8.0f;
-  if (!__any_sync(0xffffffffu, up)) return;
-  const float f = up ? exp2_fast(m - top) : 1.0f;
-  m = up ? top : m;
-  l *= f;
-  if (!o) return;
-#pragma unroll 1
-  for (int c = 0; c < D; c += 32) {
-    uint32_t x[32];
-    t5::ld32(tO + c, x);
-    t5::wait_ld32(x);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-    t5::st32(tO + c, x);
+// The reference of a row's exponentials moves only when a score passes it by 8
+// in units of log 2, so that few tiles scale O (o: it has a value). Each row goes
+// by its own scores: its bits do not depend on its neighbours.
+//
+// A weight is 2^(s sc - m), one multiply-add, with m = raw sc - lift rounded.
+// In fp16 the lift of 7 puts weights below 2^15 and 2^-21 of the reference's
+// above the type's subnormal numbers (below those, many small weights beside a
+// large one would all be off to the same side); bf16 needs none. m's rounding is
+// a factor that all weights of the row share, but among scores past 2^20 it
+// grows without limit: such a row subtracts `raw` from its scores first (`sub`),
+// which is exact near the largest ones. `far`: a row of the warp does.
+template <int D, bool BF16>
+struct Reference {
+  static constexpr float kLift = BF16 ? 0.0f : 7.0f;
+  float sc, raw, m, sub, off;  // off: what to_weights takes off the scaled scores
+  bool far;
+
+  __device__ __forceinline__ void reset(float sc_) {
+    sc = sc_;
+    raw = m = -INFINITY;
+    sub = off = 0.0f;
+    far = false;
   }
-}
+  // what m's rounding added, of a row that does not subtract
+  __device__ __forceinline__ float rounding() const { return fabsf(m) <= 0x1p20f ? fmaf(raw, sc, -m) - kLift : 0.0f; }
+
+  __device__ __forceinline__ void raise(float top, float& l, uint32_t tO, bool o) {
+    const bool up = (top - raw) * sc > 8.0f;
+    if (!__any_sync(0xffffffffu, up)) return;
+    float f = 1.0f;
+    if (up) {
+      f = (raw - top) * sc - rounding();
+      raw = top;
+      m = fmaf(raw, sc, -kLift);
+      f = exp2_fast(f + rounding());
+      const bool own = !(fabsf(m) <= 0x1p20f);
+      sub = own ? raw : 0.0f;
+      off = own ? -kLift : m;
+    }
+    far = __any_sync(0xffffffffu, sub != 0.0f);
+    l *= f;
+    if (!o) return;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      uint32_t x[32];
+      t5::ld32(tO + c, x);
+      t5::wait_ld32(x);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+      t5::st32(tO + c, x);
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void subtract(uint32_t* s) const {
+    if (!far) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) - sub);
+  }
+};
 
 // 64 bytes of an output row: whole 32-byte sectors where `out` is so aligned.
 __device__ __forceinline__ void store_row(uint16_t* to, const uint32_t* w, bool wide) {
@@ -296,15 +334,16 @@ __device__ __forceinline__ void softmax_role(const PromptArgs& a, Shared* sh, co
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, r = warp * 32 + lane;
   const uint32_t lanes = sh->tmem + ((uint32_t)(warp * 32) << 16);
   const uint32_t tS = lanes + unit * 128, tP = tS, tO = lanes + 256 + unit * D;
-  const float sc = a.scale_log2;
-  const uint64_t sc2 = f2_pack(sc, sc);
+  const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2);
+  Reference<D, BF16> ref;
   const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   uint32_t tile_phase = 0, out_phase = 0;
   Block b;
   for (int it = 0; take_block(sh, it, a.status, b); ++it) {
     const Units un(b, pair);
     const int tiles = unit ? un.tiles[1] : un.tiles[0], row = (unit ? un.row0[1] : un.row0[0]) + r;
-    float m = -INFINITY, l = 0.0f;
+    ref.reset(a.scale_log2);
+    float l = 0.0f;
     for (int j = 0; j < tiles; ++j, tile_phase ^= 1) {
       if (!wait(&sh->s_full[unit], tile_phase, a.status)) return;
       t5::fence_after();
@@ -315,11 +354,11 @@ __device__ __forceinline__ void softmax_role(const PromptArgs& a, Shared* sh, co
         for (int c = 0; c < 4; ++c) t5::ld32(tS + 32 * c, s + 32 * c);
 #pragma unroll
         for (int c = 0; c < 4; ++c) t5::wait_ld32(s + 32 * c);
-        raise_reference<D>(max_of<128>(s) * sc, m, l, tO, j > 0);  // s_full came after the last PV
-        const float ref = m == -INFINITY ? 0.0f : m;
-        sum = to_weights<BF16, 32>(s, sc2, ref, p);
+        ref.raise(max_of<128>(s), l, tO, j > 0);  // s_full came after the last PV
+        ref.template subtract<128>(s);
+        sum = to_weights<BF16, 32>(s, sc2, ref.off, p);
         t5::st32(tP, p);
-        sum = f2_add(sum, to_weights<BF16, 32>(s + 64, sc2, ref, p));
+        sum = f2_add(sum, to_weights<BF16, 32>(s + 64, sc2, ref.off, p));
         t5::st32(tP + 32, p);
       } else {
         // The tile the diagonal cuts, by groups of 32 keys: the warp's rows see
@@ -338,8 +377,7 @@ __device__ __forceinline__ void softmax_role(const PromptArgs& a, Shared* sh, co
           }
           top = fmaxf(top, max_of<32>(s));
         }
-        raise_reference<D>(top * sc, m, l, tO, j > 0);
-        const float ref = m == -INFINITY ? 0.0f : m;
+        ref.raise(top, l, tO, j > 0);
         sum = f2_pack(0.0f, 0.0f);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -352,7 +390,8 @@ __device__ __forceinline__ void softmax_role(const PromptArgs& a, Shared* sh, co
               for (int i = 0; i < 32; ++i)
                 if (i > lane) s[i] = 0xff800000u;
             }
-            sum = f2_add(sum, to_weights<BF16, 16>(s, sc2, ref, p));
+            ref.template subtract<32>(s);
+            sum = f2_add(sum, to_weights<BF16, 16>(s, sc2, ref.off, p));
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) p[i] = 0u;

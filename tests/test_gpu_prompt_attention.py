@@ -286,3 +286,72 @@ assert cache.status() == 0 and plan.lens.tolist() == [40, 40] and count.item() =
 """ % os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert p.returncode == 0, p.stderr[-2000:]
+
+
+def near(o, ref, w, dtype, extra=2.0 ** -14):
+    """Weights and the output rounded to the type, fp32 sums (extra covers both
+    exponentials and sums); no score rounds in the cases that call this."""
+    half = torch.finfo(dtype).eps / 2
+    err, tol = (o.double() - ref).abs(), (half + extra) * 1.01 * w + half * ref.abs()
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,top", [(F16, 256.0), (F16, 4096.0), (F16, 61440.0), (BF16, 2.0 ** 20), (BF16, 2.0 ** 55)])
+def test_scores_of_any_size(dtype, top, d):
+    """Scores far past where a last place of theirs is worth a weight: equal
+    ones share the output, larger ones take it over."""
+    t = 450
+    v = torch.randn(t, 1, d, generator=torch.Generator().manual_seed(6)).to(dtype).cuda()
+    q = torch.full((t, 1, d), top, dtype=dtype, device="cuda")
+    k = torch.full((t, 1, d), top / 2, dtype=dtype, device="cuda")
+    k[[150, 333]] = top
+    c = 1 / math.sqrt(d)
+    n = torch.arange(1, t + 1, device="cuda").double()[:, None, None]
+    mean, size = v.double().cumsum(0) / n, v.double().abs().cumsum(0) / n
+    ref, w = mean.clone(), size.clone()
+    ref[150:333], w[150:333] = v[150].double(), v[150].double().abs()
+    ref[333:] = (v[150].double() + v[333].double()) / 2
+    w[333:] = (v[150].double().abs() + v[333].double().abs()) / 2
+    near(kvq.prompt_attention(q, k, v, ints([0, t]), c), ref, w, dtype)
+    k[:] = top  # lowest scores, all equal
+    near(kvq.prompt_attention(-q, k, v, ints([0, t]), c), mean, size, dtype)
+
+
+@pytest.mark.parametrize("base", [726812.0 - 6000, 726812.0, 726812.0 + 6000, -726816.0, 0.0])
+def test_a_raise_among_large_scores(base):
+    """Scores (exact sums) that differ by 6 around 2^20 in units of log 2: both
+    kinds of token weigh in."""
+    t, d = 400, 64
+    v = torch.randn(t, 1, d, generator=torch.Generator().manual_seed(7)).half().cuda()
+    q = torch.zeros(t, 1, d, dtype=F16, device="cuda")
+    k = torch.zeros_like(q)
+    q[:, 0, 0], q[:, 0, 1] = 1024, 1
+    raw = torch.full((t,), base, dtype=torch.float64, device="cuda")
+    raw[[130, 300]] += 6
+    raw[390] += 12
+    hi = (raw / 1024).floor()
+    k[:, 0, 0], k[:, 0, 1] = hi.half(), (raw - 1024 * hi).half()
+    assert torch.equal((q.double() * k.double()).sum(2)[:, 0], raw)
+    p = torch.softmax((raw[None] - base).expand(t, t).masked_fill(torch.ones(t, t, device="cuda").bool().triu(1), float("-inf")), 1)
+    ref = torch.einsum("ij,jhd->ihd", p, v.double())
+    w = torch.einsum("ij,jhd->ihd", p, v.double().abs())
+    near(kvq.prompt_attention(q, k, v, ints([0, t]), 1.0), ref, w, F16)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_many_small_weights_beside_a_large_one(dtype, d):
+    """A first token of e^14.125 times the weight of each other one, which hold
+    the values: their weights keep the type's precision."""
+    t = 3000
+    q = torch.zeros(t, 1, d, dtype=dtype, device="cuda")
+    k, v = torch.zeros_like(q), torch.ones_like(q)
+    q[:, 0, 0], k[0, 0, 0], v[0] = 1, 14.125, 0
+    n = torch.arange(t, device="cuda").double()[:, None, None] * math.exp(-14.125)
+    ref = (n / (1 + n)).expand(t, 1, d)
+    o = kvq.prompt_attention(q, k, v, ints([0, t]), 1.0)
+    # an output below the type's normal range rounds by half its smallest step
+    step = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    half = torch.finfo(dtype).eps / 2
+    assert ((o.double() - ref).abs() <= (2 * half + 2.0 ** -14) * 1.01 * ref + step / 2).all()
