@@ -21,13 +21,13 @@
 // checks the values of the tiles that the diagonal cuts (check_values); 11: the
 // order of the blocks (Order).
 //
-// One prompt of 16384 tokens, 32/8 heads of 128: 1305 us, 1685 TFLOP/s, 0.89 of
+// One prompt of 16384 tokens, 32/8 heads of 128: 1315 us, 1672 TFLOP/s, 0.88 of
 // the measured bf16 rate. A key tile takes a pair of units 2700 to 3000 clocks,
 // of which the products are 2060; a unit's own chain (scores, 1200 clocks of
 // softmax, weights to the products, 500 of hand-overs) is as long. Eight
-// prompts of 1024 tokens: 74 us (930 TFLOP/s): the ends of blocks, where both
+// prompts of 1024 tokens: 75 us (912 TFLOP/s): the ends of blocks, where both
 // units write their rows, and half of every tile on the diagonal. With 64
-// channels per head the softmax is the longer part: 8192 tokens 290 us (950).
+// channels per head the softmax is the longer part: 8192 tokens 293 us (939).
 #include "paged_internal.h"
 #include "tcgen05.cuh"
 #include "tensor_map.cuh"
@@ -279,8 +279,15 @@ struct Reference {
   // what m's rounding added, of a row that does not subtract
   __device__ __forceinline__ float rounding() const { return fabsf(m) <= 0x1p20f ? fmaf(raw, sc, -m) - kLift : 0.0f; }
 
-  __device__ __forceinline__ void raise(float top, float& l, uint32_t tO, bool o) {
+  // s: N scores of the row to subtract from
+  template <int N>
+  __device__ __forceinline__ void raise(float top, float& l, uint32_t tO, bool o, uint32_t* s) {
     const bool up = (top - raw) * sc > 8.0f;
+    if (!__any_sync(0xffffffffu, up || sub != 0.0f)) return;
+    raise_rows(up, top, l, tO, o);
+    if (N > 0) subtract<N>(s);
+  }
+  __device__ __forceinline__ void raise_rows(bool up, float top, float& l, uint32_t tO, bool o) {
     if (!__any_sync(0xffffffffu, up)) return;
     float f = 1.0f;
     if (up) {
@@ -354,8 +361,7 @@ __device__ __forceinline__ void softmax_role(const PromptArgs& a, Shared* sh, co
         for (int c = 0; c < 4; ++c) t5::ld32(tS + 32 * c, s + 32 * c);
 #pragma unroll
         for (int c = 0; c < 4; ++c) t5::wait_ld32(s + 32 * c);
-        ref.raise(max_of<128>(s), l, tO, j > 0);  // s_full came after the last PV
-        ref.template subtract<128>(s);
+        ref.template raise<128>(max_of<128>(s), l, tO, j > 0, s);  // s_full came after the last PV
         sum = to_weights<BF16, 32>(s, sc2, ref.off, p);
         t5::st32(tP, p);
         sum = f2_add(sum, to_weights<BF16, 32>(s + 64, sc2, ref.off, p));
@@ -377,7 +383,7 @@ __device__ __forceinline__ void softmax_role(const PromptArgs& a, Shared* sh, co
           }
           top = fmaxf(top, max_of<32>(s));
         }
-        ref.raise(top, l, tO, j > 0);
+        ref.template raise<0>(top, l, tO, j > 0, nullptr);
         sum = f2_pack(0.0f, 0.0f);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
