@@ -240,6 +240,19 @@ __device__ __forceinline__ uint64_t to_weights(const uint32_t* s, uint64_t sc2, 
   return f2_add(sum0, sum1);
 }
 
+// N scores of a row to the exponents of their weights, s sc - off.
+template <int N>
+__device__ __forceinline__ void scaled(uint32_t* s, uint64_t sc2, float off) {
+  const uint64_t off2 = f2_pack(-off, -off);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    float x, y;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, off2), x, y);
+    s[i] = __float_as_uint(x);
+    s[i + 1] = __float_as_uint(y);
+  }
+}
+
 template <int N>
 __device__ __forceinline__ float max_of(const uint32_t* s) {
   float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
@@ -279,7 +292,8 @@ struct Reference {
   // what m's rounding added, of a row that does not subtract
   __device__ __forceinline__ float rounding() const { return fabsf(m) <= 0x1p20f ? fmaf(raw, sc, -m) - kLift : 0.0f; }
 
-  // s: N scores of the row to subtract from
+  // s: N scores of the row to subtract from. (Where sc is 0 no score raises
+  // the reference, as inf * 0 compares false: every weight is 2^0.)
   template <int N>
   __device__ __forceinline__ void raise(float top, float& l, uint32_t tO, bool o, uint32_t* s) {
     const bool up = (top - raw) * sc > 8.0f;
@@ -391,13 +405,14 @@ __device__ __forceinline__ void softmax_role(const PromptArgs& a, Shared* sh, co
           if (c <= warp) {
             t5::ld32(tS + 32 * c, s);
             t5::wait_ld32(s);
-            if (c == warp) {
+            ref.template subtract<32>(s);
+            scaled<32>(s, sc2, ref.off);
+            if (c == warp) {  // after the scale: -inf * 0 is NaN
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (i > lane) s[i] = 0xff800000u;
             }
-            ref.template subtract<32>(s);
-            sum = f2_add(sum, to_weights<BF16, 16>(s, sc2, ref.off, p));
+            sum = f2_add(sum, to_weights<BF16, 16>(s, f2_pack(1.0f, 1.0f), 0.0f, p));
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) p[i] = 0u;
