@@ -1,10 +1,12 @@
 """Prompt attention by comparisons that a NaN cannot pass: `within` asks that
 every error is at most its bound, which is false of a NaN."""
+import math
+
 import pytest
 import torch
 
 import bit_quantized_kv_kvq_gb300 as kvq
-from tests.test_gpu_prompt_attention import BF16, F16, ints, reference, rows
+from tests.test_gpu_prompt_attention import BF16, F16, LENS, check, ints, reference, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +47,45 @@ def test_scale_zero_and_bad_values_of_later_tokens(bad, part):
     got = kvq.prompt_attention(q, k, v, ints([0, 300]), 0.0)
     assert torch.isfinite(want).all() and torch.equal(got[:157], want[:157])
     assert not torch.isfinite(got[157:, :, 9]).any()
+
+
+def finite(x, hq, h, lens, scale):
+    """`check` compares with `err > tol`, which is false of a NaN as well: with
+    finite inputs every row of a sequence has to be finite for it to hold."""
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    o = check(x, hq, h, cu, scale)
+    bad = ~torch.isfinite(o[:cu[-1]]).flatten(1).all(1)
+    assert not bad.any(), bad.nonzero().flatten().tolist()[:8]
+
+
+@pytest.mark.parametrize("lens", LENS + [[2049, 31]], ids=str)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_rows_of_every_length_are_finite(lens, d, dtype):
+    finite(rows(sum(lens), 4, 2, d, dtype, seed=sum(lens) + 1), 4, 2, lens, 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("h,g", [(1, 1), (2, 1), (1, 3), (3, 2), (2, 8), (1, 16), (8, 4)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_rows_of_every_head_group_are_finite(h, g, d, dtype):
+    finite(rows(300, h * g, h, d, dtype, seed=h * g + 1), h * g, h, [170, 130], 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-45, 1e-30, 1e-3, 1.0])
+@pytest.mark.parametrize("spread", [0.0, 0.3, 8.0])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_rows_at_every_scale_are_finite(scale, spread, dtype):
+    finite(rows(300, 2, 1, 64, dtype, seed=3, spread=spread), 2, 1, [300], scale)
+
+
+@pytest.mark.parametrize("flip", [False, True])
+def test_rows_of_rising_and_falling_scores_are_finite(flip):
+    x = rows(600, 1, 1, 128, F16, seed=5)
+    x[:, 0] = 0.5
+    x[:, 1] = (torch.arange(600)[:, None] * 0.02 + 0.01 * torch.randn(600, 128, generator=torch.Generator().manual_seed(2))).half()
+    if flip:
+        x[:, 1] = x[:, 1].flip(0)
+    finite(x, 1, 1, [600], 0.1)
