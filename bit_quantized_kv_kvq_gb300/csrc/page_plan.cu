@@ -8,10 +8,10 @@
 // position and every new page its place on the free stack, so everything after
 // the sums is independent per token and per page.
 //
-// A decode step reads and writes a few hundred bytes: latency, 5.4 us in a
+// A decode step reads and writes a few hundred bytes: latency, 4.9 us in a
 // graph for 16 requests. Many packed tokens go over the GPU (8 bytes written a
-// token, searched for four at a time): 262144 tokens of 1024 requests 7.3 us;
-// one cluster of eight CTAs took 20.5 us.
+// token, searched for four at a time): 262144 tokens of 1024 requests 8.1 us,
+// 1 us of it to look over the pages first; one cluster of eight CTAs took 20.5 us.
 #include "paged_internal.h"
 
 namespace kvq {
@@ -65,7 +65,7 @@ __device__ __forceinline__ int last_le(const int* key, int n, int x) {
 // sums for itself (a few thousand lengths at most) and takes its share of the
 // tokens and pages. lens_out and free_count_out may be the input arrays: one
 // CTA writes them once it has read those; with several, a second launch does,
-// after all of the first have.
+// after all of the first have ended.
 constexpr int kPlan = 1, kState = 2;
 
 template <int WHAT>
@@ -76,14 +76,20 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
   int* first = sm + R + 1;     // [R + 1] pages taken before the request's
   int* old = sm + 2 * (R + 1); // [R] length before
   __shared__ int bad_s;
+  // the second launch makes its own sums meanwhile, and waits before it writes
+  if (WHAT == kPlan) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int P = 1 << a.page_shift;
   if (threadIdx.x == 0) bad_s = 0;
   __syncthreads();
 
   const int free_count = *a.free_count;
+  const bool over = free_count < 0 || free_count > a.num_pages;
+  // the k-th page from the stack's top, where the stack has one
+  auto popped = [&](int k) { return a.free_pages[free_count - 1 - k]; };
+  auto in_cache = [&](int page) { return page >= 0 && page < a.num_pages; };
   int n[kPer], m[kPer], g[kPer];
   long long add = 0, grow = 0;
-  bool bad = false, full = false;
+  bool bad = false, full = false, torn = false;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int b = threadIdx.x * kPer + i;
@@ -96,14 +102,29 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
     g[i] = (int)(need - have);
     add += m[i];
     grow += g[i];
+    // new tokens go into the open page first
+    if (m[i] > 0 && n[i] > 0 && (n[i] & (P - 1)) && have <= a.max_pages)
+      torn |= !in_cache(a.table[(int64_t)b * a.max_pages + have - 1]);
   }
-  const bool over = free_count < 0 || free_count > a.num_pages;
   const int flags = (bad || over ? 1 : 0) | (full ? 2 : 0);
   if (flags) atomicOr(&bad_s, flags);
   long long total, pages;
   block_scan2(add, grow, &total, &pages);  // its barriers publish bad_s too
-  const bool fits = bad_s == 0 && total <= a.max_tokens && pages <= free_count;
-  if (fits) {
+  // The pages that the step takes off the stack are looked over before anything
+  // is planned with them: every CTA does so, and all come to the same answer.
+  const bool room = bad_s == 0 && total <= a.max_tokens && pages <= free_count;
+  if (room) {
+    const int count = (int)pages, *lowest = a.free_pages + (free_count - count);
+    const int head = min(count, (int)(-reinterpret_cast<uintptr_t>(lowest) & 15) >> 2);  // up to a 16-byte border
+    const int wide = (count - head) >> 2, rest = head + 4 * wide;
+    const int at = threadIdx.x;
+    if (at < head) torn |= !in_cache(lowest[at]);
+    if (at < count - rest) torn |= !in_cache(lowest[rest + at]);
+#pragma unroll 4
+    for (int i = at; i < wide; i += kThreads) {
+      const int4 x = reinterpret_cast<const int4*>(lowest + head)[i];
+      torn |= !(in_cache(x.x) && in_cache(x.y) && in_cache(x.z) && in_cache(x.w));
+    }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int b = threadIdx.x * kPer + i;
@@ -113,8 +134,8 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
       if (b == R - 1) cu[R] = (int)add, first[R] = (int)grow;
     }
   }
-  __syncthreads();
-  if (WHAT == kPlan) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const bool bad_page = __syncthreads_or(torn);
+  const bool fits = room && !bad_page;
   if (WHAT == kState) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   const int at0 = blockIdx.x * kThreads + threadIdx.x, stride = gridDim.x * kThreads;
@@ -129,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
       for (int b = threadIdx.x; b <= R; b += kThreads) a.cu[b] = 0;
       if (threadIdx.x == 0) {
         *a.free_count_out = free_count;
-        raise_status(a.status, (bad_s & 1) ? kStatusBadIndex : kStatusNoRoom);
+        raise_status(a.status, (bad_s & 1) || bad_page ? kStatusBadIndex : kStatusNoRoom);
       }
     }
     return;
@@ -145,9 +166,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
   for (int k = at0; k < (int)pages; k += stride) {
     const int b = last_le(first, R + 1, k);
     const int j = ((old[b] + P - 1) >> a.page_shift) + (k - first[b]);
-    const int page = a.free_pages[free_count - 1 - k];
-    if (page < 0 || page >= a.num_pages) raise_status(a.status, kStatusBadIndex);
-    a.table[(int64_t)b * a.max_pages + j] = page;
+    a.table[(int64_t)b * a.max_pages + j] = popped(k);
   }
   // four packed tokens a step: one search, then on from request to request
   const bool vec = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
@@ -165,12 +184,11 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
       const int p = old[b] + (i - cu[b]), j = p >> a.page_shift;
       if (j != page_index) {
         const int have = (old[b] + P - 1) >> a.page_shift;
-        page = j < have ? a.table[(int64_t)b * a.max_pages + j] : a.free_pages[free_count - 1 - (first[b] + j - have)];
+        page = j < have ? a.table[(int64_t)b * a.max_pages + j] : popped(first[b] + j - have);
         page_index = j;
       }
       pos[k] = p;
-      if (page >= 0 && page < a.num_pages) slot[k] = (page << a.page_shift) + (p & (P - 1));
-      else raise_status(a.status, kStatusBadIndex);
+      slot[k] = (page << a.page_shift) + (p & (P - 1));
     }
     if (vec && at + 4 <= a.max_tokens) {
       *reinterpret_cast<int4*>(a.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);

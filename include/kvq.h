@@ -446,10 +446,11 @@ KVQ_API kvq_status kvq_paged_cache_status(kvq_paged_cache* cache, void* stream, 
  *   lens_out  [requests], free_count_out [1]  the state after the step; either
  *             may be the array it replaces
  * slots and positions past the last packed token are -1. The step is planned
- * whole or not at all: where it does not fit (pages, a table row, max_tokens)
- * or a length is negative, the table stays, cu_tokens is all 0, slots and
- * positions are all -1, lens_out and free_count_out repeat the inputs, and
- * the status word is set. All arrays int32 on the device. One launch, two for
+ * whole or not at all: where it does not fit (pages, a table row, max_tokens),
+ * a length is negative, or a page that the new tokens would go to (one that the
+ * step takes off the stack, or a row's open page) is not one of the cache's,
+ * the table stays, cu_tokens is all 0, slots and positions are all -1, lens_out
+ * and free_count_out repeat the inputs, and the status word is set. All arrays int32 on the device. One launch, two for
  * more than 4096 packed tokens. */
 KVQ_API kvq_status kvq_paged_reserve(kvq_paged_cache* cache, int32_t requests, const int32_t* lens,
                                      const int32_t* new_tokens, int32_t* table, const int32_t* free_pages,
@@ -461,7 +462,7 @@ KVQ_API kvq_status kvq_paged_reserve(kvq_paged_cache* cache, int32_t requests, c
  * stack (in order of request and position), lens[b] becomes 0; table rows stay
  * as they are. free_pages has room for num_pages entries; pages past that are
  * dropped and set the status word; a table entry out of range goes back as it
- * is and sets it too. A page that two rows name must be released by one of
+ * is and sets it too (a reserve that would take it is refused). A page that two rows name must be released by one of
  * them only. One launch. */
 KVQ_API kvq_status kvq_paged_release(kvq_paged_cache* cache, int32_t requests, const int32_t* done, int32_t* lens,
                                      const int32_t* table, int32_t* free_pages, int32_t* free_count, void* stream);
