@@ -117,7 +117,9 @@ def _rows(t, name, dtype, device, heads=None, dim=None):
 
 class PagedKVCache:
     """A paged 8-bit KV cache in one torch-owned device buffer, driven through
-    the C ABI. ``dtype`` is the type of K, V and Q."""
+    the C ABI. ``dtype`` is the type of K, V and Q. The buffer is allocated and
+    zeroed on ``stream`` (default: the current one): calls on other streams are
+    ordered after that by the caller, and done before the cache is dropped."""
 
     def __init__(self, num_layers, max_requests, num_kv_heads, head_dim, page_tokens, num_pages, max_pages,
                  code=PAGE_INT8, dtype=torch.float16, device=None, stream=None):
@@ -130,7 +132,7 @@ class PagedKVCache:
         n = ctypes.c_size_t()
         _check(lib.kvq_paged_cache_bytes(ctypes.byref(self.cfg), ctypes.byref(n)))
         self.nbytes = n.value
-        self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device if device is not None else "cuda")
+        self.buffer = _empty(self.nbytes, torch.uint8, device if device is not None else "cuda", stream)
         self.device = self.buffer.device
         h = _P()
         _check(lib.kvq_paged_cache_create(ctypes.byref(self.cfg), self.buffer.data_ptr(), self.nbytes,

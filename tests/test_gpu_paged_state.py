@@ -1,5 +1,6 @@
 """State of the paged path that outlives a call: a refused plan changes
-nothing, whatever it was refused for."""
+nothing, whatever it was refused for; memory belongs to the stream that a call
+was given."""
 import numpy as np
 import pytest
 import torch
@@ -75,3 +76,30 @@ def test_bad_entries_that_a_step_does_not_take_are_left(tokens):
     plan = cache.reserve(ints(lens), ints(new), dt, ints(free), ints([count]), int(new.sum()))
     assert np.array_equal(plan.lens.cpu().numpy(), lens + new) and plan.free_count.item() == count - grow
     assert (plan.slots >= 0).all() and cache.status() == 0
+
+
+# -- streams -----------------------------------------------------------------
+def test_a_cache_on_a_stream_takes_no_memory_of_the_current_one():
+    """A block that the current stream's queued work still writes is free for
+    that stream's next tensor, not for a cache that another stream zeroes."""
+    side = torch.cuda.Stream()
+    args = (2, 3, 2, 64, 16, 4000, 8)
+    n = kvq.PagedKVCache(*args).nbytes
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    late = torch.empty(n, dtype=torch.uint8, device="cuda")
+    block = late.data_ptr()
+    del late
+    cache = kvq.PagedKVCache(*args, stream=side)
+    side.synchronize()
+    lo = cache.buffer.data_ptr()
+    assert lo + n <= block or block + n <= lo
+    del cache
+    # the same with work under way: its late writes stay out of the cache
+    late = torch.empty(n, dtype=torch.uint8, device="cuda")
+    torch.cuda._sleep(50_000_000)
+    late.fill_(255)
+    del late
+    cache = kvq.PagedKVCache(*args, stream=side)
+    torch.cuda.synchronize()
+    assert not cache.buffer.any() and cache.status() == 0
