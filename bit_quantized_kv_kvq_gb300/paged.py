@@ -89,6 +89,14 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _captured(stream):
+    """Whether a graph is being captured on the stream that a call goes to."""
+    if stream is None:
+        return _capturing()
+    with torch.cuda.stream(stream):
+        return _capturing()
+
+
 def _ints(t, name, shape, device):
     """Pointer of an int32 tensor of the given shape."""
     if not isinstance(t, _Tensor) or t.dtype is not _int32 or t.device != device:
@@ -219,7 +227,7 @@ class PagedKVCache:
         return n
 
     def _workspace(self, hq, raw, stream):
-        if _capturing():
+        if _captured(stream):
             return _empty(self.workspace_bytes(hq), torch.uint8, self.device, stream)
         ws = self._ws.get((hq, raw))
         if ws is None:
@@ -230,7 +238,8 @@ class PagedKVCache:
         """Attention of one query token per request (kvq_paged_decode_attention):
         q [requests][H_q][D] -> out [requests][H_q][D], zeros where lens is 0.
         Without ``workspace`` the cache keeps one for each stream, and a captured
-        call takes one of its own: neither streams nor graphs share it."""
+        call takes one of its own from the graph's memory pool: neither streams nor
+        graphs share it (but graphs that share a pool, which replay in turn)."""
         lib = _lib or _bind()
         dev = self.device
         qp, qs = _rows(q, "q", self.dtype, dev, dim=self._dim)

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import bit_quantized_kv_kvq_gb300 as kvq
-from tests.test_gpu_paged import F16, ints
+from bit_quantized_kv_kvq_gb300 import paged
+from tests.test_gpu_paged import F16, Served, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +104,96 @@ def test_a_cache_on_a_stream_takes_no_memory_of_the_current_one():
     cache = kvq.PagedKVCache(*args, stream=side)
     torch.cuda.synchronize()
     assert not cache.buffer.any() and cache.status() == 0
+
+
+class Recorder:
+    """The library with the workspace of every decode noted."""
+
+    def __init__(self, lib):
+        self.lib, self.ws = lib, []
+
+    def __getattr__(self, name):
+        f = getattr(self.lib, name)
+        if name != "kvq_paged_decode_attention":
+            return f
+        def call(*args):
+            self.ws.append((args[11], args[11] + args[12]))
+            return f(*args)
+        return call
+
+
+def apart(ranges):
+    ranges = sorted(ranges)
+    return all(a[1] <= b[0] for a, b in zip(ranges, ranges[1:]))
+
+
+def capture(side, call):
+    """A graph of one call on `side`, made while another stream is current."""
+    gr = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        gr.capture_begin(capture_error_mode="thread_local")
+    try:
+        call()
+    finally:
+        with torch.cuda.stream(side):
+            gr.capture_end()
+    return gr
+
+
+def test_workspaces_are_a_streams_or_a_graphs_own(monkeypatch):
+    """Without `workspace`: eager calls of two streams and graphs captured on
+    a stream that is not the current one, none of which share it."""
+    s = Served(4, 2, 128, 32, "int8", F16, 640, seed=11)
+    s.step([600, 33, 0, 257])
+    q = [s.rows(4, 8).cuda() for _ in range(4)]
+    want = [s.cache.decode(0, x, s.table, s.lens, 0.1) for x in q]
+    rec = Recorder(paged._lib)
+    monkeypatch.setattr(paged, "_lib", rec)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [torch.zeros_like(want[0]) for _ in q]
+    torch.cuda.synchronize()
+    for i, st in ((0, side), (1, other)):
+        s.cache.decode(0, q[i], s.table, s.lens, 0.1, out=outs[i], stream=st)
+    graphs = [capture(side, lambda i=i: s.cache.decode(0, q[i], s.table, s.lens, 0.1, out=outs[i], stream=side))
+              for i in (2, 3)]
+    assert len(rec.ws) == 4 and apart(rec.ws)
+    # all four at once
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(30):
+        for i, st in ((0, side), (1, other)):
+            s.cache.decode(0, q[i], s.table, s.lens, 0.1, out=outs[i], stream=st)
+        for gr, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+    torch.cuda.synchronize()
+    assert rec.ws[4:] == rec.ws[:2] * 30  # a stream keeps its own
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+    assert s.cache.status() == 0
+
+
+def test_graphs_of_the_current_stream_have_workspaces_of_their_own(monkeypatch):
+    s = Served(3, 1, 64, 16, "e4m3", F16, 320, seed=2)
+    s.step([300, 10, 77])
+    q = [s.rows(3, 4).cuda() for _ in range(2)]
+    want = [s.cache.decode(0, x, s.table, s.lens, 0.1) for x in q]
+    rec = Recorder(paged._lib)
+    monkeypatch.setattr(paged, "_lib", rec)
+    outs, graphs = [torch.zeros_like(want[0]) for _ in q], []
+    for x, o in zip(q, outs):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            s.cache.decode(0, x, s.table, s.lens, 0.1, out=o)
+        graphs.append(gr)
+    assert len(rec.ws) == 2 and apart(rec.ws)
+    streams = [torch.cuda.Stream() for _ in q]
+    for _ in range(30):
+        for gr, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want)) and s.cache.status() == 0
