@@ -6,9 +6,10 @@ A step::
     plan = cache.reserve(lens, new_tokens, table, free_pages, free_count, max_tokens)
     for layer in range(num_layers):
         cache.write(layer, k, v, plan.cu_tokens, plan.slots, plan.lens)
-        o = prompt_attention(q, k, v, plan.cu_tokens, scale)     # prompts, or
-        o = cache.decode(layer, q, table, plan.lens, scale)      # one token per request
-    cache.release(done, plan.lens, table, free_pages, free_count)
+        o = prompt_attention(q, k, v, plan.cu_tokens, scale, status=cache.status_word)   # prompts, or
+        o = cache.decode(layer, q, table, plan.lens, scale)                              # one token per request
+    cache.release(done, plan.lens, table, free_pages, plan.free_count)
+    cache.status()                                               # whether a call found something amiss
 
 Lengths, tables, slots and the free list are int32 tensors on the cache's
 device; no call copies them to the host, so a step can be captured into a CUDA
@@ -262,6 +263,12 @@ class PagedKVCache:
         return out
 
     # -- inspection ---------------------------------------------------------
+    @property
+    def status_word(self):
+        """The device word that status() reads, int32 [1]: given to
+        prompt_attention as ``status``, it collects that call's bits too."""
+        return self.buffer[:4].view(_int32)
+
     def _view(self, layer, name):
         view = self._views.get((layer, name))
         if view is None:
@@ -313,7 +320,9 @@ def prompt_attention(q, k, v, cu_tokens, softmax_scale, out=None, status=None, s
     """Causal attention over packed prompts (kvq_prompt_attention): q
     [tokens][H_q][D], k and v [tokens][H_kv][D] in fp16 or bf16, cu_tokens
     int32 [sequences + 1]. Rows of ``out`` outside every sequence are left as
-    they are (uninitialised where ``out`` is not given)."""
+    they are (uninitialised where ``out`` is not given). ``status``: int32 [1],
+    such as ``PagedKVCache.status_word``, which a range of cu_tokens outside the
+    tokens or a wait that gave up sets; without it they go unseen."""
     lib = _lib or _bind()
     if not isinstance(q, torch.Tensor) or q.dtype not in (torch.float16, torch.bfloat16) or not q.is_cuda:
         raise TypeError("q must be a CUDA float16 or bfloat16 tensor")

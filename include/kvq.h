@@ -419,7 +419,8 @@ KVQ_API kvq_status kvq_paged_cache_bytes(const kvq_paged_config* cfg, size_t* by
 
 /* As kvq_cache_create: validates, lays out `dev_buf` (256-byte aligned) and
  * zeroes it on `stream`. The handle holds no state but the layout: several
- * host threads may use it at once. */
+ * host threads may use it at once. The buffer's first uint32 is the status
+ * word; kvq_prompt_attention may be given it too. */
 KVQ_API kvq_status kvq_paged_cache_create(const kvq_paged_config* cfg, void* dev_buf, size_t bytes, void* stream,
                                           kvq_paged_cache** out);
 
@@ -509,7 +510,8 @@ KVQ_API kvq_status kvq_paged_decode_attention(kvq_paged_cache* cache, int32_t la
  * are left as they are. A later token does not reach an earlier one's output,
  * not even by an infinity or NaN among its values. status: an optional uint32
  * device word that receives the bits of kvq_paged_cache_status (a range that
- * cu_tokens puts outside [0, max_tokens] is left out and sets one). All pointers
+ * cu_tokens puts outside [0, max_tokens] is left out and sets one); without it
+ * such a range, or a wait that gave up, goes unseen. All pointers
  * must be of the current device. softmax_scale: finite and >= 0. One launch. */
 KVQ_API kvq_status kvq_prompt_attention(const void* q, const void* k, const void* v, int64_t q_stride,
                                         int64_t k_stride, int64_t v_stride, int32_t max_tokens, int32_t num_seqs,

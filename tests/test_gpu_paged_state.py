@@ -1,6 +1,8 @@
 """State of the paged path that outlives a call: a refused plan changes
 nothing, whatever it was refused for; memory belongs to the stream that a call
 was given."""
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -197,3 +199,30 @@ def test_graphs_of_the_current_stream_have_workspaces_of_their_own(monkeypatch):
                 gr.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for o, w in zip(outs, want)) and s.cache.status() == 0
+
+
+# -- status ------------------------------------------------------------------
+def test_prompt_attention_reports_through_the_caches_status():
+    """As the module's step has it: a bad range is left out, and status() raises."""
+    assert re.search(r"prompt_attention\(.*status=cache.status_word", paged.__doc__)
+    cache = kvq.PagedKVCache(1, 2, 1, 64, 16, 8, 4)
+    x = torch.randn(60, 4, 64, device="cuda").half()
+    q, k, v = x[:, :2], x[:, 2:3], x[:, 3:]
+    cu, out = ints([0, 20, 60]), torch.zeros(60, 2, 64, dtype=F16, device="cuda")
+    gr = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(gr):
+        kvq.prompt_attention(q, k, v, cu, 0.1, out=out, status=cache.status_word)
+    def eager():
+        kvq.prompt_attention(q, k, v, cu, 0.1, out=out, status=cache.status_word)
+    for run in (eager, gr.replay):
+        cu.copy_(ints([0, 20, 60]))
+        run()
+        assert cache.status() == 0 and out.any()
+        cu.copy_(ints([0, 20, 61]))
+        out[20:] = 7
+        run()
+        with pytest.raises(kvq.KVQError) as e:
+            cache.status()
+        assert e.value.status == 7 and (out[20:] == 7).all() and cache.status() == 0
+    assert cache.status_word.shape == (1,) and cache.status_word.data_ptr() == cache.buffer.data_ptr()
