@@ -135,10 +135,11 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
 // Exponent k with max |x| * 2^k in [2^14, 2^15), from the bits of max |x| in
 // bf16: bf16 queries go to the fp16 products with the codes scaled by 2^k. That
 // is exact but for elements below 2^-29 of the query's largest, whose rounding
-// (2^-40 of it) is far below the fp32 sums' own.
+// (2^-40 of it) is far below the fp32 sums' own. 126 keeps 2^k and 2^-k normal,
+// and every bf16 number below 2^-111 times 2^126 is an exact fp16 one.
 __device__ __forceinline__ int bf16_shift(uint32_t top_bits) {
   const int k = 14 - ((int)(top_bits >> 7) - 127);
-  return k > 100 ? 100 : k;
+  return k > 126 ? 126 : k;
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
@@ -178,12 +179,12 @@ struct Warp {
     }
   }
 
-  // The loaded queries' factors, and the empty running state.
-  __device__ __forceinline__ void begin(float scale_log2) {
+  // The loaded queries' factors 2^-k, and the empty running state.
+  __device__ __forceinline__ void begin() {
     const int t = threadIdx.x & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float f = scale_log2;
+      float f = 1.0f;
       if (BF16) {
         uint32_t top = 0;
 #pragma unroll
@@ -198,7 +199,7 @@ struct Warp {
           qf[nt][s][0] = bf2_to_h2(qf[nt][s][0], up);
           qf[nt][s][1] = bf2_to_h2(qf[nt][s][1], up);
         }
-        f *= exp2i(-k);
+        f = exp2i(-k);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -214,7 +215,7 @@ struct Warp {
   }
 
   // Scores s of 16 tokens (c0, c1: token g; c2, c3: token g + 8) to their
-  // weights; q f: the heads' factors. va, vb: whether the two tokens count.
+  // weights; q f0: the heads' factors. va, vb: whether the two tokens count.
   __device__ __forceinline__ void weights(float (&s)[NT][4], const float (&q)[NT][2], float f0, bool va, bool vb) {
     bool up = false;
 #pragma unroll
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(kThreads + 32, ctas_per_sm(NT))
       asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
       asm volatile("prefetch.global.L2 [%0];" ::"l"(at + (int64_t)P * D));
     }
-    w.begin(a.scale_log2);
+    w.begin();
     for (int tile = cur.t0; tile < cur.t1; ++tile, ++i) {
       const int st = i % kStages;
       ok = ok && wait(&ring.full[st], (i / kStages) & 1, c.status);
@@ -667,7 +668,8 @@ __global__ void __launch_bounds__(kThreads + 32, ctas_per_sm(NT))
         float s[NT][4];
         uint32_t pb[NT][2];
         w.scores(kr[j], s);
-        w.weights(s, w.qs, sc[j].x, true, true);
+        // the page's and the softmax's scale first: 2^-k alone may be far off the scores' size
+        w.weights(s, w.qs, sc[j].x * a.scale_log2, true, true);
         w.half_weights(s, pb);
         w.values(vr[j], sc[j].y, pb);
       }
