@@ -391,7 +391,7 @@ kvq_status kvq_prompt_attention(const void* q, const void* k, const void* v, int
   if (num_seqs < 1 || num_seqs > kvq::kMaxRequests)
     return fail(KVQ_ERR_INVALID_ARG, "num_seqs %d must be in [1, %d]", num_seqs, kvq::kMaxRequests);
   if (max_tokens < 0) return fail(KVQ_ERR_INVALID_ARG, "max_tokens must be >= 0");
-  if (max_tokens > 1 << 26)  // the kernel's bounded waits cover the longest block of a prompt of that size
+  if (max_tokens > 1 << 26)  // the kernel's bounded waits are four times the longest block of such a prompt
     return fail(KVQ_ERR_UNSUPPORTED, "max_tokens %d exceeds 2^26", max_tokens);
   if (max_tokens == 0) return KVQ_OK;
   kvq_status s = check_row("q", q, q_stride, (int64_t)num_q_heads * head_dim);
