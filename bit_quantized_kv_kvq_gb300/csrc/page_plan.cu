@@ -8,8 +8,8 @@
 // position and every new page its place on the free stack, so everything after
 // the sums is independent per token and per page.
 //
-// A decode step reads and writes a few hundred bytes: latency, 4.9 us in a
-// graph for 16 requests. Many packed tokens go over the GPU (8 bytes written a
+// A decode step reads and writes a few hundred bytes: latency, 4.9 us for
+// 16 requests (thirty in a graph). Many packed tokens go over the GPU (8 bytes written a
 // token, searched for four at a time): 262144 tokens of 1024 requests 8.1 us,
 // 1 us of it to look over the pages first; one cluster of eight CTAs took 20.5 us.
 #include "paged_internal.h"
@@ -199,6 +199,8 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) 
   }
 }
 
+// One CTA: requests end a few at a time. 797 pages take 3 us, and where many
+// requests end at once its rounds of dependent loads show: 196615 pages 143 us.
 __global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseArgs a) {
   __shared__ int first[kMaxRequests + 1];
   const int R = a.requests;

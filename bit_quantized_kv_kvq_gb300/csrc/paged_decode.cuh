@@ -28,7 +28,7 @@
 // 275 us, 0.98 of the copy rate. 64 ragged requests up to 8192 tokens (0.51
 // GB): 91 us, 0.82 of it; what is left are the ends of requests (tail, merge,
 // the next queries). 24 requests up to 2500 tokens, 32 heads of 64 channels
-// (0.115 GB): 32 us, 0.53. One request of 777 tokens: 8.7 us, latency of two launches.
+// (0.115 GB): 31 us, 0.54. One request of 777 tokens: 8.7 us, latency of two launches.
 // Loads straight into the fragments' registers, without a ring, took 292, 101,
 // 39 and 8.5 us.
 #pragma once
@@ -51,6 +51,13 @@ __host__ __device__ constexpr int unit_of(int dim) { return kWarps * 16 * sub_of
 constexpr int kExtra = 5;
 
 // Heads of one pass over the codes: 8 NT (NT column tiles of the products).
+// Two tiles a pass cost registers (two CTAs an SM and, with 128 channels, some
+// spills, instead of three CTAs), but past 8 heads they save reading and
+// converting the codes once more.
+// us with one / with two, 64 ragged requests up to 8192 tokens, 8 kv-heads:
+//   heads a kv-head     8         9        12        16        24        40
+//   128 channels      95/129   173/131   177/137   182/145   267/261   435/388
+//    64 channels      54/65     95/65     97/66     99/68    144/124   231/184
 __host__ __device__ constexpr int nt_of(int group) { return group <= 8 ? 1 : 2; }
 // CTAs per SM that the registers and the rings (kTileBytes each stage) allow.
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }

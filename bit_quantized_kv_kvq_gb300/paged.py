@@ -298,7 +298,8 @@ class PagedKVCache:
         return self._view(layer, "tails")
 
     def status(self, stream=None):
-        """Synchronizes and clears the status word; raises KVQError if it was set."""
+        """Synchronizes the stream and clears the status word; raises KVQError if
+        it was set. Work on other streams is done before, by the caller."""
         lib = _lib or _bind()
         w = ctypes.c_uint32()
         _check(lib.kvq_paged_cache_status(self.handle, _raw_stream(stream, self.device), ctypes.byref(w)))
@@ -317,7 +318,8 @@ class PagedKVCache:
 
 
 def prompt_attention(q, k, v, cu_tokens, softmax_scale, out=None, status=None, stream=None):
-    """Causal attention over packed prompts (kvq_prompt_attention): q
+    """Causal attention over packed prompts on their own keys and values, not
+    on what the cache holds of them before (kvq_prompt_attention): q
     [tokens][H_q][D], k and v [tokens][H_kv][D] in fp16 or bf16, cu_tokens
     int32 [sequences + 1]. Rows of ``out`` outside every sequence are left as
     they are (uninitialised where ``out`` is not given). ``status``: int32 [1],

@@ -432,7 +432,9 @@ KVQ_API kvq_status kvq_paged_cache_get_layout(const kvq_paged_cache* cache, int3
 /* Synchronizes `stream`, reads the status word and clears it. KVQ_OK,
  * KVQ_ERR_CAPACITY (a reserve found too few pages, too small a table row or
  * too small slot arrays), KVQ_ERR_TIMEOUT or KVQ_ERR_DEVICE_STATUS (a length,
- * slot, page or count out of range). *word (optional) receives the bits. */
+ * slot, page or count out of range). *word (optional) receives the bits. Work on
+ * other streams has to be done before: a bit that it raises between the read and
+ * the clearing would go unseen. */
 KVQ_API kvq_status kvq_paged_cache_status(kvq_paged_cache* cache, void* stream, uint32_t* word);
 
 /* Plans one step for `requests` (<= max_requests) slots: request b holds
@@ -463,8 +465,10 @@ KVQ_API kvq_status kvq_paged_reserve(kvq_paged_cache* cache, int32_t requests, c
  * stack (in order of request and position), lens[b] becomes 0; table rows stay
  * as they are. free_pages has room for num_pages entries; pages past that are
  * dropped and set the status word; a table entry out of range goes back as it
- * is and sets it too (a reserve that would take it is refused). A page that two rows name must be released by one of
- * them only. One launch. */
+ * is and sets it too (a reserve that would take it is refused). A page that two
+ * rows name must go back once only: a request on a shared prefix is released by
+ * arrays of its own pages (the row's entries past the prefix, the length less
+ * the prefix). One launch. */
 KVQ_API kvq_status kvq_paged_release(kvq_paged_cache* cache, int32_t requests, const int32_t* done, int32_t* lens,
                                      const int32_t* table, int32_t* free_pages, int32_t* free_count, void* stream);
 
@@ -490,8 +494,9 @@ KVQ_API kvq_status kvq_paged_decode_workspace_bytes(const kvq_paged_cache* cache
  * multiple of 8, >= H_q * D); H_q any multiple of H_kv. out: [requests][H_q][D] in
  * out_dtype (KVQ_F32 or the config's dtype); a request with lens[b] == 0 gets
  * zeros. The sums are fp32 and normalised at the end: tokens * 2^15 * |v| must stay
- * below 3e38 (tokens * 2^8 * |v| in kvq_prompt_attention). The tiles of all requests are cut into equal ranges by the kernel
- * from lens, so the grid does not depend on the lengths. workspace: 16-byte
+ * below 3e38 (tokens * 2^8 * |v| in kvq_prompt_attention). The tiles of all
+ * requests are cut into equal ranges by the kernel from lens, so the grid does
+ * not depend on the lengths. workspace: 16-byte
  * aligned, any content, not shared with calls that overlap on the GPU. Two
  * launches (the second merges the ranges' partial sums in a fixed order). */
 KVQ_API kvq_status kvq_paged_decode_attention(kvq_paged_cache* cache, int32_t layer, int32_t requests, const void* q,
@@ -501,14 +506,20 @@ KVQ_API kvq_status kvq_paged_decode_attention(kvq_paged_cache* cache, int32_t la
 
 /* Causal attention over whole prompts, packed one after the other, on their
  * own keys and values (no cache): token i of a sequence attends tokens 0 .. i
- * of it. q: [max_tokens][H_q][D]; k, v: [max_tokens][H_kv][D]; dtype KVQ_F16 or
- * KVQ_BF16, D 64 or 128, token rows q_stride / k_stride / v_stride elements
- * apart (multiples of 8, no less than a row). H_q is a multiple of H_kv.
+ * of it. It reads no cache: tokens that a request held before (an earlier chunk of
+ * its prompt, a shared prefix) are not attended, and in a step that mixes prompts
+ * with single tokens of running requests the latter come out as sequences of one
+ * token, to be replaced by kvq_paged_decode_attention's rows.
+ * q: [max_tokens][H_q][D]; k, v: [max_tokens][H_kv][D]; dtype KVQ_F16 or KVQ_BF16,
+ * D 64 or 128, token rows q_stride / k_stride / v_stride elements apart
+ * (multiples of 8, no less than a row). H_q is a multiple of H_kv.
  * cu_tokens: [num_seqs + 1] int32 on the device, sequence s holds tokens
  * cu_tokens[s] .. cu_tokens[s + 1] - 1 (the array kvq_paged_reserve writes);
- * num_seqs <= 4096, max_tokens <= 2^26. out: [max_tokens][H_q][D] in dtype; rows outside every sequence
- * are left as they are. A later token does not reach an earlier one's output,
- * not even by an infinity or NaN among its values. status: an optional uint32
+ * a sequence that ends before it starts holds none, and sequences must not
+ * overlap. num_seqs <= 4096, max_tokens <= 2^26. out: [max_tokens][H_q][D] in
+ * dtype; rows outside every sequence are left as they are. A later token does
+ * not reach an earlier one's output, not even by an infinity or NaN among its
+ * values. status: an optional uint32
  * device word that receives the bits of kvq_paged_cache_status (a range that
  * cu_tokens puts outside [0, max_tokens] is left out and sets one); without it
  * such a range, or a wait that gave up, goes unseen. All pointers
