@@ -9,7 +9,7 @@ import torch
 
 import bit_quantized_kv_kvq_gb300 as kvq
 from bit_quantized_kv_kvq_gb300 import paged
-from tests.test_gpu_paged import F16, Served, ints
+from tests.test_gpu_paged import F16, PO, Served, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -79,6 +79,41 @@ def test_bad_entries_that_a_step_does_not_take_are_left(tokens):
     plan = cache.reserve(ints(lens), ints(new), dt, ints(free), ints([count]), int(new.sum()))
     assert np.array_equal(plan.lens.cpu().numpy(), lens + new) and plan.free_count.item() == count - grow
     assert (plan.slots >= 0).all() and cache.status() == 0
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("r,tokens", [(50, 3000), (50, 9000), (3000, 40000)])
+def test_steps_in_place_one_after_the_other(r, tokens, graph):
+    """Lengths and free count are read and written by the same launches (one,
+    or two that overlap), step after step without a wait between them."""
+    page, steps = 16, 6
+    rs = np.random.RandomState(r)
+    new = rs.multinomial(tokens, np.ones(r) / r)
+    new[rs.randint(r)] = 0
+    t = int(new.sum())
+    mp = steps * (int(new.max()) // page + 1) + 1
+    pages = steps * (t // page + r)
+    order = rs.permutation(pages)
+    cache = kvq.PagedKVCache(1, r, 1, 64, page, pages, mp)
+    lens, dn, table, free, count = ints(np.zeros(r)), ints(new), ints(np.full((r, mp), -1)), ints(order), ints([pages])
+    plan = cache.reserve(lens, ints(np.zeros(r)), table, free, count, t, lens_out=lens, free_count_out=count)
+    def run():
+        cache.reserve(lens, dn, table, free, count, t, plan=plan)
+    if graph:
+        gr = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(gr):
+            run()
+        run = gr.replay
+    for _ in range(steps):
+        run()
+    torch.cuda.synchronize()
+    want = (np.full((r, mp), -1, np.int32), None, None, None, np.zeros(r, np.int32), pages)
+    for _ in range(steps):
+        want = PO.reserve(want[4], new, want[0], order, want[5], t, page)
+    for got, ref in zip((table, plan.cu_tokens, plan.slots, plan.positions, lens, count), want):
+        assert np.array_equal(got.cpu().numpy().reshape(np.shape(ref)), ref)
+    assert cache.status() == 0
 
 
 # -- streams -----------------------------------------------------------------
