@@ -147,6 +147,9 @@ class PagedKVCache:
         _check(lib.kvq_paged_cache_create(ctypes.byref(self.cfg), self.buffer.data_ptr(), self.nbytes,
                                           _raw_stream(stream, self.device), ctypes.byref(h)))
         self.handle = h
+        #: The device word that status() reads, int32 [1]: given to prompt_attention
+        #: as ``status``, it collects that call's bits too.
+        self.status_word = self.buffer[:4].view(_int32)
         self._ws_bytes, self._ws = {}, {}
         self._views = {}
         self._table_pages, self._all_pages = max_pages, num_pages
@@ -263,12 +266,6 @@ class PagedKVCache:
         return out
 
     # -- inspection ---------------------------------------------------------
-    @property
-    def status_word(self):
-        """The device word that status() reads, int32 [1]: given to
-        prompt_attention as ``status``, it collects that call's bits too."""
-        return self.buffer[:4].view(_int32)
-
     def _view(self, layer, name):
         view = self._views.get((layer, name))
         if view is None:
