@@ -15,13 +15,13 @@ import torch
 
 from . import paged as _paged
 from . import workloads as _W
-from .paged import PAGE_E4M3, PAGE_INT8, PagedKVCache, StepPlan, prompt_attention
+from .paged import PAGE_E4M3, PAGE_INT8, PagedKVCache, Rotation, StepPlan, norm_rotate, prompt_attention
 
 __all__ = [
     "KVQError", "QuantizedKVCache", "lib", "library_path",
     "SYM_PER_TOKEN", "ASYM_PER_TOKEN", "ASYM_PER_CHANNEL", "CODEBOOK_PER_TOKEN", "F32", "F16",
     "E2M1_LEVELS",
-    "PagedKVCache", "StepPlan", "prompt_attention", "PAGE_INT8", "PAGE_E4M3",
+    "PagedKVCache", "StepPlan", "Rotation", "norm_rotate", "prompt_attention", "PAGE_INT8", "PAGE_E4M3",
 ]
 
 SYM_PER_TOKEN = 0

@@ -2,6 +2,7 @@
 // argument checks, the layout inside the caller's buffer and the launches.
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 #include <new>
 
 #include "paged_internal.h"
@@ -121,6 +122,29 @@ kvq_status check_row(const char* what, const void* p, int64_t stride, int64_t ro
   if (stride < row || stride % 8 != 0 || stride > (int64_t)1 << 31)
     return fail(KVQ_ERR_INVALID_ARG, "the token stride %lld of %s must be a multiple of 8 elements and in [%lld, 2^31]",
                 (long long)stride, what, (long long)row);
+  return KVQ_OK;
+}
+
+kvq_status check_ints(std::initializer_list<const void*> arrays) {
+  for (const void* p : arrays) {
+    if (!p) return fail(KVQ_ERR_INVALID_ARG, "the arrays must not be NULL");
+    if (!aligned(p, 4)) return fail(KVQ_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+  }
+  return KVQ_OK;
+}
+
+kvq_status check_device(std::initializer_list<const void*> pointers, const char* names) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  for (const void* p : pointers) {
+    if (!p) continue;
+    cudaPointerAttributes attr;
+    e = cudaPointerGetAttributes(&attr, p);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaPointerGetAttributes");
+    if ((attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged) || attr.device != dev)
+      return fail(KVQ_ERR_INVALID_ARG, "%s must be memory of the current device %d", names, dev);
+  }
   return KVQ_OK;
 }
 
@@ -297,6 +321,62 @@ kvq_status kvq_paged_release(kvq_paged_cache* h, int32_t requests, const int32_t
   return done(kvq::launch_release(a, static_cast<cudaStream_t>(stream)), 1, "release launch");
 }
 
+kvq_status kvq_paged_release_shared(kvq_paged_cache* h, int32_t requests, const int32_t* done_flags, int32_t* lens,
+                                    const int32_t* table, int32_t* free_pages, int32_t* free_count, int32_t* shared,
+                                    void* stream) {
+  kvq_status s = check_handle(h);
+  if (s == KVQ_OK) s = check_requests(h, requests);
+  if (s == KVQ_OK) s = check_ints({done_flags, lens, table, free_pages, free_count, shared});
+  if (s != KVQ_OK) return s;
+  kvq::ReleaseSharedArgs a;
+  a.r.requests = requests;
+  a.r.page_shift = log2_of(h->cfg.page_tokens);
+  a.r.num_pages = h->cfg.num_pages;
+  a.r.max_pages = h->cfg.max_pages;
+  a.r.done = done_flags;
+  a.r.table = table;
+  a.r.lens = lens;
+  a.r.free_pages = free_pages;
+  a.r.free_count = free_count;
+  a.r.status = reinterpret_cast<uint32_t*>(h->base);
+  a.shared = shared;
+  return done(kvq::launch_release_shared(a, static_cast<cudaStream_t>(stream)), 1, "shared release launch");
+}
+
+kvq_status kvq_paged_fork(kvq_paged_cache* h, int32_t requests, int32_t pairs, const int32_t* src, const int32_t* dst,
+                          int32_t* lens, int32_t* table, const int32_t* free_pages, int32_t* free_count,
+                          int32_t* shared, void* stream) {
+  kvq_status s = check_handle(h);
+  if (s == KVQ_OK) s = check_requests(h, requests);
+  if (s != KVQ_OK) return s;
+  if (pairs < 0 || pairs > h->cfg.max_requests)
+    return fail(KVQ_ERR_INVALID_ARG, "pairs %d must be in [0, %d]", pairs, h->cfg.max_requests);
+  if (pairs == 0) return KVQ_OK;
+  s = check_ints({src, dst, lens, table, free_pages, free_count, shared});
+  if (s != KVQ_OK) return s;
+  const kvq::PagedDev c = layer_dev(h, 0);
+  kvq::ForkArgs a;
+  a.requests = requests;
+  a.pairs = pairs;
+  a.page_shift = c.page_shift;
+  a.num_pages = c.num_pages;
+  a.max_pages = c.max_pages;
+  a.layers = h->cfg.num_layers;
+  a.slabs = 2 * c.heads;
+  a.row_bytes = 2 * c.dim;
+  a.src = src;
+  a.dst = dst;
+  a.free_pages = free_pages;
+  a.lens = lens;
+  a.table = table;
+  a.free_count = free_count;
+  a.shared = shared;
+  a.tails = reinterpret_cast<unsigned char*>(c.tails);
+  a.layer_bytes = h->plan.layer_bytes;
+  a.status = c.status;
+  return done(kvq::launch_fork(a, h->sm_count, static_cast<cudaStream_t>(stream)), kvq::fork_launches(a), "fork launch");
+}
+
 kvq_status kvq_paged_write(kvq_paged_cache* h, int32_t layer, int32_t requests, const void* k, const void* v,
                            int64_t k_stride, int64_t v_stride, int32_t max_tokens, const int32_t* cu_tokens,
                            const int32_t* slots, const int32_t* lens, void* stream) {
@@ -376,6 +456,121 @@ kvq_status kvq_paged_decode_attention(kvq_paged_cache* h, int32_t layer, int32_t
               "paged decode launch");
 }
 
+kvq_status kvq_paged_attention_workspace_bytes(const kvq_paged_cache* h, int32_t num_q_heads, size_t* bytes) {
+  if (!h) return fail(KVQ_ERR_INVALID_ARG, "cache handle is NULL");
+  if (!bytes) return fail(KVQ_ERR_INVALID_ARG, "bytes is NULL");
+  const int hkv = h->cfg.num_kv_heads;
+  if (num_q_heads < hkv || num_q_heads % hkv != 0 || num_q_heads > 65535)
+    return fail(KVQ_ERR_INVALID_ARG, "num_q_heads %d must be a multiple of num_kv_heads %d and at most 65535",
+                num_q_heads, hkv);
+  *bytes = kvq::paged_attn_workspace(h->cfg.head_dim, h->sm_count);
+  return KVQ_OK;
+}
+
+kvq_status kvq_paged_attention(kvq_paged_cache* h, int32_t layer, int32_t requests, const void* q, int64_t q_stride,
+                               int32_t max_tokens, int32_t num_q_heads, const int32_t* cu_tokens,
+                               const int32_t* table, const int32_t* lens, float softmax_scale, void* out,
+                               void* workspace, size_t ws_bytes, void* stream) {
+  kvq_status s = check_layer(h, layer);
+  if (s == KVQ_OK) s = check_handle(h);
+  if (s == KVQ_OK) s = check_requests(h, requests);
+  size_t need = 0;
+  if (s == KVQ_OK) s = kvq_paged_attention_workspace_bytes(h, num_q_heads, &need);
+  if (s != KVQ_OK) return s;
+  if (max_tokens < 0) return fail(KVQ_ERR_INVALID_ARG, "max_tokens must be >= 0");
+  if (max_tokens > 1 << 26) return fail(KVQ_ERR_UNSUPPORTED, "max_tokens %d exceeds 2^26", max_tokens);
+  if (!(softmax_scale >= 0.0f && softmax_scale < 2.0e38f))
+    return fail(KVQ_ERR_INVALID_ARG, "softmax_scale must be finite and >= 0");
+  if (max_tokens == 0) return KVQ_OK;
+  s = check_row("q", q, q_stride, (int64_t)num_q_heads * h->cfg.head_dim);
+  if (s == KVQ_OK) s = check_ints({cu_tokens, table, lens});
+  if (s != KVQ_OK) return s;
+  if (!out || !workspace) return fail(KVQ_ERR_INVALID_ARG, "out and workspace must not be NULL");
+  if (!aligned(out, 16) || !aligned(workspace, 16))
+    return fail(KVQ_ERR_INVALID_ARG, "out and workspace must be 16-byte aligned");
+  if (ws_bytes < need) return fail(KVQ_ERR_BUFFER_TOO_SMALL, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  kvq::PagedAttnArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.tokens = max_tokens;
+  a.requests = requests;
+  a.q_heads = num_q_heads;
+  a.group = num_q_heads / h->cfg.num_kv_heads;
+  a.cu = cu_tokens;
+  a.table = table;
+  a.lens = lens;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.out = static_cast<uint16_t*>(out);
+  a.ws = workspace;
+  a.sm_count = h->sm_count;
+  return done(kvq::launch_paged_attention(layer_dev(h, layer), a, static_cast<cudaStream_t>(stream)), 1,
+              "paged attention launch");
+}
+
+kvq_status kvq_norm_rotate(const void* q, const void* k, int64_t q_stride, int64_t k_stride, int32_t tokens,
+                           int32_t num_q_heads, int32_t num_k_heads, int32_t head_dim, int32_t dtype,
+                           const int32_t* positions, const uint64_t* turns, int32_t rot_dim, int32_t interleaved,
+                           float magnitude, const float* q_weight, const float* k_weight, float eps, void* q_out,
+                           void* k_out, int64_t q_out_stride, int64_t k_out_stride, void* stream) {
+  if (head_dim != 64 && head_dim != 128) return fail(KVQ_ERR_UNSUPPORTED, "head_dim %d must be 64 or 128", head_dim);
+  if (dtype != KVQ_F16 && dtype != KVQ_BF16)
+    return fail(KVQ_ERR_INVALID_ARG, "dtype %d must be KVQ_F16 or KVQ_BF16", dtype);
+  if (num_q_heads < 0 || num_q_heads > 65535 || num_k_heads < 0 || num_k_heads > 65535)
+    return fail(KVQ_ERR_INVALID_ARG, "num_q_heads %d and num_k_heads %d must be in [0, 65535]", num_q_heads, num_k_heads);
+  if (tokens < 0) return fail(KVQ_ERR_INVALID_ARG, "tokens must be >= 0");
+  if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 8 != 0)
+    return fail(KVQ_ERR_INVALID_ARG, "rot_dim %d must be a multiple of 8 in [0, %d]", rot_dim, head_dim);
+  if (!(magnitude > -3.0e38f && magnitude < 3.0e38f)) return fail(KVQ_ERR_INVALID_ARG, "magnitude must be finite");
+  if (!(eps >= 0.0f && eps < 3.0e38f)) return fail(KVQ_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (tokens == 0 || num_q_heads + num_k_heads == 0) return KVQ_OK;
+  kvq_status s = KVQ_OK;
+  if (num_q_heads > 0) {
+    const int64_t row = (int64_t)num_q_heads * head_dim;
+    s = check_row("q", q, q_stride, row);
+    if (s == KVQ_OK) s = check_row("q_out", q_out, q_out_stride, row);
+    if (s == KVQ_OK && q == q_out && q_stride != q_out_stride)
+      s = fail(KVQ_ERR_INVALID_ARG, "q_out is q with another stride");
+  }
+  if (s == KVQ_OK && num_k_heads > 0) {
+    const int64_t row = (int64_t)num_k_heads * head_dim;
+    s = check_row("k", k, k_stride, row);
+    if (s == KVQ_OK) s = check_row("k_out", k_out, k_out_stride, row);
+    if (s == KVQ_OK && k == k_out && k_stride != k_out_stride)
+      s = fail(KVQ_ERR_INVALID_ARG, "k_out is k with another stride");
+  }
+  if (s != KVQ_OK) return s;
+  if (!positions || (rot_dim > 0 && !turns)) return fail(KVQ_ERR_INVALID_ARG, "positions and turns must not be NULL");
+  if (!aligned(positions, 4) || !aligned(turns, 8) || !aligned(q_weight, 16) || !aligned(k_weight, 16))
+    return fail(KVQ_ERR_INVALID_ARG, "weights must be 16-byte, turns 8-byte, positions 4-byte aligned");
+  s = check_device({num_q_heads ? q : nullptr, num_q_heads ? q_out : nullptr, num_k_heads ? k : nullptr,
+                    num_k_heads ? k_out : nullptr, positions, rot_dim ? turns : nullptr, q_weight, k_weight},
+                   "q, k, q_out, k_out, positions, turns and the weights");
+  if (s != KVQ_OK) return s;
+  kvq::RotateArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_out_stride = k_out_stride;
+  a.tokens = tokens;
+  a.q_heads = num_q_heads;
+  a.k_heads = num_k_heads;
+  a.dim = head_dim;
+  a.dtype = dtype;
+  a.rot = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.positions = positions;
+  a.turns = turns;
+  a.magnitude = magnitude;
+  a.eps = eps;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  return done(kvq::launch_norm_rotate(a, static_cast<cudaStream_t>(stream)), 1, "norm and rotation launch");
+}
+
 kvq_status kvq_prompt_attention(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
                                 int64_t v_stride, int32_t max_tokens, int32_t num_seqs, const int32_t* cu_tokens,
                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
@@ -403,18 +598,8 @@ kvq_status kvq_prompt_attention(const void* q, const void* k, const void* v, int
     return fail(KVQ_ERR_INVALID_ARG, "out must be 16-byte, cu_tokens and status 4-byte aligned");
   if (!(softmax_scale >= 0.0f && softmax_scale < 2.0e38f))
     return fail(KVQ_ERR_INVALID_ARG, "softmax_scale must be finite and >= 0");
-  int dev = -1;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  for (const void* p : {q, k, v, (const void*)out, (const void*)cu_tokens, (const void*)status}) {
-    if (!p) continue;
-    cudaPointerAttributes attr;
-    e = cudaPointerGetAttributes(&attr, p);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaPointerGetAttributes");
-    if ((attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged) || attr.device != dev)
-      return fail(KVQ_ERR_INVALID_ARG, "q, k, v, out, cu_tokens and status must be memory of the current device %d",
-                  dev);
-  }
+  s = check_device({q, k, v, out, cu_tokens, status}, "q, k, v, out, cu_tokens and status");
+  if (s != KVQ_OK) return s;
   kvq::PromptArgs a;
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);

@@ -1,0 +1,148 @@
+// Norm of query and key heads and rotation by position in one pass
+// (kvq_norm_rotate).
+//
+//   y = x / sqrt(mean(x^2) + eps) * w,  (a, b) -> (a cos t - b sin t, b cos t + a sin t),  t = position * f_j
+//
+// Bound by bytes: every row is read once and written once. D / 8 lanes hold a
+// head's row, eight channels each, such that both channels of a pair are in one
+// lane: two runs of four, `rot / 2` apart (or side by side for neighbouring
+// pairs), so the rotation needs no exchange and the norm one sum over the
+// lanes. A lane's four pairs are the same in every head: a warp makes a token's
+// sines and cosines once and takes the token's heads in turn.
+//
+// The angle is kept in turns as a 64-bit fraction: position * turns[j] mod 2^64
+// is exact, its upper half goes to sincospif (2^-25 of half a turn off), so a
+// position of a million is as good as one of ten.
+#include "paged_internal.h"
+
+namespace kvq {
+namespace {
+
+constexpr int kWarps = 4;
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// `passes`: passes over 256 / D heads each that a warp makes of its token;
+// `parts`: warps of a token.
+template <int D, bool BF16, bool INTERLEAVED>
+__global__ void __launch_bounds__(kWarps * 32) norm_rotate_kernel(const RotateArgs a, const int passes, const int parts) {
+  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;  // lanes of a head, heads of a pass
+  const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
+  const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int token = (int)(task / parts), part = (int)(task % parts);
+  if (token >= a.tokens) return;
+  const int position = a.positions[token];
+  if (position < 0) return;
+  const int heads = a.q_heads + a.k_heads;
+
+  // the lane's channels: ch0 .. + 3 and ch1 .. + 3
+  const int rotated = a.rot / 8;  // lanes that hold pairs
+  const bool turn = l < rotated;
+  int ch0, ch1;
+  if (INTERLEAVED) {
+    ch0 = 8 * l, ch1 = 8 * l + 4;
+  } else if (turn) {
+    ch0 = 4 * l, ch1 = a.rot / 2 + 4 * l;
+  } else {
+    ch0 = 8 * l, ch1 = 8 * l + 4;
+  }
+  float c[4], s[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    c[j] = 1.0f, s[j] = 0.0f;
+    if (turn) {
+      const uint64_t t = (uint64_t)(uint32_t)position * a.turns[4 * l + j] + (1ull << 31);
+      sincospif((float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f, &s[j], &c[j]);
+      c[j] *= a.magnitude, s[j] *= a.magnitude;
+    }
+  }
+  float wq[8], wk[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    wq[j] = a.q_weight ? a.q_weight[ch0 + j] : 1.0f, wq[4 + j] = a.q_weight ? a.q_weight[ch1 + j] : 1.0f;
+    wk[j] = a.k_weight ? a.k_weight[ch0 + j] : 1.0f, wk[4 + j] = a.k_weight ? a.k_weight[ch1 + j] : 1.0f;
+  }
+  constexpr int kBatch = 4;  // passes whose loads are in flight together
+  const int last = min(heads, (part + 1) * passes * kHeads);
+  for (int h0 = part * passes * kHeads; h0 < last; h0 += kBatch * kHeads) {
+    uint2 x[kBatch][2];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * kHeads + sub;
+      if (h >= last) continue;
+      const uint16_t* row = h < a.q_heads ? a.q + token * a.q_stride + (int64_t)h * D
+                                          : a.k + token * a.k_stride + (int64_t)(h - a.q_heads) * D;
+      x[i][0] = *reinterpret_cast<const uint2*>(row + ch0);
+      x[i][1] = *reinterpret_cast<const uint2*>(row + ch1);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * kHeads + sub;
+      const bool is_q = h < a.q_heads;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float2 p = unpack2<BF16>(x[i][j].x), q = unpack2<BF16>(x[i][j].y);
+        v[4 * j] = p.x, v[4 * j + 1] = p.y, v[4 * j + 2] = q.x, v[4 * j + 3] = q.y;
+      }
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
+#pragma unroll
+      for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (h >= last) continue;
+      if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
+        const float r = rsqrtf(sum * (1.0f / D) + a.eps);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = v[j] * r * (is_q ? wq[j] : wk[j]);
+      }
+      if (turn) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float& p = INTERLEAVED ? v[2 * j] : v[j];
+          float& q = INTERLEAVED ? v[2 * j + 1] : v[4 + j];
+          const float y = p * c[j] - q * s[j];
+          q = q * c[j] + p * s[j];
+          p = y;
+        }
+      }
+      uint16_t* to = is_q ? a.q_out + token * a.q_out_stride + (int64_t)h * D
+                          : a.k_out + token * a.k_out_stride + (int64_t)(h - a.q_heads) * D;
+      *reinterpret_cast<uint2*>(to + ch0) = make_uint2(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]));
+      *reinterpret_cast<uint2*>(to + ch1) = make_uint2(pack2<BF16>(v[4], v[5]), pack2<BF16>(v[6], v[7]));
+    }
+  }
+}
+
+template <int D, bool BF16>
+cudaError_t launch(const RotateArgs& a, cudaStream_t st) {
+  constexpr int kHeads = 256 / D;
+  const int all = (a.q_heads + a.k_heads + kHeads - 1) / kHeads;
+  // few tokens: a warp a pass, for latency; many: the sines of a token serve all its heads
+  const int parts = a.tokens < 1024 ? (all + 3) / 4 : 1, passes = (all + parts - 1) / parts;
+  const int64_t grid = ((int64_t)a.tokens * parts + kWarps - 1) / kWarps;
+  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (a.interleaved) norm_rotate_kernel<D, BF16, true><<<(unsigned)grid, kWarps * 32, 0, st>>>(a, passes, parts);
+  else norm_rotate_kernel<D, BF16, false><<<(unsigned)grid, kWarps * 32, 0, st>>>(a, passes, parts);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rotate(const RotateArgs& a, cudaStream_t st) {
+  if (a.dim == 64) return a.dtype == KVQ_BF16 ? launch<64, true>(a, st) : launch<64, false>(a, st);
+  return a.dtype == KVQ_BF16 ? launch<128, true>(a, st) : launch<128, false>(a, st);
+}
+
+}  // namespace kvq

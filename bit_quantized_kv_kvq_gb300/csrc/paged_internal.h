@@ -45,6 +45,23 @@ struct ReleaseArgs {
 };
 cudaError_t launch_release(const ReleaseArgs& a, cudaStream_t st);
 
+struct ReleaseSharedArgs {
+  ReleaseArgs r;
+  int32_t* shared;
+};
+cudaError_t launch_release_shared(const ReleaseSharedArgs& a, cudaStream_t st);
+
+struct ForkArgs {
+  int requests, pairs, page_shift, num_pages, max_pages, layers, slabs, row_bytes;  // slabs: heads times 2
+  const int32_t *src, *dst, *free_pages;
+  int32_t *lens, *table, *free_count, *shared;
+  unsigned char* tails;  // of layer 0
+  int64_t layer_bytes;
+  uint32_t* status;
+};
+int fork_launches(const ForkArgs& a);
+cudaError_t launch_fork(const ForkArgs& a, int sm_count, cudaStream_t st);
+
 struct PagedWriteArgs {
   const uint16_t *k, *v;
   int64_t k_stride, v_stride;  // elements between tokens
@@ -66,6 +83,31 @@ struct PagedDecodeArgs {
 };
 size_t paged_decode_workspace(int dim, int group, int requests, int sm_count);
 cudaError_t launch_paged_decode(const PagedDev& c, const PagedDecodeArgs& a, cudaStream_t st);
+
+struct PagedAttnArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  int tokens, requests, q_heads, group;
+  const int32_t *cu, *table, *lens;  // lens: after the step
+  float scale_log2;
+  uint16_t* out;
+  void* ws;
+  int sm_count;
+};
+size_t paged_attn_workspace(int dim, int sm_count);
+cudaError_t launch_paged_attention(const PagedDev& c, const PagedAttnArgs& a, cudaStream_t st);
+
+struct RotateArgs {
+  const uint16_t *q, *k;
+  uint16_t *q_out, *k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  int tokens, q_heads, k_heads, dim, dtype, rot, interleaved;
+  const int32_t* positions;
+  const uint64_t* turns;
+  float magnitude, eps;
+  const float *q_weight, *k_weight;
+};
+cudaError_t launch_norm_rotate(const RotateArgs& a, cudaStream_t st);
 
 struct PromptArgs {
   const uint16_t *q, *k, *v;

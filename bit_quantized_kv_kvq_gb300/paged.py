@@ -5,11 +5,17 @@ A step::
 
     plan = cache.reserve(lens, new_tokens, table, free_pages, free_count, max_tokens)
     for layer in range(num_layers):
+        q, k = norm_rotate(q, k, plan.positions, rotation, q_weight, k_weight)           # where the model has it
         cache.write(layer, k, v, plan.cu_tokens, plan.slots, plan.lens)
-        o = prompt_attention(q, k, v, plan.cu_tokens, scale, status=cache.status_word)   # prompts, or
-        o = cache.decode(layer, q, table, plan.lens, scale)                              # one token per request
+        o = prompt_attention(q, k, v, plan.cu_tokens, scale, status=cache.status_word)   # whole prompts, or
+        o = cache.decode(layer, q, table, plan.lens, scale)                              # one token per request, or
+        o = cache.attend(layer, q, plan.cu_tokens, table, plan.lens, scale)              # any number of each
     cache.release(done, plan.lens, table, free_pages, plan.free_count)
     cache.status()                                               # whether a call found something amiss
+
+Requests may branch: ``cache.fork(src, dst, plan.lens, table, free_pages,
+plan.free_count, shared)`` makes requests ``dst`` of requests ``src``, on the same complete
+pages, and ``release(..., shared=shared)`` gives a page back with its last holder.
 
 Lengths, tables, slots and the free list are int32 tensors on the cache's
 device; no call copies them to the host, so a step can be captured into a CUDA
@@ -18,7 +24,9 @@ graph and replayed.
 from __future__ import annotations
 
 import ctypes
+import math
 from collections import namedtuple
+from fractions import Fraction
 
 import torch
 
@@ -49,11 +57,19 @@ SIGNATURES = {
     "kvq_paged_cache_status": [_P, _P, ctypes.POINTER(ctypes.c_uint32)],
     "kvq_paged_reserve": [_P, _I] + [_P] * 5 + [_I] + [_P] * 6,
     "kvq_paged_release": [_P, _I] + [_P] * 6,
+    "kvq_paged_release_shared": [_P, _I] + [_P] * 7,
+    "kvq_paged_fork": [_P, _I, _I] + [_P] * 8,
     "kvq_paged_write": [_P, _I, _I, _P, _P, _L, _L, _I, _P, _P, _P, _P],
     "kvq_paged_decode_workspace_bytes": [_P, _I, ctypes.POINTER(ctypes.c_size_t)],
     "kvq_paged_decode_attention": [_P, _I, _I, _P, _L, _I, _P, _P, ctypes.c_float, _P, _I, _P, ctypes.c_size_t, _P],
+    "kvq_paged_attention_workspace_bytes": [_P, _I, ctypes.POINTER(ctypes.c_size_t)],
+    "kvq_paged_attention": [_P, _I, _I, _P, _L, _I, _I, _P, _P, _P, ctypes.c_float, _P, _P, ctypes.c_size_t, _P],
+    "kvq_norm_rotate": [_P, _P, _L, _L] + [_I] * 5 + [_P, _P, _I, _I, ctypes.c_float, _P, _P, ctypes.c_float, _P, _P,
+                                                      _L, _L, _P],
     "kvq_prompt_attention": [_P, _P, _P, _L, _L, _L, _I, _I, _P, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P],
 }
+
+_TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510")
 
 #: What reserve() planned: prefix sums of the new tokens, the slot and the
 #: position of each packed token, the lengths and the free count after the step.
@@ -197,15 +213,34 @@ class PagedKVCache:
             max_tokens, cu_p, slots_p, positions_p, lo_p, fo_p, _raw_stream(stream, dev)))
         return plan
 
-    def release(self, done, lens, table, free_pages, free_count, stream=None):
-        """Ends the requests with done != 0 (kvq_paged_release), in place."""
+    def release(self, done, lens, table, free_pages, free_count, stream=None, shared=None):
+        """Ends the requests with done != 0, in place (kvq_paged_release; with
+        ``shared``, as fork() keeps it, kvq_paged_release_shared)."""
         lib = _lib or _bind()
         dev = self.device
         r = lens.shape[0]
-        _check(lib.kvq_paged_release(
-            self.handle, r, _ints(done, "done", (r,), dev), _ints(lens, "lens", (r,), dev),
+        args = (self.handle, r, _ints(done, "done", (r,), dev), _ints(lens, "lens", (r,), dev),
+                _ints(table, "table", (r, self._table_pages), dev), _ints(free_pages, "free_pages", (self._all_pages,), dev),
+                _ints(free_count, "free_count", (1,), dev))
+        raw = _raw_stream(stream, dev)
+        if shared is None:
+            _check(lib.kvq_paged_release(*args, raw))
+        else:
+            _check(lib.kvq_paged_release_shared(*args, _ints(shared, "shared", (self._all_pages,), dev), raw))
+
+    def fork(self, src, dst, lens, table, free_pages, free_count, shared, stream=None):
+        """Request dst[i], which is empty, becomes a copy of request src[i] on the
+        same complete pages, in place (kvq_paged_fork); pairs with src[i] < 0 are left
+        out. ``shared``: int32 [pages], zeros where nothing is shared yet; requests that
+        share pages end by release(..., shared=shared)."""
+        lib = _lib or _bind()
+        dev = self.device
+        r, n = lens.shape[0], src.shape[0]
+        _check(lib.kvq_paged_fork(
+            self.handle, r, n, _ints(src, "src", (n,), dev), _ints(dst, "dst", (n,), dev), _ints(lens, "lens", (r,), dev),
             _ints(table, "table", (r, self._table_pages), dev), _ints(free_pages, "free_pages", (self._all_pages,), dev),
-            _ints(free_count, "free_count", (1,), dev), _raw_stream(stream, dev)))
+            _ints(free_count, "free_count", (1,), dev), _ints(shared, "shared", (self._all_pages,), dev),
+            _raw_stream(stream, dev)))
 
     def write(self, layer, k, v, cu_tokens, slots, lens, stream=None):
         """Writes the step's packed tokens (kvq_paged_write). ``lens``: the
@@ -222,20 +257,22 @@ class PagedKVCache:
                                   _ints(cu_tokens, "cu_tokens", (r + 1,), dev), _ints(slots, "slots", (t,), dev),
                                   _ints(lens, "lens", (r,), dev), _raw_stream(stream, dev)))
 
-    def workspace_bytes(self, num_q_heads):
-        n = self._ws_bytes.get(num_q_heads)
+    def workspace_bytes(self, num_q_heads, attend=False):
+        """Bytes of a workspace of decode(), or of attend()."""
+        n = self._ws_bytes.get((num_q_heads, attend))
         if n is None:
             size = ctypes.c_size_t()
-            _check(_lib.kvq_paged_decode_workspace_bytes(self.handle, num_q_heads, ctypes.byref(size)))
-            n = self._ws_bytes[num_q_heads] = size.value
+            f = _lib.kvq_paged_attention_workspace_bytes if attend else _lib.kvq_paged_decode_workspace_bytes
+            _check(f(self.handle, num_q_heads, ctypes.byref(size)))
+            n = self._ws_bytes[num_q_heads, attend] = size.value
         return n
 
-    def _workspace(self, hq, raw, stream):
+    def _workspace(self, hq, raw, stream, attend=False):
         if _captured(stream):
-            return _empty(self.workspace_bytes(hq), torch.uint8, self.device, stream)
-        ws = self._ws.get((hq, raw))
+            return _empty(self.workspace_bytes(hq, attend), torch.uint8, self.device, stream)
+        ws = self._ws.get((hq, attend, raw))
         if ws is None:
-            ws = self._ws[hq, raw] = _empty(self.workspace_bytes(hq), torch.uint8, self.device, stream)
+            ws = self._ws[hq, attend, raw] = _empty(self.workspace_bytes(hq, attend), torch.uint8, self.device, stream)
         return ws
 
     def decode(self, layer, q, table, lens, softmax_scale, out=None, out_dtype=None, workspace=None, stream=None):
@@ -263,6 +300,34 @@ class PagedKVCache:
             self.handle, layer, r, qp, qs, hq, _ints(table, "table", (r, self._table_pages), dev),
             _ints(lens, "lens", (r,), dev), softmax_scale, out.data_ptr(), _DTYPES[out.dtype], ws.data_ptr(), ws.nbytes,
             raw))
+        return out
+
+    def attend(self, layer, q, cu_tokens, table, lens, softmax_scale, out=None, workspace=None, stream=None):
+        """Attention of a step's packed new tokens, any number of each request, over
+        all that the cache holds of it with them, causally (kvq_paged_attention; call
+        after write()): q [tokens][H_q][D] -> out [tokens][H_q][D]. cu_tokens, lens: as
+        reserve() planned the step. Rows of ``out`` outside every request are left
+        as they are (uninitialised where ``out`` is not given). ``workspace``: as in decode()."""
+        lib = _lib or _bind()
+        dev = self.device
+        qp, qs = _rows(q, "q", self.dtype, dev, dim=self._dim)
+        t, hq, d = q.shape
+        r = lens.shape[0]
+        if out is None:
+            out = _empty((t, hq, d), self.dtype, dev, stream)
+        elif tuple(out.shape) != (t, hq, d) or out.device != dev or not out.is_contiguous() or out.dtype != self.dtype:
+            raise ValueError("out must be a contiguous %s tensor of shape %s on %s" % (self.dtype, (t, hq, d), dev))
+        raw = _raw_stream(stream, dev)
+        if workspace is None:
+            ws = self._workspace(hq, raw, stream, True)
+        else:
+            ws = workspace
+            if not isinstance(ws, _Tensor) or ws.device != dev or not ws.is_contiguous():
+                raise TypeError("workspace must be a contiguous tensor on %s" % dev)
+        _check(lib.kvq_paged_attention(
+            self.handle, layer, r, qp, qs, t, hq, _ints(cu_tokens, "cu_tokens", (r + 1,), dev),
+            _ints(table, "table", (r, self._table_pages), dev), _ints(lens, "lens", (r,), dev), softmax_scale,
+            out.data_ptr(), ws.data_ptr(), ws.nbytes, raw))
         return out
 
     # -- inspection ---------------------------------------------------------
@@ -312,6 +377,80 @@ class PagedKVCache:
             self.close()
         except Exception:
             pass
+
+
+class Rotation:
+    """Rotation by position, for norm_rotate: pair j of a row's first
+    ``2 * len(inv_freq)`` channels is turned by position * inv_freq[j] radians. Pairs are
+    channels (j, j + len(inv_freq)), or neighbours where ``interleaved``; the rotated
+    channels are multiplied by ``magnitude``. len(inv_freq) is a multiple of 4."""
+
+    def __init__(self, inv_freq, interleaved=False, magnitude=1.0, device=None):
+        freq = [float(f) for f in inv_freq]
+        if len(freq) % 4 != 0:
+            raise ValueError("inv_freq has %d frequencies, a multiple of 4 is needed" % len(freq))
+        if not all(math.isfinite(f) for f in freq):
+            raise ValueError("inv_freq must be finite")
+        self.dim, self.interleaved, self.magnitude = 2 * len(freq), bool(interleaved), float(magnitude)
+        # turns a position as a 64-bit fraction; a negative frequency turns back
+        turns = [round(Fraction(f) / _TWO_PI * 2 ** 64) % 2 ** 64 for f in freq]
+        signed = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
+        #: The turns' bits, int64 on the device.
+        self.turns = torch.tensor(signed, dtype=torch.int64, device=device if device is not None else "cuda")
+
+    @classmethod
+    def standard(cls, dim, theta=10000.0, **kw):
+        """theta^(-2 j / dim) for the pairs of ``dim`` channels."""
+        return cls([theta ** (-2.0 * j / dim) for j in range(dim // 2)], **kw)
+
+
+def _head_rows(x, out, name, stream):
+    """Pointer, stride and heads of rows, and the same of their output."""
+    if not isinstance(x, _Tensor) or x.dtype not in (torch.float16, torch.bfloat16) or not x.is_cuda:
+        raise TypeError("%s must be a CUDA float16 or bfloat16 tensor" % name)
+    p, s = _rows(x, name, x.dtype, x.device)
+    t, h, d = x.shape
+    if out is None:
+        out = _empty((t, h, d), x.dtype, x.device, stream)
+    op, os = _rows(out, name + "_out", x.dtype, x.device, heads=h, dim=d)
+    if out.shape[0] != t:
+        raise ValueError("%s_out holds %d tokens, expected %d" % (name, out.shape[0], t))
+    return out, p, s, h, op, os
+
+
+def _weight(w, name, d, device):
+    if w is None:
+        return None
+    if not isinstance(w, _Tensor) or w.dtype is not torch.float32 or w.device != device:
+        raise TypeError("%s must be a float32 tensor on %s" % (name, device))
+    if w.shape != (d,) or not w.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of shape (%d,)" % (name, d))
+    return w.data_ptr()
+
+
+def norm_rotate(q, k, positions, rotation, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Norm of each head and rotation by position in one pass (kvq_norm_rotate): q
+    [tokens][H_q][D], k [tokens][H_k][D] in fp16 or bf16, positions int32 [tokens]
+    (reserve()'s), rotation a Rotation. Without a weight (fp32 [D]) there is no norm.
+    Returns (q, k) rotated: new tensors, or ``q_out`` / ``k_out``, which may be q and k
+    themselves. Rows of tokens with a negative position are left as they are there."""
+    lib = _lib or _bind()
+    q_out, qp, qs, hq, qop, qos = _head_rows(q, q_out, "q", stream)
+    k_out, kp, ks, hk, kop, kos = _head_rows(k, k_out, "k", stream)
+    t, _, d = q.shape
+    dev = q.device
+    if k.dtype is not q.dtype or k.device != dev:
+        raise TypeError("q and k must have the same type and device")
+    if k.shape[0] != t or k.shape[2] != d:
+        raise ValueError("q has shape %s, k %s" % (tuple(q.shape), tuple(k.shape)))
+    turns = rotation.turns
+    if turns.device != dev:
+        raise TypeError("the rotation must be on %s" % dev)
+    _check(lib.kvq_norm_rotate(
+        qp, kp, qs, ks, t, hq, hk, d, _DTYPES[q.dtype], _ints(positions, "positions", (t,), dev), turns.data_ptr(),
+        rotation.dim, rotation.interleaved, rotation.magnitude, _weight(q_weight, "q_weight", d, dev),
+        _weight(k_weight, "k_weight", d, dev), eps, qop, kop, qos, kos, _raw_stream(stream, dev)))
+    return q_out, k_out
 
 
 def prompt_attention(q, k, v, cu_tokens, softmax_scale, out=None, status=None, stream=None):

@@ -382,9 +382,12 @@ KVQ_API kvq_status kvq_cache_status(kvq_cache* cache, void* stream, uint32_t* wo
  * arrays, must be ordered on the GPU; decodes of one layer may overlap, each
  * with a workspace of its own.
  *
- * A step: kvq_paged_reserve once; then per layer kvq_paged_write, and
- * kvq_prompt_attention for prompts or kvq_paged_decode_attention for single
- * tokens; kvq_paged_release when requests end.
+ * A step: kvq_paged_reserve once; then per layer kvq_norm_rotate (by the step's
+ * positions) and kvq_paged_write, and kvq_prompt_attention for whole prompts,
+ * kvq_paged_decode_attention for single tokens or kvq_paged_attention for any
+ * mix of chunks, drafts and single tokens; kvq_paged_release when requests end.
+ * kvq_paged_fork branches requests, which then share pages and end by
+ * kvq_paged_release_shared.
  * ------------------------------------------------------------------------ */
 typedef enum kvq_page_code { KVQ_PAGE_INT8 = 0, KVQ_PAGE_E4M3 = 1 } kvq_page_code;
 
@@ -472,6 +475,36 @@ KVQ_API kvq_status kvq_paged_reserve(kvq_paged_cache* cache, int32_t requests, c
 KVQ_API kvq_status kvq_paged_release(kvq_paged_cache* cache, int32_t requests, const int32_t* done, int32_t* lens,
                                      const int32_t* table, int32_t* free_pages, int32_t* free_count, void* stream);
 
+/* Release of requests whose pages others may hold too. shared: int32
+ * [num_pages], for each page the number of its holders beyond the first (0 for a
+ * page of one request, and for those on the stack; kvq_paged_fork keeps it). As
+ * kvq_paged_release, but every released table entry gives up one holder, and a
+ * page goes onto the stack only with its last one: in the order (of request and
+ * position) of the last released entry that names it. A page that is released
+ * more often than held goes back once and sets the status word, an entry out of
+ * range is left out and sets it too. At most 2^30 - 1 entries are released by one call
+ * (more set the status word and change nothing). One launch. */
+KVQ_API kvq_status kvq_paged_release_shared(kvq_paged_cache* cache, int32_t requests, const int32_t* done,
+                                            int32_t* lens, const int32_t* table, int32_t* free_pages,
+                                            int32_t* free_count, int32_t* shared, void* stream);
+
+/* Forks requests: for each i < pairs with src[i] >= 0, request dst[i], which holds
+ * no tokens, becomes a copy of request src[i] as it is before the call. Its table row
+ * names the source's complete pages (one more holder each in `shared`, see
+ * kvq_paged_release_shared); for a source with an open page it takes a page of its own
+ * off the stack, in order of i, and the open rows are copied in every layer's
+ * tails. lens[dst[i]] becomes the source's length. A source may be named by
+ * several pairs, a destination by one. pairs <= max_requests. All or nothing:
+ * where a slot or a length is out of range, a destination holds tokens, is named
+ * twice or is its own source, a page off the stack is not one of the cache's, or
+ * the stack is too short, nothing changes and the status word is set. (A source's
+ * table entry out of range is copied as it is, counts no holder and sets the status
+ * word.) Entries past the copied ones stay as they are. All arrays int32 on
+ * the device. One launch, two where the pairs' tails have room for more than 64 KiB. */
+KVQ_API kvq_status kvq_paged_fork(kvq_paged_cache* cache, int32_t requests, int32_t pairs, const int32_t* src,
+                                  const int32_t* dst, int32_t* lens, int32_t* table, const int32_t* free_pages,
+                                  int32_t* free_count, int32_t* shared, void* stream);
+
 /* Writes the step's packed tokens into layer `layer`. k, v: [max_tokens]
  * [H_kv][D] in the config's dtype, token rows k_stride / v_stride elements
  * apart (multiples of 8, >= H_kv * D). cu_tokens, slots: as reserve wrote
@@ -503,6 +536,61 @@ KVQ_API kvq_status kvq_paged_decode_attention(kvq_paged_cache* cache, int32_t la
                                               int64_t q_stride, int32_t num_q_heads, const int32_t* table,
                                               const int32_t* lens, float softmax_scale, void* out,
                                               int32_t out_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of kvq_paged_attention for num_q_heads query heads and any
+ * number of requests up to max_requests. Host only. */
+KVQ_API kvq_status kvq_paged_attention_workspace_bytes(const kvq_paged_cache* cache, int32_t num_q_heads,
+                                                       size_t* bytes);
+
+/* Attention of a step's new tokens over all that the cache holds, after
+ * kvq_paged_write of the step: request b has m = cu_tokens[b + 1] - cu_tokens[b]
+ * new tokens, any number from 0 on (a chunk of a prompt, drafted tokens to check, a
+ * single token), and holds n = lens[b] tokens with them. Its token i sits at
+ * position p = n - m + i and attends positions 0 .. p of its pages and tail:
+ *   e_t = softmax_scale * <q_i, k_hat_t>,  o_i = sum_{t <= p} softmax(e)_t v_hat_t,
+ * with k_hat, v_hat as kvq_paged_decode_attention reads them: tokens of this
+ * step whose page is complete count as they are coded.
+ * q: [max_tokens][H_q][D] in the config's dtype, token rows q_stride elements apart
+ * (a multiple of 8, >= H_q * D); H_q any multiple of H_kv. cu_tokens
+ * [requests + 1], table, lens as kvq_paged_reserve left them (lens AFTER the step);
+ * cu_tokens need not start at 0. out: [max_tokens][H_q][D] in the config's dtype;
+ * rows outside every request are left as they are. A request with a length
+ * or range out of bounds is left out and sets the status word; so is a page out of range.
+ * In the open page a later token does not reach an earlier one, not even by an
+ * infinity or NaN; a complete page that took one in reads as NaN for every token that
+ * attends any of it. softmax_scale: finite and >= 0; weights are rounded to the config's
+ * dtype, sums are fp32 (tokens * 2^15 * |v| must stay below 3e38). max_tokens <=
+ * 2^26. workspace: 16-byte aligned, any content, not shared with calls that
+ * overlap on the GPU. One launch. */
+KVQ_API kvq_status kvq_paged_attention(kvq_paged_cache* cache, int32_t layer, int32_t requests, const void* q,
+                                       int64_t q_stride, int32_t max_tokens, int32_t num_q_heads,
+                                       const int32_t* cu_tokens, const int32_t* table, const int32_t* lens,
+                                       float softmax_scale, void* out, void* workspace, size_t ws_bytes,
+                                       void* stream);
+
+/* Norm and position rotation of queries and keys in one pass, before
+ * kvq_paged_write and the attention. For each token and head row x of D channels:
+ *   y = x / sqrt(mean(x^2) + eps) * w       (w NULL: y = x)
+ * then the pairs (a, b) of y's first rot_dim channels, j = 0 .. rot_dim / 2 - 1, become
+ *   (a cos t - b sin t, b cos t + a sin t) * magnitude,  t = position * f_j,
+ * and the others stay (without the magnitude). Pair j is channels (j, j + rot_dim / 2), or
+ * (2 j, 2 j + 1) where `interleaved` is not 0. turns[j] = round(f_j / (2 pi) *
+ * 2^64) mod 2^64 (uint64, on the device): a position's angle is reduced in integers, so
+ * that far positions lose nothing. Norm and rotation are fp32, rounded once (the sum
+ * of squares of a row must stay below 3e38).
+ * q [tokens][H_q][D] and k [tokens][H_k][D] in dtype (KVQ_F16 or KVQ_BF16), D 64 or 128;
+ * either may be NULL with 0 heads. Token rows *_stride elements apart (multiples of 8,
+ * no less than a row). q_out, k_out: as q and k, with strides of their own; they may be
+ * q and k themselves (with the same stride), else must not overlap them. q_weight, k_weight: fp32 [D] or
+ * NULL. positions: int32 [tokens] (kvq_paged_reserve's); a token whose position is negative is
+ * left out, its output rows as they are. rot_dim: a multiple of 8 in [0, D]. eps >= 0.
+ * 16-byte aligned pointers, all of the current device. One launch. */
+KVQ_API kvq_status kvq_norm_rotate(const void* q, const void* k, int64_t q_stride, int64_t k_stride, int32_t tokens,
+                                   int32_t num_q_heads, int32_t num_k_heads, int32_t head_dim, int32_t dtype,
+                                   const int32_t* positions, const uint64_t* turns, int32_t rot_dim,
+                                   int32_t interleaved, float magnitude, const float* q_weight,
+                                   const float* k_weight, float eps, void* q_out, void* k_out,
+                                   int64_t q_out_stride, int64_t k_out_stride, void* stream);
 
 /* Causal attention over whole prompts, packed one after the other, on their
  * own keys and values (no cache): token i of a sequence attends tokens 0 .. i

@@ -142,3 +142,59 @@ def prompt_attention(q, k, v, cu, scale):
             for i in range(lo, hi):
                 o[i, h], w[i, h], size[i, h] = attend(q[i, h], k[lo:i + 1, h // g], v[lo:i + 1, h // g], scale)
     return o, w, size
+
+
+def fork(src, dst, lens, table, free_pages, free_count, shared, page):
+    """(lens, table, free_count, shared) after the forks, or None where they are refused."""
+    lens, table, shared, count = lens.copy(), table.copy(), shared.copy(), int(free_count)
+    before = lens.copy()
+    taken = set()
+    for s, d in zip(src.tolist(), dst.tolist()):
+        if s < 0:
+            continue
+        if s >= len(lens) or not 0 <= d < len(lens) or s == d or d in taken or before[d] != 0:
+            return None
+        if not 0 <= before[s] <= table.shape[1] * page:
+            return None
+        taken.add(d)
+        full = int(before[s]) // page
+        for j in range(full):
+            table[d, j] = table[s, j]
+            shared[table[s, j]] += 1
+        if before[s] % page:
+            count -= 1
+            if count < 0 or not 0 <= free_pages[count] < len(shared):
+                return None
+            table[d, full] = free_pages[count]
+        lens[d] = before[s]
+    return lens, table, count, shared
+
+
+def release_shared(done, lens, table, free_pages, free_count, shared, page):
+    """(lens, free_pages, free_count, shared): pages whose last holder ends, in the order of that."""
+    lens, free_pages, shared, count = lens.copy(), free_pages.copy(), shared.copy(), int(free_count)
+    for b in np.flatnonzero(done):
+        for j in range(-(-int(lens[b]) // page)):
+            p = table[b, j]
+            if shared[p] == 0:
+                free_pages[count] = p
+                count += 1
+            else:
+                shared[p] -= 1
+        lens[b] = 0
+    return lens, free_pages, count, shared
+
+
+def rotate(x, positions, inv_freq, interleaved=False, magnitude=1.0, weight=None, eps=1e-6):
+    """Norm and rotation of rows x [token][head][channel] in fp64, and what the
+    bound of the fp32 form goes by: the rotated pairs' magnitude at each channel."""
+    x = np.asarray(x, np.float64)
+    y = x if weight is None else x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * weight
+    n = len(inv_freq)
+    t = np.asarray(positions, np.float64)[:, None, None] * np.asarray(inv_freq, np.float64)
+    a, b = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if interleaved else (slice(0, n), slice(n, 2 * n))
+    out, size = y.copy(), np.abs(y)
+    out[..., a] = (y[..., a] * np.cos(t) - y[..., b] * np.sin(t)) * magnitude
+    out[..., b] = (y[..., b] * np.cos(t) + y[..., a] * np.sin(t)) * magnitude
+    size[..., a] = size[..., b] = (np.abs(y[..., a]) + np.abs(y[..., b])) * abs(magnitude)
+    return out, size
