@@ -503,7 +503,7 @@ kvq_status kvq_paged_attention(kvq_paged_cache* h, int32_t layer, int32_t reques
   a.out = static_cast<uint16_t*>(out);
   a.ws = workspace;
   a.sm_count = h->sm_count;
-  return done(kvq::launch_paged_attention(layer_dev(h, layer), a, static_cast<cudaStream_t>(stream)), 1,
+  return done(kvq::launch_paged_attention(layer_dev(h, layer), a, static_cast<cudaStream_t>(stream)), 2,
               "paged attention launch");
 }
 

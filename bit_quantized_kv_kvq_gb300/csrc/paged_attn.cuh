@@ -1,0 +1,1190 @@
+// Attention of several new tokens per request over the paged 8-bit cache
+// (kvq_paged_attention).
+//
+//   e_t = c <q_i, k_hat_t>,  o_i = sum_{t <= p_i} softmax(e)_t v_hat_t,  x_hat = code * s(page, head)
+//
+// For long chunks the 4 D operations per (row, key) bound it, for a few tokens the
+// 2 D bytes of codes per key. Both products run on the 5th-generation tensor
+// cores as in the prompt attention: S = Q K^T into tensor memory, P where S was,
+// O += P V. A unit is 128 rows: every query head of one kv-head on 128 / group
+// consecutive tokens, so that the group shares each key tile and the diagonal cuts few.
+//
+// Codes are exact numbers of the input type (fp16 or bf16, int8 or e4m3), so the
+// operands are the codes themselves, converted on the way from L2 to shared memory by four
+// warps, and the scales stay out of them: a score's factor is c s_k of its page;
+// a value's scale s_v = f 2^e goes half into the weight (2^(s - m + log2 f), f in
+// [1, 2)) and half into the operand (code 2^e, exact), which bounds both
+// whatever the scales; the sum of weights takes 1 / f off again. All of this is per
+// group of 16 keys, so pages of any size cost the same.
+//
+// A block is two units: consecutive tokens of a request on the same key tiles, or,
+// where the tokens left fit one unit, the same rows on every other tile (their sums
+// are joined at the end), so that a few rows still keep two chains of scores,
+// softmax and products going. The blocks' tiles form a line that is cut into
+// equal ranges, one per CTA, as in the decode: the grid needs no lengths, ragged
+// steps stay even, and one long request fills the GPU. A block that a range's end
+// cuts leaves partial sums, which a second kernel merges in the order of the CTAs.
+//
+// Warps 0-3 and 4-7: softmax of the units; 8: the range's blocks and their
+// queries; 9: tensor core issue; 10: tiles (page ids, scales, L2 prefetch); 12-15: codes
+// and open rows to operands.
+#pragma once
+
+#include "attn_common.cuh"
+#include "paged_internal.h"
+
+namespace kvq {
+namespace patt {
+
+constexpr int kThreads = 512;
+constexpr int kRows = 128;  // rows of a unit, keys of a tile
+constexpr int kGroups = kRows / 16;
+constexpr int kInfo = 8;    // tiles looked up ahead
+constexpr int kNever = 0x7fffffff;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kFar = 0x1p20f;
+
+// Places on the line: 2 a tile of two units' rows, 1 where the units take every other
+// tile, and kExtra a block for its queries, ends and merge.
+constexpr int kExtra = 6;
+
+template <int D>
+struct Cfg {
+  static constexpr int kTile = kRows * D * 2;       // bytes of a Q, K or V operand
+  static constexpr int kStages = D == 128 ? 4 : 8;  // K and V operands
+  static constexpr int kSmem = 1024 + (2 + kStages) * kTile;
+};
+
+struct Params {
+  CUtensorMap mq;
+  PagedDev c;
+  PagedAttnArgs a;
+  int ctas;
+  // heads of a unit, chunks of 128 heads of a larger group, tokens of a unit, (kv-head, chunk) pairs
+  int unit_heads, chunks, unit_tokens, lots;
+  int4* pos;     // [ctas + 1] where each CTA's range starts: request, lot, block, tile
+  float* part_o; // [ctas][2][256][D]
+  float* part_ml;
+};
+
+__host__ __device__ inline size_t pos_bytes(int ctas) { return ((size_t)(ctas + 1) * 16 + 255) / 256 * 256; }
+
+// --------------------------------------------------------------------------
+// The line
+// --------------------------------------------------------------------------
+struct Req {
+  int c0, m, n;  // first packed token, new tokens, length with them
+};
+
+__device__ __forceinline__ Req load_req(const Params& p, int b, bool& bad) {
+  Req r;
+  r.c0 = p.a.cu[b];
+  const long long m = (long long)p.a.cu[b + 1] - r.c0;
+  r.n = p.a.lens[b];
+  r.m = 0;
+  if (m <= 0) return r;
+  if (r.c0 < 0 || m > p.a.tokens - r.c0 || r.n < m || r.n > (long long)p.c.max_pages << p.c.page_shift) {
+    bad = true;
+    return r;
+  }
+  r.m = (int)m;
+  return r;
+}
+
+// The blocks of a request for one lot, and the places before block i (whole
+// blocks: their tiles by the sum of their ends).
+struct Blocks {
+  long long old, whole, rest;
+  int bt, ut, n;
+  __device__ __forceinline__ Blocks(const Params& p, const Req& r) {
+    ut = p.unit_tokens;
+    bt = 2 * ut;
+    n = r.n;
+    old = r.n - r.m;
+    whole = r.m / bt;
+    rest = r.m % bt;
+  }
+  __device__ __forceinline__ long long count() const { return whole + (rest > 0); }
+  __device__ __forceinline__ int last_weight() const { return rest <= ut ? 1 : 2; }
+  __device__ __forceinline__ long long before(long long i) const {
+    return i * kExtra + ((i * old + bt * (i * (i + 1) / 2)) >> 6);
+  }
+  __device__ __forceinline__ long long all() const {
+    return before(whole) + (rest > 0 ? kExtra + (long long)last_weight() * ((n + kRows - 1) / kRows) : 0);
+  }
+  __device__ __forceinline__ int tiles(long long i) const {
+    const long long end = i < whole ? old + (i + 1) * bt : n;
+    return (int)((end + kRows - 1) / kRows);
+  }
+};
+
+struct Pos {
+  int b, lot, i, t;
+};
+
+// The place v of a request's line.
+__device__ __forceinline__ Pos locate(const Params& p, int b, const Req& r, long long v) {
+  const Blocks k(p, r);
+  const long long all = k.all();
+  Pos x;
+  x.b = b;
+  x.lot = (int)(v / all);
+  const long long w = v - x.lot * all;
+  long long i = k.whole, lo = k.before(k.whole), hi = all;
+  if (w < lo) {
+    i = 0;
+    for (long long n = k.whole; n > 1;) {
+      const long long half = n >> 1;
+      if (k.before(i + half) <= w) i += half, n -= half;
+      else n = half;
+    }
+    lo = k.before(i);
+    hi = k.before(i + 1);
+  }
+  const int tiles = k.tiles(i);
+  long long t = (w - lo) * tiles / (hi - lo);
+  // no slivers: a cut near an end is none
+  const int least = tiles >= 16 ? 2 : 1;
+  if (t < least) t = 0;
+  if (tiles - t < least) t = 0, ++i;
+  x.i = (int)i;
+  x.t = (int)t;
+  if (i == k.count()) x.i = 0, ++x.lot;
+  return x;
+}
+
+// --------------------------------------------------------------------------
+// Shared memory
+// --------------------------------------------------------------------------
+struct Info {
+  float4 f[kGroups];  // per 16 keys: score factor, log2 f, 1 / f, the pair 2^e
+  int page[2][kGroups];  // of keys, of values; -1: open rows or none, -2: zeros
+  int coded;             // all of them pages
+};
+
+struct Part {
+  int b, h, hq0, heads;  // kv-head, first query head and how many of the chunk
+  int c0, tokens, pos0;  // first packed token, how many, position of the first
+  int n, t0, t1, tiles, slot;  // slot: -1 the whole block, else where its partial sums go
+  bool both;             // two units of rows; else one, on every other tile
+  __device__ __forceinline__ bool has(int unit) const { return unit == 0 || both || t1 - t0 > 1; }
+  __device__ __forceinline__ bool mine(int unit, int t) const { return both || ((t - t0) & 1) == unit; }
+};
+
+struct Shared {
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], drain;
+  uint64_t kv_full[8], kv_empty[8];  // by operand stage
+  uint64_t info_full[kInfo], info_empty[kInfo];
+  uint64_t part_full[2], part_empty[2];
+  uint64_t fix_ready[2], fix_free[2];  // by parity of the part: `first` written, read
+  uint64_t join_ready, join_done, conv;
+  Info info[kInfo];
+  Part part[2];
+  uint32_t tmem;
+  int any_nonfinite[2];
+  int first[2][3][128];  // first position in the open page whose value is NaN, +inf, -inf, per channel
+  float join[2][kRows][3];  // of a unit's row: reference, sum, factor of its O
+  long long scan[kThreads / 32];
+  Pos from, to;
+};
+
+// Waits last as long as a few tiles, but the walker's as long as a block.
+constexpr int kPolls = 8 * kWaitLimit, kLongPolls = 64 * kWaitLimit;
+
+// Whole warp: false where the wait gave up.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* status, int polls = kPolls) {
+  const bool done = mbar_wait_limited(bar, parity, polls, kWaitHintNs);
+  if (!done) raise_status(status, kStatusTimeout);
+  return __all_sync(kFull, done);
+}
+
+// The part of step `it`, for one warp; false at the end or on a timeout.
+__device__ __forceinline__ bool take_part(Shared* sh, int it, uint32_t* status, Part& x) {
+  const int slot = it & 1;
+  if (!wait(&sh->part_full[slot], (it >> 1) & 1, status)) return false;
+  x = sh->part[slot];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) arrive(&sh->part_empty[slot]);
+  return x.b >= 0;
+}
+
+// --------------------------------------------------------------------------
+// Blocks and their queries
+// --------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ void part_role(const Params& p, Shared* sh, unsigned char* smem) {
+  const int lane = threadIdx.x & 31;
+  uint32_t* status = p.c.status;
+  uint32_t q_phase[2] = {0, 0};
+  Pos x = sh->from;
+  const Pos to = sh->to;
+  bool ok = true, bad = false;
+  Req r = {0, 0, 0};
+  if (x.b < p.a.requests) r = load_req(p, x.b, bad);
+  for (int it = 0; ok; ++it) {
+    // the next request with a place
+    while (x.b < p.a.requests && (x.lot == p.lots || r.m == 0)) {
+      x.lot = x.i = x.t = 0;
+      if (++x.b < p.a.requests) r = load_req(p, x.b, bad);
+    }
+    const bool before = x.b < to.b || (x.b == to.b && (x.lot < to.lot || (x.lot == to.lot && x.i < to.i)));
+    const bool here = x.b == to.b && x.lot == to.lot && x.i == to.i;
+    Part y;
+    y.b = -1;
+    if (x.b < p.a.requests && (before || (here && x.t < to.t))) {
+      const Blocks k(p, r);
+      const int chunk = x.lot % p.chunks;
+      y.b = x.b;
+      y.h = x.lot / p.chunks;
+      y.hq0 = y.h * p.a.group + chunk * kRows;
+      y.heads = min(p.unit_heads, p.a.group - chunk * kRows);
+      const long long first = (long long)x.i * k.bt;
+      y.c0 = r.c0 + (int)first;
+      y.tokens = (int)min((long long)k.bt, r.m - first);
+      y.pos0 = (int)(k.old + first);
+      y.n = r.n;
+      y.tiles = k.tiles(x.i);
+      y.t0 = x.t;
+      y.t1 = here ? to.t : y.tiles;
+      y.slot = y.t0 > 0 ? 0 : y.t1 < y.tiles ? 1 : -1;
+      y.both = y.tokens > k.ut;
+      x.t = 0;
+      if (++x.i == k.count()) x.i = 0, ++x.lot;
+    }
+    const int slot = it & 1;
+    if (it >= 2 && !wait(&sh->part_empty[slot], ((it >> 1) - 1) & 1, status, kLongPolls)) break;
+    if (lane == 0) {
+      sh->part[slot] = y;
+      arrive(&sh->part_full[slot]);
+    }
+    __syncwarp();
+    if (y.b < 0) break;
+    const uint32_t bytes = (uint32_t)p.unit_heads * p.unit_tokens * D * 2;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (!ok || !y.has(u)) continue;
+      // the first wait is for the phase before the first and passes at once
+      ok = wait(&sh->q_empty[u], q_phase[u] ^ 1, status, kLongPolls);
+      if (!ok) break;
+      q_phase[u] ^= 1;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sh->q_full[u], bytes);
+        for (int half = 0; half < D / 64; ++half)
+          tma_tile(smem_u32(smem + u * Cfg<D>::kTile + half * (kRows * 128)), &p.mq, half * 64, y.hq0,
+                   y.c0 + (y.both ? u * p.unit_tokens : 0), &sh->q_full[u]);
+      }
+    }
+  }
+  __syncwarp();
+  // nothing is in flight into this CTA's shared memory when it ends
+  for (int u = 0; u < 2; ++u) wait(&sh->q_full[u], q_phase[u] ^ 1, status);
+}
+
+// --------------------------------------------------------------------------
+// Tiles: pages, scales, prefetch
+// --------------------------------------------------------------------------
+template <int CODE, bool BF16>
+__device__ __forceinline__ float4 factors(float sk, float sv, float scale_log2, bool& zero_values) {
+  // 2^e stays a number of the type, with products code 2^e exact (e4m3: multiples of 2^-9)
+  constexpr int kMin = BF16 ? -126 : CODE == KVQ_PAGE_INT8 ? -24 : -15;
+  const uint32_t bits = __float_as_uint(sv);
+  int e = (int)((bits >> 23) & 255) - 127;
+  float f = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);
+  if (e < kMin) e = kMin, f = sv * (BF16 ? 0x1p126f : CODE == KVQ_PAGE_INT8 ? 0x1p24f : 0x1p15f);  // exact
+  zero_values = !(fabsf(sv) <= 3.0e38f) || sv == 0.0f;
+  if (sv == 0.0f) e = 0, f = 1.0f;
+  if (!(fabsf(sv) <= 3.0e38f)) e = 0, f = NAN;
+  uint32_t w;
+  if (BF16) w = (uint32_t)(e + 127) << 7;
+  else w = e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24);
+  float4 r;
+  r.x = fabsf(sk) <= 3.0e38f ? sk * scale_log2 : NAN;
+  r.y = log2f(f);
+  r.z = f == f ? 1.0f / f : 1.0f;  // a masked weight's share stays 0
+  r.w = __uint_as_float(w | (w << 16));
+  return r;
+}
+
+template <int D, int CODE, bool BF16>
+__device__ __forceinline__ void tile_role(const Params& p, Shared* sh) {
+  const PagedDev& c = p.c;
+  const int lane = threadIdx.x & 31, g = lane & 7, ahead = lane >> 3, P = 1 << c.page_shift;
+  int i = 0;  // tiles so far
+  Part x;
+  for (int it = 0; take_part(sh, it, c.status, x); ++it) {
+    const int full = x.n & ~(P - 1);
+    const int32_t* row = p.a.table + (int64_t)x.b * c.max_pages;
+    for (int t = x.t0; t < x.t1; t += 4) {  // four tiles at a time
+      const int pos = (t + ahead) * kRows + 16 * g, live = min(4, x.t1 - t);
+      float4 f = make_float4(p.a.scale_log2, 0.0f, 1.0f, 0.0f);
+      int page_k = -1, page_v = -1;
+      if (ahead < live && pos < full) {
+        const int page = row[pos >> c.page_shift];
+        if (page < 0 || page >= c.num_pages) {
+          raise_status(c.status, kStatusBadIndex);
+          page_k = page_v = -2;
+          f = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);
+        } else {
+          const int64_t ph = ((int64_t)page * c.heads + x.h) * 2;
+          if ((pos & (P - 1)) == 0)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.pages + (ph << c.page_shift) * D),
+                         "r"(2 * P * D)
+                         : "memory");
+          const float2 s = *reinterpret_cast<const float2*>(c.scales + ph);
+          bool zero;
+          f = factors<CODE, BF16>(s.x, s.y, p.a.scale_log2, zero);
+          page_k = page;
+          page_v = zero ? -2 : page;
+        }
+      }
+      const uint32_t pages = __ballot_sync(kFull, page_k >= 0 && page_v >= 0);
+      for (int k = 0; k < live; ++k, ++i) {
+        const int slot = i % kInfo;
+        if (!wait(&sh->info_empty[slot], ((i / kInfo) & 1) ^ 1, c.status)) return;
+        if (ahead == k) {
+          Info& o = sh->info[slot];
+          o.f[g] = f;
+          o.page[0][g] = page_k;
+          o.page[1][g] = page_v;
+          if (g == 0) o.coded = ((pages >> (8 * k)) & 255u) == 255u;
+        }
+        __syncwarp();
+        if (lane == 0) arrive(&sh->info_full[slot]);
+      }
+    }
+  }
+}
+
+// --------------------------------------------------------------------------
+// Codes to operands
+// --------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bsub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (BF16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The four codes of a word as numbers of the input type, times the pair `up` (values).
+template <int CODE, bool BF16, bool VALUES>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t up, uint32_t& lo, uint32_t& hi) {
+  if (CODE == KVQ_PAGE_INT8 && !BF16) {
+    // 0x6400 | u is 1024 + u in fp16; u = code + 128
+    const uint32_t u = w ^ 0x80808080u;
+    lo = hsub2(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
+    hi = hsub2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
+  } else if (CODE == KVQ_PAGE_INT8) {
+    // 0x4300 | u is 128 + u in bf16 for u < 128: the low seven bits, less 128, and 128 more where the sign is set
+    const uint32_t u = w & 0x7f7f7f7fu, s = w & 0x80808080u;
+    lo = bsub2(__byte_perm(u, 0x43434343u, 0x4140), __byte_perm(s, 0x43434343u, 0x4140));
+    hi = bsub2(__byte_perm(u, 0x43434343u, 0x4342), __byte_perm(s, 0x43434343u, 0x4342));
+  } else if (!BF16) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {
+    // the code's bits as those of a bf16 number 2^-120 of it
+    const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
+    lo = mul2<true>((a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), 0x7b807b80u);
+    hi = mul2<true>((b & 0x80008000u) | ((b >> 4) & 0x07f007f0u), 0x7b807b80u);
+  }
+  if (VALUES) lo = mul2<BF16>(lo, up), hi = mul2<BF16>(hi, up);
+}
+
+template <int D>
+struct Place {  // of a thread in a tile: 16 channels of row 16 * pass * (128 / D) + row
+  int row, half, seg;
+  __device__ __forceinline__ Place(int tid) {
+    // eight threads on two rows' halves: their 16-byte chunks fall into eight different bank groups
+    seg = tid & 3;
+    half = D == 128 ? (tid >> 3) & 1 : 0;
+    row = D == 128 ? ((tid >> 4) << 1) + ((tid >> 2) & 1) : tid >> 2;
+  }
+  __device__ __forceinline__ int channel() const { return half * 64 + seg * 16; }
+};
+
+// 16 channels of a row of the operand tile: two 16-byte chunks, swizzled.
+__device__ __forceinline__ void put16(unsigned char* tile, int row, int half, int seg, const uint4& a, const uint4& b) {
+  unsigned char* at = tile + half * (kRows * 128) + row * 128;
+  *reinterpret_cast<uint4*>(at + (((2 * seg) ^ (row & 7)) << 4)) = a;
+  *reinterpret_cast<uint4*>(at + (((2 * seg + 1) ^ (row & 7)) << 4)) = b;
+}
+
+template <int CODE, bool BF16, bool VALUES>
+__device__ __forceinline__ void put_codes(unsigned char* tile, int row, int half, int seg, const uint4& x, uint32_t up) {
+  uint4 a, b;
+  widen4<CODE, BF16, VALUES>(x.x, up, a.x, a.y);
+  widen4<CODE, BF16, VALUES>(x.y, up, a.z, a.w);
+  widen4<CODE, BF16, VALUES>(x.z, up, b.x, b.y);
+  widen4<CODE, BF16, VALUES>(x.w, up, b.z, b.w);
+  put16(tile, row, half, seg, a, b);
+}
+
+// Infinities and NaN of 8 values of an open row: 0 in their place, and where
+// they were, in sh->first (0 * inf would carry them to rows that do not see them).
+template <bool BF16>
+__device__ __forceinline__ void finite8(uint4& x, int pos, int ch, int (*first)[128], int* any) {
+  constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
+  uint32_t acc = fma_zero<BF16>(x.w, fma_zero<BF16>(x.z, fma_zero<BF16>(x.y, fma_zero<BF16>(x.x, 0u))));
+  if ((acc & 0x7fff7fffu) == 0) return;
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t v = (w[j >> 1] >> (16 * (j & 1))) & 0xffffu;
+    if ((v & kInf) == kInf) {
+      const int kind = (v & 0x7fffu) != kInf ? 0 : (v >> 15) ? 2 : 1;
+      atomicMin(&first[kind][ch + j], pos);
+      *any = 1;
+      w[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
+    }
+  }
+  x = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int D, int CODE, bool BF16>
+__device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsigned char* ring) {
+  using C = Cfg<D>;
+  constexpr int kPasses = D / 16, kStep = 2048 / D;  // passes over a tile, rows of one
+  const PagedDev& c = p.c;
+  const int tid = threadIdx.x & 127, lane = threadIdx.x & 31, P = 1 << c.page_shift;
+  const Place<D> at(tid);
+  const int ch = at.channel();
+  uint4 x[kPasses];  // codes of the next operand
+  int i = 0, tile = 0;  // operands and tiles so far
+  uint32_t conv_phase = 0;
+  Part y;
+  y.h = 0;
+
+  // codes of pass k of the tile's keys or values (which = 0, 1), all of it pages
+  auto load = [&](const Info& info, int which, int k) {
+    const int row = k * kStep + at.row;
+    const int64_t ph = ((int64_t)info.page[which][row >> 4] * c.heads + y.h) * 2 + which;
+    return *reinterpret_cast<const uint4*>(c.pages + ((ph << c.page_shift) + (row & (P - 1))) * D + ch);
+  };
+  for (int it = 0; take_part(sh, it, c.status, y); ++it) {
+    const int par = it & 1, full = y.n & ~(P - 1);
+    // the rows of the part before the last have read what this one may overwrite
+    if (!wait(&sh->fix_free[par], ((it >> 1) & 1) ^ 1, c.status)) return;
+    if (sh->any_nonfinite[par]) {
+      __syncwarp();
+      if (lane == 0) arrive(&sh->conv);
+      if (!wait(&sh->conv, conv_phase, c.status)) return;
+      for (int k = tid; k < 3 * 128; k += 128) sh->first[par][k / 128][k % 128] = kNever;
+      if (tid == 0) sh->any_nonfinite[par] = 0;
+      __syncwarp();
+      if (lane == 0) arrive(&sh->conv);
+      if (!wait(&sh->conv, conv_phase ^ 1, c.status)) return;
+    }
+    bool loaded = false;  // x holds the codes of the next operand
+    for (int t = y.t0; t < y.t1; ++t, ++tile) {
+      const int slot = tile % kInfo;
+      Info& info = sh->info[slot];
+      if (!wait(&sh->info_full[slot], (tile / kInfo) & 1, c.status)) return;
+      bool next_coded = false;
+      const int next_slot = (tile + 1) % kInfo;
+      const Info& next = sh->info[next_slot];
+#pragma unroll
+      for (int which = 0; which < 2; ++which, ++i) {
+        const int st = i % C::kStages;
+        unsigned char* to = ring + st * C::kTile;
+        if (info.coded) {
+          if (!loaded) {
+#pragma unroll
+            for (int k = 0; k < kPasses; ++k) x[k] = load(info, which, k);
+          }
+          if (which == 1 && t + 1 < y.t1) {
+            if (!wait(&sh->info_full[next_slot], ((tile + 1) / kInfo) & 1, c.status)) return;
+            next_coded = next.coded;
+          }
+          if (!wait(&sh->kv_empty[st], ((i / C::kStages) & 1) ^ 1, c.status)) return;
+          // each pass's registers take the next operand's codes as soon as they are free
+          const bool more = which == 0 || next_coded;
+          const Info& from = which ? next : info;
+#pragma unroll
+          for (int k = 0; k < kPasses; ++k) {
+            const uint4 w = x[k];
+            if (more) x[k] = load(from, which ^ 1, k);
+            const int row = k * kStep + at.row;
+            if (which == 0) put_codes<CODE, BF16, false>(to, row, at.half, at.seg, w, 0u);
+            else put_codes<CODE, BF16, true>(to, row, at.half, at.seg, w, __float_as_uint(info.f[row >> 4].w));
+          }
+          loaded = more;
+        } else {
+          loaded = false;
+          if (!wait(&sh->kv_empty[st], ((i / C::kStages) & 1) ^ 1, c.status)) return;
+          const uint16_t* tail = c.tails + (((((int64_t)y.b * c.heads + y.h) * 2 + which) << c.page_shift)) * D + ch;
+#pragma unroll 1
+          for (int k0 = 0; k0 < kPasses; k0 += 4) {
+            uint4 a[4], b[4];
+            int page[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = (k0 + k) * kStep + at.row, pos = t * kRows + row;
+              page[k] = info.page[which][row >> 4];
+              a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
+              if (page[k] >= 0) {
+                a[k] = load(info, which, k0 + k);
+              } else if (page[k] == -1 && pos < y.n) {
+                const uint4* src = reinterpret_cast<const uint4*>(tail + (int64_t)(pos - full) * D);
+                a[k] = src[0];
+                b[k] = src[1];
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = (k0 + k) * kStep + at.row, pos = t * kRows + row;
+              if (page[k] >= 0) {
+                if (which == 0) put_codes<CODE, BF16, false>(to, row, at.half, at.seg, a[k], 0u);
+                else put_codes<CODE, BF16, true>(to, row, at.half, at.seg, a[k], __float_as_uint(info.f[row >> 4].w));
+              } else {
+                if (which == 1) {
+                  finite8<BF16>(a[k], pos, ch, sh->first[par], &sh->any_nonfinite[par]);
+                  finite8<BF16>(b[k], pos, ch + 8, sh->first[par], &sh->any_nonfinite[par]);
+                }
+                put16(to, row, at.half, at.seg, a[k], b[k]);
+              }
+            }
+          }
+        }
+        fence_proxy_async_smem();  // the tensor cores read what was written here
+        __syncwarp();
+        if (lane == 0) arrive(&sh->kv_full[st]);
+      }
+      __syncwarp();
+      if (lane == 0) arrive(&sh->info_empty[slot]);
+    }
+    __syncwarp();
+    if (lane == 0) arrive(&sh->fix_ready[par]);
+  }
+}
+
+// --------------------------------------------------------------------------
+// Products
+// --------------------------------------------------------------------------
+template <int D, bool BF16>
+__device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned char* smem) {
+  using C = Cfg<D>;
+  constexpr uint32_t kQK = t5::instr_desc(128, 128, BF16, false), kPV = t5::instr_desc(128, D, BF16, true);
+  const uint32_t tmem = sh->tmem;
+  uint32_t* status = p.c.status;
+  const unsigned char* ring = smem + 2 * C::kTile;
+  const uint64_t dq = t5::smem_desc(smem_u32(smem), 16), dk = t5::smem_desc(smem_u32(ring), 16);
+  const uint64_t dv = t5::smem_desc(smem_u32(ring), kRows * 128);
+  uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+  auto scores = [&](int u, int st) {
+    const uint64_t q = dq + (uint32_t)(u * C::kTile >> 4), k = dk + (uint32_t)(st * C::kTile >> 4);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint32_t off = ((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4;
+      t5::mma_ss(tmem + u * 128, q + off, k + off, kQK, kk > 0);
+    }
+    t5::commit(&sh->s_full[u]);
+  };
+  auto values = [&](int u, int st, bool first) {
+    const uint64_t v = dv + (uint32_t)(st * C::kTile >> 4);
+#pragma unroll
+    for (int kk = 0; kk < kRows / 16; ++kk)
+      t5::mma_ts(tmem + 256 + u * D, tmem + u * 128 + kk * 8, v + kk * (2048 >> 4), kPV, !first || kk > 0);
+  };
+  auto full = [&](int x) { return wait(&sh->kv_full[x % C::kStages], (x / C::kStages) & 1, status); };
+  auto query = [&](int u) {
+    const bool ok = wait(&sh->q_full[u], q_phase[u], status);
+    q_phase[u] ^= 1;
+    return ok;
+  };
+  auto weights = [&](int u) {
+    const bool ok = wait(&sh->p_full[u], p_phase[u], status);
+    p_phase[u] ^= 1;
+    t5::fence_after();
+    return ok;
+  };
+  int i = 0;  // operands before this part
+  bool ok = true;
+  Part y;
+  for (int it = 0; ok && take_part(sh, it, status, y); ++it) {
+    const int n = y.t1 - y.t0;
+    if (y.both) {
+      ok = full(i);
+      t5::fence_after();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        ok = ok && query(u);
+        if (ok && t5::elect_one()) {
+          scores(u, i % C::kStages);
+          if (n == 1) t5::commit(&sh->q_empty[u]);
+          if (u) t5::commit(&sh->kv_empty[i % C::kStages]);
+        }
+        __syncwarp();
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const int v = i + 2 * j + 1, k = v + 1;
+        const bool more = j + 1 < n;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (u == 0) ok = ok && full(v);
+          ok = ok && weights(u);
+          if (ok && t5::elect_one()) {
+            values(u, v % C::kStages, j == 0);
+            if (!more) t5::commit(&sh->o_done[u]);
+            if (u) t5::commit(&sh->kv_empty[v % C::kStages]);
+          }
+          __syncwarp();
+          if (!more) continue;
+          if (u == 0) ok = ok && full(k);
+          if (ok && t5::elect_one()) {
+            scores(u, k % C::kStages);
+            if (j + 1 == n - 1) t5::commit(&sh->q_empty[u]);
+            if (u) t5::commit(&sh->kv_empty[k % C::kStages]);
+          }
+          __syncwarp();
+        }
+      }
+    } else {  // tile j is unit j & 1's
+      auto one = [&](int j) {
+        const int u = j & 1, k = i + 2 * j;
+        if (j < 2) ok = ok && query(u);
+        ok = ok && full(k);
+        t5::fence_after();
+        if (ok && t5::elect_one()) {
+          scores(u, k % C::kStages);
+          if (j + 2 >= n) t5::commit(&sh->q_empty[u]);
+          t5::commit(&sh->kv_empty[k % C::kStages]);
+        }
+        __syncwarp();
+      };
+      one(0);
+      if (n > 1) one(1);
+      for (int j = 0; j < n && ok; ++j) {
+        const int u = j & 1, v = i + 2 * j + 1;
+        ok = ok && full(v);
+        ok = ok && weights(u);
+        if (ok && t5::elect_one()) {
+          values(u, v % C::kStages, j < 2);
+          if (j + 2 >= n) t5::commit(&sh->o_done[u]);
+          t5::commit(&sh->kv_empty[v % C::kStages]);
+        }
+        __syncwarp();
+        if (j + 2 < n) one(j + 2);
+      }
+    }
+    i += 2 * n;
+  }
+  __syncwarp();
+  if (t5::elect_one()) t5::commit(&sh->drain);
+  __syncwarp();
+  wait(&sh->drain, 0, status);
+}
+
+// --------------------------------------------------------------------------
+// Softmax
+// --------------------------------------------------------------------------
+// 16 scores to weights: p = 2^(s a + off), packed; their sum.
+template <bool BF16>
+__device__ __forceinline__ uint64_t to_weights(const uint32_t* s, float a, float off, uint32_t* p) {
+  const uint64_t a2 = f2_pack(a, a), off2 = f2_pack(off, off);
+  uint64_t sum0, sum1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float x, y;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), a2, off2), x, y);
+    x = exp2_fast(x);
+    y = exp2_fast(y);
+    const uint64_t xy = f2_pack(x, y);
+    if (i == 0) sum0 = xy;
+    else if (i == 1) sum1 = xy;
+    else if (i & 1) sum1 = f2_add(sum1, xy);
+    else sum0 = f2_add(sum0, xy);
+    p[i] = pack2<BF16>(x, y);
+  }
+  return f2_add(sum0, sum1);
+}
+
+// The reference of a row's exponentials: it moves only when a score (by its
+// page's factor, in units of log 2) passes it by 8, so that few tiles scale O.
+// Each row goes by its own scores. A weight is 2^(s a + log2 f - m), one multiply-add.
+// In fp16 m lies 6 below the score that set it: weights with f stay below 2^15, and
+// those 2^-20 of it above the type's subnormal numbers. Past 2^20 m's own
+// rounding would be a factor without limit: such a row (`far`) rounds its scaled scores and
+// subtracts the score itself, which is exact near the largest ones.
+template <int D, bool BF16>
+struct Reference {
+  static constexpr float kLift = BF16 ? 0.0f : 6.0f;
+  float m;       // far: the score, else what is subtracted
+  bool far, any_far;
+
+  __device__ __forceinline__ void reset() { m = -INFINITY, far = any_far = false; }
+  __device__ __forceinline__ float lift() const { return far ? kLift : 0.0f; }
+  __device__ __forceinline__ void raise(float top, float& l, uint32_t tO, bool o) {
+    const bool up = top - m > 8.0f + (far ? 0.0f : kLift);
+    if (!__any_sync(kFull, up)) return;
+    float f = 1.0f;
+    if (up) {
+      const float was = m, was_lift = lift();
+      far = !(fabsf(top) <= kFar);
+      m = far ? top : top - kLift;
+      f = exp2_fast((was - m) - (was_lift - lift()));
+    }
+    any_far = __any_sync(kFull, far);
+    l *= f;
+    if (!o) return;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      uint32_t x[32];
+      t5::ld32(tO + c, x);
+      t5::wait_ld32(x);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+      t5::st32(tO + c, x);
+    }
+  }
+  // what is added to the scaled scores of a group, but for its log2 f
+  __device__ __forceinline__ float off() const { return far ? kLift : m == -INFINITY ? 0.0f : -m; }
+  // 16 scores of a far row: scaled, less the reference; a: the factor left for to_weights
+  __device__ __forceinline__ void settle(uint32_t* s, float& a) const {
+    if (!any_far) return;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = far ? __float_as_uint(__fmul_rn(__uint_as_float(s[i]), a) - m) : s[i];
+    a = far ? 1.0f : a;
+  }
+};
+
+template <int D, bool BF16>
+__device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const int unit) {
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, r = warp * 32 + lane;
+  uint32_t* status = p.c.status;
+  const uint32_t lanes = sh->tmem + ((uint32_t)(warp * 32) << 16);
+  const uint32_t tS = lanes + unit * 128, tP = tS, tO = lanes + 256 + unit * D, tO_other = lanes + 256 + (1 - unit) * D;
+  const int tok = r / p.unit_heads, head = r - tok * p.unit_heads;
+  const bool wide = (reinterpret_cast<uintptr_t>(p.a.out) & 31) == 0;
+  const bool wide_part = (reinterpret_cast<uintptr_t>(p.part_o) & 31) == 0;
+  Reference<D, BF16> ref;
+  uint32_t s_phase = 0, out_phase[2] = {0, 0}, join_phase = 0;
+  int tile = 0;
+  Part y;
+  for (int it = 0; take_part(sh, it, status, y); ++it) {
+    const int my_token = (y.both ? unit * p.unit_tokens : 0) + tok;  // of the block
+    const bool live = tok < p.unit_tokens && head < y.heads && my_token < y.tokens;
+    const bool warp_live = __any_sync(kFull, live);
+    const int pos = y.pos0 + my_token;
+    ref.reset();
+    float l = 0.0f;
+    bool any = false;  // a tile of this unit came before
+    for (int t = y.t0; t < y.t1; ++t, ++tile) {
+      const int slot = tile % kInfo;
+      if (!wait(&sh->info_full[slot], (tile / kInfo) & 1, status)) return;
+      if (y.mine(unit, t)) {
+        if (!wait(&sh->s_full[unit], s_phase, status)) return;
+        s_phase ^= 1;
+        t5::fence_after();
+        const Info& info = sh->info[slot];
+        const int seen = live ? pos + 1 - t * kRows : kRows;  // keys of the tile that the row attends
+        if (!warp_live) {
+          // nothing reads these rows' weights
+        } else if (__all_sync(kFull, seen >= kRows)) {
+          uint32_t s[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) t5::ld32(tS + 32 * c, s + 32 * c);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) t5::wait_ld32(s + 32 * c);
+          float top = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) top = fmaxf(top, max_of<16>(s + 16 * g) * info.f[g].x);
+          ref.raise(live ? top : -INFINITY, l, tO, any);  // s_full came after the unit's last PV
+          const float off = ref.off();
+          uint64_t sum = 0;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t w[32];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const float4 f = info.f[4 * half + g];
+              float a = f.x;
+              ref.settle(s + 64 * half + 16 * g, a);
+              sum = f2_fma(to_weights<BF16>(s + 64 * half + 16 * g, a, off + f.y, w + 8 * g), f2_pack(f.z, f.z), sum);
+            }
+            t5::st32(tP + 32 * half, w);
+          }
+          float u, v;
+          f2_unpack(sum, u, v);
+          l += u + v;
+        } else {
+          // a tile that ends past some row's own key, by groups of 32 keys
+          // (P of a group lies where scores already read were)
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s[32];
+            t5::ld32(tS + 32 * c, s);
+            t5::wait_ld32(s);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= seen) s[i] = 0xff800000u;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) top = fmaxf(top, max_of<16>(s + 16 * g) * info.f[2 * c + g].x);
+          }
+          ref.raise(live ? top : -INFINITY, l, tO, any);
+          const float off = ref.off();
+          uint64_t sum = 0;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s[32], w[16];
+            t5::ld32(tS + 32 * c, s);
+            t5::wait_ld32(s);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const float4 f = info.f[2 * c + g];
+              float a = f.x;
+              ref.settle(s + 16 * g, a);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)  // masked after the factor: -inf * 0 is NaN
+                s[16 * g + i] = 32 * c + 16 * g + i >= seen ? 0xff800000u
+                                                            : __float_as_uint(fmaf(__uint_as_float(s[16 * g + i]), a, off + f.y));
+              sum = f2_fma(to_weights<BF16>(s + 16 * g, 1.0f, 0.0f, w + 8 * g), f2_pack(f.z, f.z), sum);
+            }
+            t5::st16(tP + 16 * c, w);
+          }
+          float u, v;
+          f2_unpack(sum, u, v);
+          l += u + v;
+        }
+        t5::wait_st();
+        t5::fence_before();
+        arrive(&sh->p_full[unit]);
+        any = true;
+      }
+      __syncwarp();
+      if (lane == 0) arrive(&sh->info_empty[slot]);
+    }
+
+    const int par = it & 1;
+    if (!wait(&sh->fix_ready[par], (it >> 1) & 1, status)) return;
+    const bool fix = sh->any_nonfinite[par] != 0;
+    // sums by the reference itself
+    float top = ref.m;
+    l *= ref.far ? exp2_fast(-ref.kLift) : 1.0f;
+    float mine = ref.far ? exp2_fast(-ref.kLift) : 1.0f, other = 0.0f;
+    if (!y.both) {  // join the units' sums: each thread half of the row's channels
+      sh->join[unit][r][0] = top;
+      sh->join[unit][r][1] = l;
+      sh->join[unit][r][2] = mine;
+      // (a unit without a tile has m = -inf and l = 0)
+      if (!wait(&sh->o_done[0], out_phase[0], status)) return;
+      if (y.has(1) && !wait(&sh->o_done[1], out_phase[1], status)) return;
+      t5::fence_after();
+      arrive(&sh->join_ready);
+      if (!wait(&sh->join_ready, join_phase, status)) return;
+      const float top2 = sh->join[1 - unit][r][0], l2 = sh->join[1 - unit][r][1];
+      const float best = fmaxf(top, top2), base = best == -INFINITY ? 0.0f : best;
+      const float f1 = exp2_fast(top - base), f2 = exp2_fast(top2 - base);
+      l = l * f1 + l2 * f2;
+      mine *= f1;
+      other = f2 * sh->join[1 - unit][r][2];
+      top = best;
+    } else if (y.has(unit)) {
+      if (!wait(&sh->o_done[unit], out_phase[unit], status)) return;
+      t5::fence_after();
+    }
+    out_phase[0] ^= 1;
+    if (y.has(1)) out_phase[1] ^= 1;
+
+    const int c0 = y.both ? 0 : unit * (D / 2), c1 = y.both ? D : c0 + D / 2;
+    const bool own = y.both || y.has(unit), both_o = !y.both && y.has(1);
+    const float scale = y.slot < 0 ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+    const int part_row = y.slot < 0 ? 0 : ((blockIdx.x * 2 + y.slot) * 2 + (y.both ? unit : 0)) * kRows + r;
+    if (warp_live) {
+#pragma unroll 1
+      for (int c = c0; c < c1; c += 32) {
+        uint32_t o[32];
+        if (own) {
+          t5::ld32(tO + c, o);
+          t5::wait_ld32(o);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = own ? __float_as_uint(__uint_as_float(o[i]) * mine) : 0u;
+        if (!y.both && (unit == 1 || both_o)) {
+          uint32_t o2[32];
+          t5::ld32(tO_other + c, o2);
+          t5::wait_ld32(o2);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            o[i] = __float_as_uint(fmaf(__uint_as_float(o2[i]), other, __uint_as_float(o[i])));
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * scale);
+        if (fix) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float x = __uint_as_float(o[i]);
+            if (pos >= sh->first[par][1][c + i]) x += INFINITY;
+            if (pos >= sh->first[par][2][c + i]) x -= INFINITY;
+            if (pos >= sh->first[par][0][c + i]) x = NAN;
+            o[i] = __float_as_uint(x);
+          }
+        }
+        if (live && y.slot < 0) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = pack2<BF16>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+          store_row(p.a.out + ((int64_t)(y.c0 + my_token) * p.a.q_heads + y.hq0 + head) * D + c, w, wide);
+        } else if (live) {
+          uint16_t* to = reinterpret_cast<uint16_t*>(p.part_o + (int64_t)part_row * D + c);
+          store_row(to, o, wide_part);
+          store_row(to + 32, o + 16, wide_part);
+        }
+      }
+      if (live && y.slot >= 0 && (y.both || unit == 0))
+        *reinterpret_cast<float2*>(p.part_ml + (int64_t)part_row * 2) = make_float2(top, l);
+    }
+    if (!y.both) {
+      t5::fence_before();
+      arrive(&sh->join_done);
+      if (!wait(&sh->join_done, join_phase, status)) return;
+      join_phase ^= 1;
+    }
+    t5::fence_before();  // O has been read: ordered before the next part's first weights
+    __syncwarp();
+    if (lane == 0) arrive(&sh->fix_free[par]);
+  }
+}
+
+// --------------------------------------------------------------------------
+// The kernel
+// --------------------------------------------------------------------------
+// Where the CTA's range starts and ends: sums of the requests' places over the block.
+__device__ __forceinline__ void find_range(const Params& p, Shared* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, R = p.a.requests;
+  const int per = (R + kThreads - 1) / kThreads;
+  long long sum = 0;
+  bool bad = false;
+  for (int k = 0; k < per; ++k) {
+    const int b = threadIdx.x * per + k;
+    if (b >= R) break;
+    const Req r = load_req(p, b, bad);
+    if (r.m > 0) sum += Blocks(p, r).all() * p.lots;
+  }
+  if (bad && blockIdx.x == 0) raise_status(p.c.status, kStatusBadIndex);
+  long long in = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long u = __shfl_up_sync(kFull, in, d);
+    if (lane >= d) in += u;
+  }
+  if (lane == 31) sh->scan[warp] = in;
+  if (threadIdx.x == 0) {
+    const Pos end = {R, 0, 0, 0};
+    sh->from = sh->to = end;
+  }
+  __syncthreads();
+  long long at = in - sum, places = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) at += sh->scan[w];
+    places += sh->scan[w];
+  }
+  const int ctas = places < p.ctas ? (int)places : p.ctas;
+  if ((int)blockIdx.x >= ctas) return;
+  const long long v[2] = {places / ctas * blockIdx.x + places % ctas * blockIdx.x / ctas,
+                          places / ctas * (blockIdx.x + 1) + places % ctas * (blockIdx.x + 1) / ctas};
+  for (int e = 0; e < 2; ++e) {
+    if (v[e] < at || v[e] >= at + sum) continue;
+    long long a = at;
+    for (int k = 0; k < per; ++k) {
+      const int b = threadIdx.x * per + k;
+      if (b >= R) break;
+      const Req r = load_req(p, b, bad);
+      const long long size = r.m > 0 ? Blocks(p, r).all() * p.lots : 0;
+      if (v[e] < a + size) {
+        (e ? sh->to : sh->from) = locate(p, b, r, v[e] - a);
+        break;
+      }
+      a += size;
+    }
+  }
+}
+
+template <int D, int CODE, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ Shared sh;
+  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (threadIdx.x == 0) {
+    prefetch_map(&p.mq);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 128);
+      mbar_init(&sh.o_done[i], 1);
+      mbar_init(&sh.part_full[i], 1);
+      mbar_init(&sh.part_empty[i], 14);  // every warp but the one that fills it and the idle one
+      mbar_init(&sh.fix_ready[i], 4);
+      mbar_init(&sh.fix_free[i], 8);
+    }
+    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.join_ready, 256);
+    mbar_init(&sh.join_done, 256);
+    mbar_init(&sh.conv, 4);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&sh.kv_full[i], 4);
+      mbar_init(&sh.kv_empty[i], 1);
+    }
+    for (int i = 0; i < kInfo; ++i) {
+      mbar_init(&sh.info_full[i], 1);
+      mbar_init(&sh.info_empty[i], 12);
+    }
+    mbar_fence_init();
+    sh.any_nonfinite[0] = sh.any_nonfinite[1] = 0;
+  }
+  for (int k = threadIdx.x; k < 2 * 3 * 128; k += kThreads) (&sh.first[0][0][0])[k] = kNever;
+  find_range(p, &sh);
+  if (warp == 9) t5::alloc(&sh.tmem, 512);
+  t5::fence_before();
+  __syncthreads();
+  t5::fence_after();
+  if (threadIdx.x == 0) {
+    p.pos[blockIdx.x] = make_int4(sh.from.b, sh.from.lot, sh.from.i, sh.from.t);
+    if (blockIdx.x == gridDim.x - 1) p.pos[gridDim.x] = make_int4(p.a.requests, 0, 0, 0);
+  }
+
+  // 256 threads x 176 + 128 x 72 + 128 x 88 registers = 512 x 128, what the launch holds
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    softmax_role<D, BF16>(p, &sh, warp >> 2);
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8) part_role<D>(p, &sh, smem);
+    else if (warp == 9) mma_role<D, BF16>(p, &sh, smem);
+    else if (warp == 10) tile_role<D, CODE, BF16>(p, &sh);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    convert_role<D, CODE, BF16>(p, &sh, smem + 2 * C::kTile);
+  }
+  __syncwarp();
+  t5::fence_before();
+  __syncthreads();
+  t5::fence_after();
+  if (warp == 9) t5::dealloc(sh.tmem, 512);
+}
+
+// Merges the partial sums of the blocks that a range's end cuts, in the order of
+// the CTAs. CTA x: the block that range x + 1 starts inside, if no earlier range
+// does; y: which 32 of its rows.
+constexpr int kMergeThreads = 256;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const __grid_constant__ Params p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kPer = D / 32;
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int4 at = p.pos[c], prev = p.pos[c - 1];
+  if (at.w == 0) return;
+  auto same = [&](const int4& x) { return x.x == at.x && x.y == at.y && x.z == at.z; };
+  if (same(prev) && prev.w > 0) return;
+  int last = c;  // the last CTA with a part of the block
+  while (last + 1 <= p.ctas) {
+    const int4 q = p.pos[last + 1];
+    if (!same(q) || q.w == 0) break;
+    ++last;
+  }
+  bool bad = false;
+  const Req r = load_req(p, at.x, bad);
+  const Blocks k(p, r);
+  const int chunk = at.y % p.chunks, hq0 = at.y / p.chunks * p.a.group + chunk * kRows;
+  const int heads = min(p.unit_heads, p.a.group - chunk * kRows);
+  const long long first = (long long)at.z * k.bt;
+  const int tokens = (int)min((long long)k.bt, r.m - first);
+#pragma unroll 1
+  for (int i = warp; i < 32; i += kMergeThreads / 32) {
+    const int row = blockIdx.y * 32 + i, unit = row / kRows, in = row % kRows, tok = in / p.unit_heads;
+    const int head = in - tok * p.unit_heads, token = unit * p.unit_tokens + tok;
+    if (tok >= p.unit_tokens || head >= heads || token >= tokens) continue;
+    float top = -INFINITY, l = 0.0f, o[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] = 0.0f;
+    int4 from = prev;
+    for (int x = c - 1; x <= last; ++x) {
+      const int4 to = p.pos[x + 1];
+      const bool empty = x >= c && same(to) && to.w == from.w;
+      from = to;
+      if (empty) continue;
+      const int64_t pr = ((int64_t)(x * 2 + (x >= c ? 0 : 1)) * 2 + unit) * kRows + in;
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + pr * 2);
+      float v[kPer];
+      const float* src = p.part_o + pr * D + lane * kPer;
+      if (D == 128) {
+        const float4 w = *reinterpret_cast<const float4*>(src);
+        v[0] = w.x, v[1] = w.y, v[2 % kPer] = w.z, v[3 % kPer] = w.w;
+      } else {
+        const float2 w = *reinterpret_cast<const float2*>(src);
+        v[0] = w.x, v[1] = w.y;
+      }
+      const float now = fmaxf(top, ml.x), base = now == -INFINITY ? 0.0f : now;
+      const float fo = exp2_fast(top - base), fn = exp2_fast(ml.x - base);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] = o[e] * fo + v[e] * fn;
+      l = l * fo + ml.y * fn;
+      top = now;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t* out = p.a.out + ((int64_t)(r.c0 + first + token) * p.a.q_heads + hq0 + head) * D + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack2<BF16>(o[e] * inv, o[e + 1] * inv);
+  }
+}
+
+template <int D, int CODE, bool BF16>
+cudaError_t launch(const PagedDev& c, const PagedAttnArgs& a, cudaStream_t st) {
+  Params p;
+  p.c = c;
+  p.a = a;
+  p.ctas = a.sm_count;
+  p.unit_heads = a.group < kRows ? a.group : kRows;
+  p.chunks = (a.group + kRows - 1) / kRows;
+  p.unit_tokens = kRows / p.unit_heads;
+  p.lots = c.heads * p.chunks;
+  unsigned char* ws = static_cast<unsigned char*>(a.ws);
+  p.pos = reinterpret_cast<int4*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + pos_bytes(p.ctas));
+  p.part_o = p.part_ml + (size_t)p.ctas * 4 * kRows * 2;
+  cudaError_t e = encode_heads(&p.mq, a.q, D, a.q_heads, a.tokens, a.q_stride, BF16, p.unit_heads, p.unit_tokens);
+  if (e != cudaSuccess) return e;
+  static SmemAttr attr;
+  e = attr.ensure(paged_attn_kernel<D, CODE, BF16>, Cfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  paged_attn_kernel<D, CODE, BF16><<<p.ctas, kThreads, Cfg<D>::kSmem, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.ctas < 2) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.ctas - 1, 8);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_attn_merge_kernel<D, BF16>, p);
+}
+
+template <int D, int CODE>
+cudaError_t by_type(const PagedDev& c, const PagedAttnArgs& a, cudaStream_t st) {
+  return c.dtype == KVQ_BF16 ? launch<D, CODE, true>(c, a, st) : launch<D, CODE, false>(c, a, st);
+}
+
+}  // namespace patt
+}  // namespace kvq

@@ -28,9 +28,8 @@
 // prompts of 1024 tokens: 75 us (912 TFLOP/s): the ends of blocks, where both
 // units write their rows, and half of every tile on the diagonal. With 64
 // channels per head the softmax is the longer part: 8192 tokens 293 us (939).
+#include "attn_common.cuh"
 #include "paged_internal.h"
-#include "tcgen05.cuh"
-#include "tensor_map.cuh"
 
 namespace kvq {
 namespace {
@@ -64,33 +63,6 @@ struct Shared {
   int any_nonfinite[2];
   int first[2][3][128];  // first token of the cut tiles whose value is NaN, +inf, -inf, per channel
 };
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  if (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int ch, int head, int token,
-                                         uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(ch), "r"(head), "r"(token), "r"(smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 
 // The order of the blocks and an empty unit wait for a whole block: 0.87 s in
 // the longest prompt (2^26 tokens, 524288 tiles of 1.65 us for a pair). A poll
@@ -186,12 +158,6 @@ struct Order {
 // the tiles that the diagonal cuts, the tensor cores get 0 in their place; the
 // rows from that token on get them at the end (Shared::first). One warp; a
 // tile of finite values (0 * x summed is 0) costs one multiply-add a pair.
-template <bool BF16>
-__device__ __forceinline__ uint32_t fma_zero(uint32_t x, uint32_t acc) {
-  if (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
-  else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
-  return acc;
-}
 template <int D, bool BF16>
 __device__ __forceinline__ void check_values(unsigned char* tile, int k0, int (*first)[128], int* any) {
   constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
@@ -256,19 +222,6 @@ __device__ __forceinline__ void scaled(uint32_t* s, uint64_t sc2, float off) {
     s[i] = __float_as_uint(x);
     s[i + 1] = __float_as_uint(y);
   }
-}
-
-template <int N>
-__device__ __forceinline__ float max_of(const uint32_t* s) {
-  float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
-#pragma unroll
-  for (int c = 0; c < N; c += 8) {
-    t0 = fmaxf(fmaxf(t0, __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
-    t1 = fmaxf(fmaxf(t1, __uint_as_float(s[c + 2])), __uint_as_float(s[c + 3]));
-    t2 = fmaxf(fmaxf(t2, __uint_as_float(s[c + 4])), __uint_as_float(s[c + 5]));
-    t3 = fmaxf(fmaxf(t3, __uint_as_float(s[c + 6])), __uint_as_float(s[c + 7]));
-  }
-  return fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
 }
 
 // The reference of a row's exponentials moves only when a score passes it by 8
@@ -338,21 +291,6 @@ struct Reference {
     for (int i = 0; i < N; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) - sub);
   }
 };
-
-// 64 bytes of an output row: whole 32-byte sectors where `out` is so aligned.
-__device__ __forceinline__ void store_row(uint16_t* to, const uint32_t* w, bool wide) {
-  if (wide) {
-#pragma unroll
-    for (int q = 0; q < 16; q += 8)
-      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 2 * q), "r"(w[q]), "r"(w[q + 1]),
-                   "r"(w[q + 2]), "r"(w[q + 3]), "r"(w[q + 4]), "r"(w[q + 5]), "r"(w[q + 6]), "r"(w[q + 7])
-                   : "memory");
-  } else {
-#pragma unroll
-    for (int q = 0; q < 16; q += 4)
-      *reinterpret_cast<uint4*>(to + 2 * q) = make_uint4(w[q], w[q + 1], w[q + 2], w[q + 3]);
-  }
-}
 
 // One unit's warps: scores to weights tile by tile, then the output rows.
 template <int D, bool BF16>
@@ -754,26 +692,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) t5::dealloc(sh.tmem, 512);
 }
 
-cudaError_t encode(CUtensorMap* m, const void* base, int dim, int heads, int tokens, int64_t stride, bool bf16) {
-  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (!fn) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
-  const cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)stride * 2};
-  const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)kRows};
-  const cuuint32_t es[3] = {1u, 1u, 1u};
-  const CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                        const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <int D, bool BF16>
 cudaError_t launch(const PromptArgs& a, cudaStream_t st) {
   CUtensorMap mq, mk, mv;
-  cudaError_t e = encode(&mq, a.q, D, a.q_heads, a.tokens, a.q_stride, BF16);
-  if (e == cudaSuccess) e = encode(&mk, a.k, D, a.kv_heads, a.tokens, a.k_stride, BF16);
-  if (e == cudaSuccess) e = encode(&mv, a.v, D, a.kv_heads, a.tokens, a.v_stride, BF16);
+  cudaError_t e = encode_heads(&mq, a.q, D, a.q_heads, a.tokens, a.q_stride, BF16, 1, kRows);
+  if (e == cudaSuccess) e = encode_heads(&mk, a.k, D, a.kv_heads, a.tokens, a.k_stride, BF16, 1, kRows);
+  if (e == cudaSuccess) e = encode_heads(&mv, a.v, D, a.kv_heads, a.tokens, a.v_stride, BF16, 1, kRows);
   if (e != cudaSuccess) return e;
   static SmemAttr attr;
   const size_t smem = Cfg<D>::kSmem + (size_t)a.seqs * 4;

@@ -561,7 +561,8 @@ KVQ_API kvq_status kvq_paged_attention_workspace_bytes(const kvq_paged_cache* ca
  * attends any of it. softmax_scale: finite and >= 0; weights are rounded to the config's
  * dtype, sums are fp32 (tokens * 2^15 * |v| must stay below 3e38). max_tokens <=
  * 2^26. workspace: 16-byte aligned, any content, not shared with calls that
- * overlap on the GPU. One launch. */
+ * overlap on the GPU. Two launches (the second merges the partial sums of requests that
+ * several CTAs share, in a fixed order). */
 KVQ_API kvq_status kvq_paged_attention(kvq_paged_cache* cache, int32_t layer, int32_t requests, const void* q,
                                        int64_t q_stride, int32_t max_tokens, int32_t num_q_heads,
                                        const int32_t* cu_tokens, const int32_t* table, const int32_t* lens,
