@@ -26,8 +26,8 @@
 // cuts leaves partial sums, which a second kernel merges in the order of the CTAs.
 //
 // Warps 0-3 and 4-7: softmax of the units; 8: the range's blocks and their
-// queries; 9: tensor core issue; 10: tiles (page ids, scales, L2 prefetch); 12-15: codes
-// and open rows to operands.
+// queries; 9: tensor core issue; 10: tiles (page ids, scales, L2 prefetch); 12-15 and
+// 16-19: codes and open rows to operands, of keys and of values.
 #pragma once
 
 #include "attn_common.cuh"
@@ -36,10 +36,11 @@
 namespace kvq {
 namespace patt {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kRows = 128;  // rows of a unit, keys of a tile
 constexpr int kGroups = kRows / 16;
 constexpr int kInfo = 8;    // tiles looked up ahead
+constexpr int kParts = 4;   // parts handed out ahead
 constexpr int kNever = 0x7fffffff;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kFar = 0x1p20f;
@@ -175,11 +176,11 @@ struct Shared {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], drain;
   uint64_t kv_full[8], kv_empty[8];  // by operand stage
   uint64_t info_full[kInfo], info_empty[kInfo];
-  uint64_t part_full[2], part_empty[2];
+  uint64_t part_full[kParts], part_empty[kParts];
   uint64_t fix_ready[2], fix_free[2];  // by parity of the part: `first` written, read
   uint64_t join_ready, join_done, conv;
   Info info[kInfo];
-  Part part[2];
+  Part part[kParts];
   uint32_t tmem;
   int any_nonfinite[2];
   int first[2][3][128];  // first position in the open page whose value is NaN, +inf, -inf, per channel
@@ -198,14 +199,16 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* s
   return __all_sync(kFull, done);
 }
 
-// The part of step `it`, for one warp; false at the end or on a timeout.
-__device__ __forceinline__ bool take_part(Shared* sh, int it, uint32_t* status, Part& x) {
-  const int slot = it & 1;
-  if (!wait(&sh->part_full[slot], (it >> 1) & 1, status)) return false;
-  x = sh->part[slot];
+// The part of step `it`, for one warp, which gives it back when done with it;
+// null at the end or on a timeout.
+__device__ __forceinline__ const Part* take_part(Shared* sh, int it, uint32_t* status) {
+  const int slot = it % kParts;
+  if (!wait(&sh->part_full[slot], (it / kParts) & 1, status)) return nullptr;
+  return sh->part[slot].b >= 0 ? &sh->part[slot] : nullptr;
+}
+__device__ __forceinline__ void give_part(Shared* sh, int it) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) arrive(&sh->part_empty[slot]);
-  return x.b >= 0;
+  if ((threadIdx.x & 31) == 0) arrive(&sh->part_empty[it % kParts]);
 }
 
 // --------------------------------------------------------------------------
@@ -251,8 +254,8 @@ __device__ __forceinline__ void part_role(const Params& p, Shared* sh, unsigned 
       x.t = 0;
       if (++x.i == k.count()) x.i = 0, ++x.lot;
     }
-    const int slot = it & 1;
-    if (it >= 2 && !wait(&sh->part_empty[slot], ((it >> 1) - 1) & 1, status, kLongPolls)) break;
+    const int slot = it % kParts;
+    if (it >= kParts && !wait(&sh->part_empty[slot], (it / kParts - 1) & 1, status, kLongPolls)) break;
     if (lane == 0) {
       sh->part[slot] = y;
       arrive(&sh->part_full[slot]);
@@ -310,8 +313,10 @@ __device__ __forceinline__ void tile_role(const Params& p, Shared* sh) {
   const PagedDev& c = p.c;
   const int lane = threadIdx.x & 31, g = lane & 7, ahead = lane >> 3, P = 1 << c.page_shift;
   int i = 0;  // tiles so far
-  Part x;
-  for (int it = 0; take_part(sh, it, c.status, x); ++it) {
+  for (int it = 0;; ++it) {
+    const Part* at = take_part(sh, it, c.status);
+    if (!at) return;
+    const Part& x = *at;
     const int full = x.n & ~(P - 1);
     const int32_t* row = p.a.table + (int64_t)x.b * c.max_pages;
     for (int t = x.t0; t < x.t1; t += 4) {  // four tiles at a time
@@ -352,6 +357,7 @@ __device__ __forceinline__ void tile_role(const Params& p, Shared* sh) {
         if (lane == 0) arrive(&sh->info_full[slot]);
       }
     }
+    give_part(sh, it);
   }
 }
 
@@ -453,7 +459,10 @@ __device__ __forceinline__ void finite8(uint4& x, int pos, int ch, int (*first)[
   x = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int D, int CODE, bool BF16>
+// One of the two groups of four warps: keys (WHICH 0) or values (1). Each has a
+// tile's time for its operand, so that the codes' way from L2 (no load is left
+// on its way over the fence) hides behind the other group's work.
+template <int D, int CODE, bool BF16, int WHICH>
 __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsigned char* ring) {
   using C = Cfg<D>;
   constexpr int kPasses = D / 16, kStep = 2048 / D;  // passes over a tile, rows of one
@@ -461,222 +470,182 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
   const int tid = threadIdx.x & 127, lane = threadIdx.x & 31, P = 1 << c.page_shift;
   const Place<D> at(tid);
   const int ch = at.channel();
-  uint4 x[kPasses];  // codes of the next operand
-  int i = 0, tile = 0;  // operands and tiles so far
-  uint32_t conv_phase = 0;
-  Part y;
-  y.h = 0;
-
-  // codes of pass k of the tile's keys or values (which = 0, 1), all of it pages
-  auto load = [&](const Info& info, int which, int k) {
-    const int row = k * kStep + at.row;
-    const int64_t ph = ((int64_t)info.page[which][row >> 4] * c.heads + y.h) * 2 + which;
-    return *reinterpret_cast<const uint4*>(c.pages + ((ph << c.page_shift) + (row & (P - 1))) * D + ch);
-  };
-  for (int it = 0; take_part(sh, it, c.status, y); ++it) {
-    const int par = it & 1, full = y.n & ~(P - 1);
-    // the rows of the part before the last have read what this one may overwrite
-    if (!wait(&sh->fix_free[par], ((it >> 1) & 1) ^ 1, c.status)) return;
-    if (sh->any_nonfinite[par]) {
-      __syncwarp();
-      if (lane == 0) arrive(&sh->conv);
-      if (!wait(&sh->conv, conv_phase, c.status)) return;
-      for (int k = tid; k < 3 * 128; k += 128) sh->first[par][k / 128][k % 128] = kNever;
-      if (tid == 0) sh->any_nonfinite[par] = 0;
-      __syncwarp();
-      if (lane == 0) arrive(&sh->conv);
-      if (!wait(&sh->conv, conv_phase ^ 1, c.status)) return;
+  int tile = 0;  // tiles so far
+  for (int it = 0;; ++it) {
+    const Part* part = take_part(sh, it, c.status);
+    if (!part) return;
+    const int par = it & 1, t1 = part->t1, head = part->h;
+    if (WHICH == 1) {
+      // the rows of the part before the last have read what this one may overwrite
+      if (!wait(&sh->fix_free[par], ((it >> 1) & 1) ^ 1, c.status)) return;
+      if (sh->any_nonfinite[par]) {
+        __syncwarp();
+        if (lane == 0) arrive(&sh->conv);
+        if (!wait(&sh->conv, 0, c.status)) return;
+        for (int k = tid; k < 3 * 128; k += 128) sh->first[par][k / 128][k % 128] = kNever;
+        if (tid == 0) sh->any_nonfinite[par] = 0;
+        __syncwarp();
+        if (lane == 0) arrive(&sh->conv);
+        if (!wait(&sh->conv, 1, c.status)) return;
+      }
     }
-    bool loaded = false;  // x holds the codes of the next operand
-    for (int t = y.t0; t < y.t1; ++t, ++tile) {
-      const int slot = tile % kInfo;
-      Info& info = sh->info[slot];
+    for (int t = part->t0; t < t1; ++t, ++tile) {
+      const int slot = tile % kInfo, i = 2 * tile + WHICH, st = i % C::kStages;
+      const Info& info = sh->info[slot];
+      unsigned char* to = ring + st * C::kTile;
       if (!wait(&sh->info_full[slot], (tile / kInfo) & 1, c.status)) return;
-      bool next_coded = false;
-      const int next_slot = (tile + 1) % kInfo;
-      const Info& next = sh->info[next_slot];
+      // codes of pass k, where they are a page's
+      auto load = [&](int k) {
+        const int row = k * kStep + at.row;
+        const int64_t ph = ((int64_t)info.page[WHICH][row >> 4] * c.heads + head) * 2 + WHICH;
+        return *reinterpret_cast<const uint4*>(c.pages + ((ph << c.page_shift) + (row & (P - 1))) * D + ch);
+      };
+      auto put = [&](int k, const uint4& x) {
+        const int row = k * kStep + at.row;
+        put_codes<CODE, BF16, WHICH == 1>(to, row, at.half, at.seg, x,
+                                          WHICH ? __float_as_uint(info.f[row >> 4].w) : 0u);
+      };
+      if (info.coded) {
+        uint4 x[kPasses];
 #pragma unroll
-      for (int which = 0; which < 2; ++which, ++i) {
-        const int st = i % C::kStages;
-        unsigned char* to = ring + st * C::kTile;
-        if (info.coded) {
-          if (!loaded) {
+        for (int k = 0; k < kPasses; ++k) x[k] = load(k);
+        if (!wait(&sh->kv_empty[st], ((i / C::kStages) & 1) ^ 1, c.status)) return;
 #pragma unroll
-            for (int k = 0; k < kPasses; ++k) x[k] = load(info, which, k);
-          }
-          if (which == 1 && t + 1 < y.t1) {
-            if (!wait(&sh->info_full[next_slot], ((tile + 1) / kInfo) & 1, c.status)) return;
-            next_coded = next.coded;
-          }
-          if (!wait(&sh->kv_empty[st], ((i / C::kStages) & 1) ^ 1, c.status)) return;
-          // each pass's registers take the next operand's codes as soon as they are free
-          const bool more = which == 0 || next_coded;
-          const Info& from = which ? next : info;
-#pragma unroll
-          for (int k = 0; k < kPasses; ++k) {
-            const uint4 w = x[k];
-            if (more) x[k] = load(from, which ^ 1, k);
-            const int row = k * kStep + at.row;
-            if (which == 0) put_codes<CODE, BF16, false>(to, row, at.half, at.seg, w, 0u);
-            else put_codes<CODE, BF16, true>(to, row, at.half, at.seg, w, __float_as_uint(info.f[row >> 4].w));
-          }
-          loaded = more;
-        } else {
-          loaded = false;
-          if (!wait(&sh->kv_empty[st], ((i / C::kStages) & 1) ^ 1, c.status)) return;
-          const uint16_t* tail = c.tails + (((((int64_t)y.b * c.heads + y.h) * 2 + which) << c.page_shift)) * D + ch;
+        for (int k = 0; k < kPasses; ++k) put(k, x[k]);
+      } else {
+        const int n = part->n, full = n & ~(P - 1);
+        const uint16_t* tail = c.tails + (((((int64_t)part->b * c.heads + head) * 2 + WHICH) << c.page_shift)) * D + ch;
+        if (!wait(&sh->kv_empty[st], ((i / C::kStages) & 1) ^ 1, c.status)) return;
 #pragma unroll 1
-          for (int k0 = 0; k0 < kPasses; k0 += 4) {
-            uint4 a[4], b[4];
-            int page[4];
+        for (int k0 = 0; k0 < kPasses; k0 += 2) {
+          uint4 a[2], b[2];
+          int page[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int row = (k0 + k) * kStep + at.row, pos = t * kRows + row;
-              page[k] = info.page[which][row >> 4];
-              a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
-              if (page[k] >= 0) {
-                a[k] = load(info, which, k0 + k);
-              } else if (page[k] == -1 && pos < y.n) {
-                const uint4* src = reinterpret_cast<const uint4*>(tail + (int64_t)(pos - full) * D);
-                a[k] = src[0];
-                b[k] = src[1];
-              }
+          for (int k = 0; k < 2; ++k) {
+            const int row = (k0 + k) * kStep + at.row, pos = t * kRows + row;
+            page[k] = info.page[WHICH][row >> 4];
+            a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (page[k] >= 0) {
+              a[k] = load(k0 + k);
+            } else if (page[k] == -1 && pos < n) {
+              const uint4* src = reinterpret_cast<const uint4*>(tail + (int64_t)(pos - full) * D);
+              a[k] = src[0];
+              b[k] = src[1];
             }
+          }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int row = (k0 + k) * kStep + at.row, pos = t * kRows + row;
-              if (page[k] >= 0) {
-                if (which == 0) put_codes<CODE, BF16, false>(to, row, at.half, at.seg, a[k], 0u);
-                else put_codes<CODE, BF16, true>(to, row, at.half, at.seg, a[k], __float_as_uint(info.f[row >> 4].w));
-              } else {
-                if (which == 1) {
-                  finite8<BF16>(a[k], pos, ch, sh->first[par], &sh->any_nonfinite[par]);
-                  finite8<BF16>(b[k], pos, ch + 8, sh->first[par], &sh->any_nonfinite[par]);
-                }
-                put16(to, row, at.half, at.seg, a[k], b[k]);
+          for (int k = 0; k < 2; ++k) {
+            const int row = (k0 + k) * kStep + at.row, pos = t * kRows + row;
+            if (page[k] >= 0) {
+              put(k0 + k, a[k]);
+            } else {
+              if (WHICH == 1) {
+                finite8<BF16>(a[k], pos, ch, sh->first[par], &sh->any_nonfinite[par]);
+                finite8<BF16>(b[k], pos, ch + 8, sh->first[par], &sh->any_nonfinite[par]);
               }
+              put16(to, row, at.half, at.seg, a[k], b[k]);
             }
           }
         }
-        fence_proxy_async_smem();  // the tensor cores read what was written here
-        __syncwarp();
-        if (lane == 0) arrive(&sh->kv_full[st]);
       }
+      fence_proxy_async_smem();  // the tensor cores read what was written here
       __syncwarp();
-      if (lane == 0) arrive(&sh->info_empty[slot]);
+      if (lane == 0) {
+        arrive(&sh->kv_full[st]);
+        arrive(&sh->info_empty[slot]);
+      }
     }
-    __syncwarp();
-    if (lane == 0) arrive(&sh->fix_ready[par]);
+    if (WHICH == 1) {
+      __syncwarp();
+      if (lane == 0) arrive(&sh->fix_ready[par]);
+    }
+    give_part(sh, it);
   }
 }
 
 // --------------------------------------------------------------------------
 // Products
 // --------------------------------------------------------------------------
+// Operand descriptors differ in the lower word only (address, stride); the
+// upper one says 1024 bytes between groups of eight rows and the 128-byte swizzle.
+__device__ __forceinline__ uint64_t operand(uint32_t lower) {
+  return (uint64_t)lower | ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32);
+}
+
 template <int D, bool BF16>
 __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned char* smem) {
   using C = Cfg<D>;
   constexpr uint32_t kQK = t5::instr_desc(128, 128, BF16, false), kPV = t5::instr_desc(128, D, BF16, true);
-  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem = sh->tmem, base = smem_u32(smem) >> 4;
   uint32_t* status = p.c.status;
-  const unsigned char* ring = smem + 2 * C::kTile;
-  const uint64_t dq = t5::smem_desc(smem_u32(smem), 16), dk = t5::smem_desc(smem_u32(ring), 16);
-  const uint64_t dv = t5::smem_desc(smem_u32(ring), kRows * 128);
-  uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-  auto scores = [&](int u, int st) {
-    const uint64_t q = dq + (uint32_t)(u * C::kTile >> 4), k = dk + (uint32_t)(st * C::kTile >> 4);
+  uint32_t phase = 0;  // bits 0, 1: of the units' queries, 2, 3: of their weights
+  // S of unit u from the keys in stage st
+  auto scores = [&](uint32_t u, uint32_t st) {
+    const uint32_t q = (base + u * (C::kTile >> 4)) | (1u << 16), k = (base + (2 + st) * (C::kTile >> 4)) | (1u << 16);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       const uint32_t off = ((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4;
-      t5::mma_ss(tmem + u * 128, q + off, k + off, kQK, kk > 0);
+      t5::mma_ss(tmem + u * 128, operand(q + off), operand(k + off), kQK, kk > 0);
     }
     t5::commit(&sh->s_full[u]);
   };
-  auto values = [&](int u, int st, bool first) {
-    const uint64_t v = dv + (uint32_t)(st * C::kTile >> 4);
+  auto values = [&](uint32_t u, uint32_t st, bool first) {
+    const uint32_t v = (base + (2 + st) * (C::kTile >> 4)) | ((kRows * 128 >> 4) << 16);
 #pragma unroll
     for (int kk = 0; kk < kRows / 16; ++kk)
-      t5::mma_ts(tmem + 256 + u * D, tmem + u * 128 + kk * 8, v + kk * (2048 >> 4), kPV, !first || kk > 0);
+      t5::mma_ts(tmem + 256 + u * D, tmem + u * 128 + 64 + kk * 8, operand(v + kk * (2048 >> 4)), kPV, !first || kk > 0);
   };
-  auto full = [&](int x) { return wait(&sh->kv_full[x % C::kStages], (x / C::kStages) & 1, status); };
-  auto query = [&](int u) {
-    const bool ok = wait(&sh->q_full[u], q_phase[u], status);
-    q_phase[u] ^= 1;
+  auto full = [&](uint32_t x) { return wait(&sh->kv_full[x % C::kStages], (x / C::kStages) & 1, status); };
+  auto query = [&](uint32_t u) {
+    const bool ok = wait(&sh->q_full[u], (phase >> u) & 1, status);
+    phase ^= 1u << u;
     return ok;
   };
-  auto weights = [&](int u) {
-    const bool ok = wait(&sh->p_full[u], p_phase[u], status);
-    p_phase[u] ^= 1;
+  auto weights = [&](uint32_t u) {
+    const bool ok = wait(&sh->p_full[u], (phase >> (2 + u)) & 1, status);
+    phase ^= 4u << u;
     t5::fence_after();
     return ok;
   };
-  int i = 0;  // operands before this part
+  uint32_t i = 0;  // operands before this part
   bool ok = true;
-  Part y;
-  for (int it = 0; ok && take_part(sh, it, status, y); ++it) {
-    const int n = y.t1 - y.t0;
-    if (y.both) {
-      ok = full(i);
-      t5::fence_after();
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        ok = ok && query(u);
+  for (int it = 0; ok; ++it) {
+    const Part* at = take_part(sh, it, status);
+    if (!at) break;
+    const int n = at->t1 - at->t0;
+    const bool both = at->both;
+    give_part(sh, it);
+    // Steps of (unit, tile): with two units of rows each tile is both's in turn,
+    // else unit and tile alternate. A step's products are PV of its tile, then S of
+    // the unit's next one; the first S of each unit come before.
+    const int steps = both ? 2 * n : n, ahead = both ? 2 : (n > 1 ? 2 : 1);
+#pragma unroll 1
+    for (int x = -ahead; x < steps && ok; ++x) {
+      const uint32_t u = x & 1;  // -2: unit 0, -1: unit 1 (or, of one tile alone, unit 0)
+      const uint32_t unit = ahead == 1 ? 0u : u;
+      if (x >= 0) {
+        const uint32_t j = both ? x >> 1 : x, v = i + 2 * j + 1;
+        if (!both || u == 0) ok = full(v);
+        ok = ok && weights(unit);
         if (ok && t5::elect_one()) {
-          scores(u, i % C::kStages);
-          if (n == 1) t5::commit(&sh->q_empty[u]);
-          if (u) t5::commit(&sh->kv_empty[i % C::kStages]);
+          values(unit, v % C::kStages, x < 2);
+          if (x + 2 >= steps) t5::commit(&sh->o_done[unit]);
+          if (!both || u) t5::commit(&sh->kv_empty[v % C::kStages]);
         }
         __syncwarp();
       }
-      for (int j = 0; j < n && ok; ++j) {
-        const int v = i + 2 * j + 1, k = v + 1;
-        const bool more = j + 1 < n;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (u == 0) ok = ok && full(v);
-          ok = ok && weights(u);
-          if (ok && t5::elect_one()) {
-            values(u, v % C::kStages, j == 0);
-            if (!more) t5::commit(&sh->o_done[u]);
-            if (u) t5::commit(&sh->kv_empty[v % C::kStages]);
-          }
-          __syncwarp();
-          if (!more) continue;
-          if (u == 0) ok = ok && full(k);
-          if (ok && t5::elect_one()) {
-            scores(u, k % C::kStages);
-            if (j + 1 == n - 1) t5::commit(&sh->q_empty[u]);
-            if (u) t5::commit(&sh->kv_empty[k % C::kStages]);
-          }
-          __syncwarp();
-        }
-      }
-    } else {  // tile j is unit j & 1's
-      auto one = [&](int j) {
-        const int u = j & 1, k = i + 2 * j;
-        if (j < 2) ok = ok && query(u);
-        ok = ok && full(k);
+      const int y = x + ahead;  // the step whose scores come now
+      if (y < steps) {
+        const uint32_t j = both ? y >> 1 : y, k = i + 2 * j;
+        if (x < 0) ok = ok && query(unit);
+        if (!both || u == 0) ok = ok && full(k);
         t5::fence_after();
         if (ok && t5::elect_one()) {
-          scores(u, k % C::kStages);
-          if (j + 2 >= n) t5::commit(&sh->q_empty[u]);
-          t5::commit(&sh->kv_empty[k % C::kStages]);
+          scores(unit, k % C::kStages);
+          if (y + 2 >= steps) t5::commit(&sh->q_empty[unit]);
+          if (!both || u) t5::commit(&sh->kv_empty[k % C::kStages]);
         }
         __syncwarp();
-      };
-      one(0);
-      if (n > 1) one(1);
-      for (int j = 0; j < n && ok; ++j) {
-        const int u = j & 1, v = i + 2 * j + 1;
-        ok = ok && full(v);
-        ok = ok && weights(u);
-        if (ok && t5::elect_one()) {
-          values(u, v % C::kStages, j < 2);
-          if (j + 2 >= n) t5::commit(&sh->o_done[u]);
-          t5::commit(&sh->kv_empty[v % C::kStages]);
-        }
-        __syncwarp();
-        if (j + 2 < n) one(j + 2);
       }
     }
     i += 2 * n;
@@ -726,9 +695,10 @@ struct Reference {
 
   __device__ __forceinline__ void reset() { m = -INFINITY, far = any_far = false; }
   __device__ __forceinline__ float lift() const { return far ? kLift : 0.0f; }
-  __device__ __forceinline__ void raise(float top, float& l, uint32_t tO, bool o) {
+  // true where a row of the warp moved
+  __device__ __forceinline__ bool raise(float top, float& l, uint32_t tO, bool o) {
     const bool up = top - m > 8.0f + (far ? 0.0f : kLift);
-    if (!__any_sync(kFull, up)) return;
+    if (!__any_sync(kFull, up)) return false;
     float f = 1.0f;
     if (up) {
       const float was = m, was_lift = lift();
@@ -738,7 +708,7 @@ struct Reference {
     }
     any_far = __any_sync(kFull, far);
     l *= f;
-    if (!o) return;
+    if (!o) return true;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       uint32_t x[32];
@@ -748,15 +718,38 @@ struct Reference {
       for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
       t5::st32(tO + c, x);
     }
+    return true;
   }
   // what is added to the scaled scores of a group, but for its log2 f
   __device__ __forceinline__ float off() const { return far ? kLift : m == -INFINITY ? 0.0f : -m; }
-  // 16 scores of a far row: scaled, less the reference; a: the factor left for to_weights
-  __device__ __forceinline__ void settle(uint32_t* s, float& a) const {
-    if (!any_far) return;
+  // 16 scores of a far row: scaled, less the reference. Factor: what is left for to_weights.
+  __device__ __forceinline__ void settle(uint32_t* s, float a) const {
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = far ? __float_as_uint(__fmul_rn(__uint_as_float(s[i]), a) - m) : s[i];
-    a = far ? 1.0f : a;
+  }
+  __device__ __forceinline__ float factor(float a) const { return far ? 1.0f : a; }
+};
+
+// A group's factors, read here and not earlier (the compiler would keep all eight
+// groups' in registers, and the scores out of them).
+__device__ __forceinline__ float4 group_factors(const Info& info, int g) {
+  float4 f;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
+               : "r"(smem_u32(&info.f[g])));
+  return f;
+}
+
+// What row r of a unit is: its token of the block, its head of the unit.
+struct RowOf {
+  int token, head;
+  bool live;
+  __device__ __forceinline__ RowOf(const Params& p, const Part& y, int unit, int r) {
+    asm volatile("" : "+r"(r));
+    const int tok = r / p.unit_heads;
+    head = r - tok * p.unit_heads;
+    token = (y.both ? unit * p.unit_tokens : 0) + tok;
+    live = tok < p.unit_tokens && head < y.heads && token < y.tokens;
   }
 };
 
@@ -765,19 +758,19 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, r = warp * 32 + lane;
   uint32_t* status = p.c.status;
   const uint32_t lanes = sh->tmem + ((uint32_t)(warp * 32) << 16);
-  const uint32_t tS = lanes + unit * 128, tP = tS, tO = lanes + 256 + unit * D, tO_other = lanes + 256 + (1 - unit) * D;
-  const int tok = r / p.unit_heads, head = r - tok * p.unit_heads;
-  const bool wide = (reinterpret_cast<uintptr_t>(p.a.out) & 31) == 0;
-  const bool wide_part = (reinterpret_cast<uintptr_t>(p.part_o) & 31) == 0;
+  const uint32_t tS = lanes + unit * 128, tP = tS + 64, tO = lanes + 256 + unit * D, tO_other = lanes + 256 + (1 - unit) * D;
   Reference<D, BF16> ref;
-  uint32_t s_phase = 0, out_phase[2] = {0, 0}, join_phase = 0;
+  uint32_t phase = 0;  // bits 0: scores, 1, 2: the units' outputs, 3: joins
   int tile = 0;
-  Part y;
-  for (int it = 0; take_part(sh, it, status, y); ++it) {
-    const int my_token = (y.both ? unit * p.unit_tokens : 0) + tok;  // of the block
-    const bool live = tok < p.unit_tokens && head < y.heads && my_token < y.tokens;
-    const bool warp_live = __any_sync(kFull, live);
-    const int pos = y.pos0 + my_token;
+  for (int it = 0;; ++it) {
+    const Part* part = take_part(sh, it, status);
+    if (!part) return;
+    const Part& y = *part;
+    // Keys that the row attends, or none where it is no (token, head) of the
+    // block. (What else the row is gets worked out at the end: registers are short here.)
+    const RowOf row(p, y, unit, r);
+    const int limit = row.live ? y.pos0 + row.token + 1 : kNever;
+    const bool warp_live = __any_sync(kFull, limit != kNever);
     ref.reset();
     float l = 0.0f;
     bool any = false;  // a tile of this unit came before
@@ -785,75 +778,110 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
       const int slot = tile % kInfo;
       if (!wait(&sh->info_full[slot], (tile / kInfo) & 1, status)) return;
       if (y.mine(unit, t)) {
-        if (!wait(&sh->s_full[unit], s_phase, status)) return;
-        s_phase ^= 1;
+        if (!wait(&sh->s_full[unit], phase & 1, status)) return;
+        phase ^= 1;
         t5::fence_after();
         const Info& info = sh->info[slot];
-        const int seen = live ? pos + 1 - t * kRows : kRows;  // keys of the tile that the row attends
+        const int seen = limit - t * kRows;  // keys of the tile that the row attends
         if (!warp_live) {
           // nothing reads these rows' weights
-        } else if (__all_sync(kFull, seen >= kRows)) {
-          uint32_t s[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) t5::ld32(tS + 32 * c, s + 32 * c);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) t5::wait_ld32(s + 32 * c);
-          float top = -INFINITY;
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) top = fmaxf(top, max_of<16>(s + 16 * g) * info.f[g].x);
-          ref.raise(live ? top : -INFINITY, l, tO, any);  // s_full came after the unit's last PV
-          const float off = ref.off();
-          uint64_t sum = 0;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t w[32];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const float4 f = info.f[4 * half + g];
-              float a = f.x;
-              ref.settle(s + 64 * half + 16 * g, a);
-              sum = f2_fma(to_weights<BF16>(s + 64 * half + 16 * g, a, off + f.y, w + 8 * g), f2_pack(f.z, f.z), sum);
-            }
-            t5::st32(tP + 32 * half, w);
-          }
-          float u, v;
-          f2_unpack(sum, u, v);
-          l += u + v;
         } else {
-          // a tile that ends past some row's own key, by groups of 32 keys
-          // (P of a group lies where scores already read were)
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t s[32];
-            t5::ld32(tS + 32 * c, s);
-            t5::wait_ld32(s);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= seen) s[i] = 0xff800000u;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) top = fmaxf(top, max_of<16>(s + 16 * g) * info.f[2 * c + g].x);
-          }
-          ref.raise(live ? top : -INFINITY, l, tO, any);
-          const float off = ref.off();
+          float off;
           uint64_t sum = 0;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t s[32], w[16];
-            t5::ld32(tS + 32 * c, s);
-            t5::wait_ld32(s);
+          // 32 scores to weights. P takes the upper half of the scores' place: of the
+          // keys in descending order, a group's weights lie where scores already read were.
+          auto weights32 = [&](uint32_t* x, int c) {
+            uint32_t w[16];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-              const float4 f = info.f[2 * c + g];
-              float a = f.x;
-              ref.settle(s + 16 * g, a);
-#pragma unroll
-              for (int i = 0; i < 16; ++i)  // masked after the factor: -inf * 0 is NaN
-                s[16 * g + i] = 32 * c + 16 * g + i >= seen ? 0xff800000u
-                                                            : __float_as_uint(fmaf(__uint_as_float(s[16 * g + i]), a, off + f.y));
-              sum = f2_fma(to_weights<BF16>(s + 16 * g, 1.0f, 0.0f, w + 8 * g), f2_pack(f.z, f.z), sum);
+              const float4 f = group_factors(info, 2 * c + g);
+              sum = f2_fma(to_weights<BF16>(x + 16 * g, ref.factor(f.x), off + f.y, w + 8 * g), f2_pack(f.z, f.z), sum);
             }
             t5::st16(tP + 16 * c, w);
+          };
+          if (__all_sync(kFull, seen >= kRows)) {
+            // The lower half of the scores is read twice: for the maximum, and again
+            // once the upper half's registers are free.
+            uint32_t s[64];
+            float top;
+            {
+              uint32_t lo[64];
+              t5::ld32(tS, lo);
+              t5::ld32(tS + 32, lo + 32);
+              t5::ld32(tS + 64, s);
+              t5::wait_ld32(lo);
+              t5::wait_ld32(lo + 32);
+              t5::wait_ld32(s);
+              top = fmaxf(max_of<16>(lo) * info.f[0].x, max_of<16>(lo + 16) * info.f[1].x);
+              t5::ld32(tS + 96, s + 32);
+              top = fmaxf(top, fmaxf(max_of<16>(lo + 32) * info.f[2].x, max_of<16>(lo + 48) * info.f[3].x));
+            }
+            top = fmaxf(top, fmaxf(max_of<16>(s) * info.f[4].x, max_of<16>(s + 16) * info.f[5].x));
+            t5::wait_ld32(s + 32);
+            top = fmaxf(top, fmaxf(max_of<16>(s + 32) * info.f[6].x, max_of<16>(s + 48) * info.f[7].x));
+            // (s_full came after the unit's last PV.) Read again after a rescale of
+            // O: held over it, the scores' registers would push others out of every tile.
+            if (ref.raise(limit != kNever ? top : -INFINITY, l, tO, any)) {
+              t5::ld32(tS + 64, s);
+              t5::ld32(tS + 96, s + 32);
+              t5::wait_ld32(s);
+              t5::wait_ld32(s + 32);
+            }
+            off = ref.off();
+            if (!ref.any_far) {
+              uint32_t a[32];
+              weights32(s + 32, 3);
+              t5::ld32(tS + 32, a);
+              weights32(s, 2);
+              t5::wait_ld32(a);
+              t5::ld32(tS, s);
+              weights32(a, 1);
+              t5::wait_ld32(s);
+              weights32(s, 0);
+            } else {
+#pragma unroll 1
+              for (int c = 3; c >= 0; --c) {
+                t5::ld32(tS + 32 * c, s);
+                t5::wait_ld32(s);
+                ref.settle(s, info.f[2 * c].x);
+                ref.settle(s + 16, info.f[2 * c + 1].x);
+                weights32(s, c);
+              }
+            }
+          } else {
+            // a tile that ends past some row's own key
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s[32];
+              t5::ld32(tS + 32 * c, s);
+              t5::wait_ld32(s);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (32 * c + i >= seen) s[i] = 0xff800000u;
+#pragma unroll
+              for (int g = 0; g < 2; ++g) top = fmaxf(top, max_of<16>(s + 16 * g) * info.f[2 * c + g].x);
+            }
+            ref.raise(limit != kNever ? top : -INFINITY, l, tO, any);
+            off = ref.off();
+#pragma unroll 1
+            for (int c = 3; c >= 0; --c) {
+              uint32_t s[32], w[16];
+              t5::ld32(tS + 32 * c, s);
+              t5::wait_ld32(s);
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const float4 f = info.f[2 * c + g];
+                if (ref.any_far) ref.settle(s + 16 * g, f.x);
+                const float a = ref.factor(f.x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)  // masked after the factor: -inf * 0 is NaN
+                  s[16 * g + i] = 32 * c + 16 * g + i >= seen ? 0xff800000u
+                                                              : __float_as_uint(fmaf(__uint_as_float(s[16 * g + i]), a, off + f.y));
+                sum = f2_fma(to_weights<BF16>(s + 16 * g, 1.0f, 0.0f, w + 8 * g), f2_pack(f.z, f.z), sum);
+              }
+              t5::st16(tP + 16 * c, w);
+            }
           }
           float u, v;
           f2_unpack(sum, u, v);
@@ -868,6 +896,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
       if (lane == 0) arrive(&sh->info_empty[slot]);
     }
 
+    const RowOf end(p, y, unit, r);
+    const bool live = end.live;
+    const int head = end.head, my_token = end.token, pos = y.pos0 + my_token;
     const int par = it & 1;
     if (!wait(&sh->fix_ready[par], (it >> 1) & 1, status)) return;
     const bool fix = sh->any_nonfinite[par] != 0;
@@ -880,11 +911,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
       sh->join[unit][r][1] = l;
       sh->join[unit][r][2] = mine;
       // (a unit without a tile has m = -inf and l = 0)
-      if (!wait(&sh->o_done[0], out_phase[0], status)) return;
-      if (y.has(1) && !wait(&sh->o_done[1], out_phase[1], status)) return;
+      if (!wait(&sh->o_done[0], (phase >> 1) & 1, status)) return;
+      if (y.has(1) && !wait(&sh->o_done[1], (phase >> 2) & 1, status)) return;
       t5::fence_after();
       arrive(&sh->join_ready);
-      if (!wait(&sh->join_ready, join_phase, status)) return;
+      if (!wait(&sh->join_ready, (phase >> 3) & 1, status)) return;
       const float top2 = sh->join[1 - unit][r][0], l2 = sh->join[1 - unit][r][1];
       const float best = fmaxf(top, top2), base = best == -INFINITY ? 0.0f : best;
       const float f1 = exp2_fast(top - base), f2 = exp2_fast(top2 - base);
@@ -893,12 +924,13 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
       other = f2 * sh->join[1 - unit][r][2];
       top = best;
     } else if (y.has(unit)) {
-      if (!wait(&sh->o_done[unit], out_phase[unit], status)) return;
+      if (!wait(&sh->o_done[unit], (phase >> (1 + unit)) & 1, status)) return;
       t5::fence_after();
     }
-    out_phase[0] ^= 1;
-    if (y.has(1)) out_phase[1] ^= 1;
+    phase ^= y.has(1) ? 6 : 2;
 
+    const bool wide = (reinterpret_cast<uintptr_t>(p.a.out) & 31) == 0;
+    const bool wide_part = (reinterpret_cast<uintptr_t>(p.part_o) & 31) == 0;
     const int c0 = y.both ? 0 : unit * (D / 2), c1 = y.both ? D : c0 + D / 2;
     const bool own = y.both || y.has(unit), both_o = !y.both && y.has(1);
     const float scale = y.slot < 0 ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
@@ -950,12 +982,13 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
     if (!y.both) {
       t5::fence_before();
       arrive(&sh->join_done);
-      if (!wait(&sh->join_done, join_phase, status)) return;
-      join_phase ^= 1;
+      if (!wait(&sh->join_done, (phase >> 3) & 1, status)) return;
+      phase ^= 8;
     }
     t5::fence_before();  // O has been read: ordered before the next part's first weights
     __syncwarp();
     if (lane == 0) arrive(&sh->fix_free[par]);
+    give_part(sh, it);
   }
 }
 
@@ -1030,10 +1063,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], 128);
       mbar_init(&sh.o_done[i], 1);
-      mbar_init(&sh.part_full[i], 1);
-      mbar_init(&sh.part_empty[i], 14);  // every warp but the one that fills it and the idle one
       mbar_init(&sh.fix_ready[i], 4);
       mbar_init(&sh.fix_free[i], 8);
+    }
+    for (int i = 0; i < kParts; ++i) {
+      mbar_init(&sh.part_full[i], 1);
+      mbar_init(&sh.part_empty[i], 18);  // every warp but the one that fills it and the idle one
     }
     mbar_init(&sh.drain, 1);
     mbar_init(&sh.join_ready, 256);
@@ -1045,7 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     }
     for (int i = 0; i < kInfo; ++i) {
       mbar_init(&sh.info_full[i], 1);
-      mbar_init(&sh.info_empty[i], 12);
+      mbar_init(&sh.info_empty[i], 16);
     }
     mbar_fence_init();
     sh.any_nonfinite[0] = sh.any_nonfinite[1] = 0;
@@ -1061,18 +1096,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     if (blockIdx.x == gridDim.x - 1) p.pos[gridDim.x] = make_int4(p.a.requests, 0, 0, 0);
   }
 
-  // 256 threads x 176 + 128 x 72 + 128 x 88 registers = 512 x 128, what the launch holds
+  // 256 threads x 152 + 128 x 48 + 256 x 64 registers = 640 x 96, what the launch holds
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     softmax_role<D, BF16>(p, &sh, warp >> 2);
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == 8) part_role<D>(p, &sh, smem);
     else if (warp == 9) mma_role<D, BF16>(p, &sh, smem);
     else if (warp == 10) tile_role<D, CODE, BF16>(p, &sh);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    convert_role<D, CODE, BF16>(p, &sh, smem + 2 * C::kTile);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp < 16) convert_role<D, CODE, BF16, 0>(p, &sh, smem + 2 * C::kTile);
+    else convert_role<D, CODE, BF16, 1>(p, &sh, smem + 2 * C::kTile);
   }
   __syncwarp();
   t5::fence_before();
