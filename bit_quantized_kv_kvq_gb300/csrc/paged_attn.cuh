@@ -26,8 +26,8 @@
 // cuts leaves partial sums, which a second kernel merges in the order of the CTAs.
 //
 // Warps 0-3 and 4-7: softmax of the units; 8: the range's blocks and their
-// queries; 9: tensor core issue; 10: tiles (page ids, scales, L2 prefetch); 12-15 and
-// 16-19: codes and open rows to operands, of keys and of values.
+// queries; 9: tensor core issue; 10: tiles (page ids, scales, copies of their codes);
+// 12-19: codes and open rows to operands.
 #pragma once
 
 #include "attn_common.cuh"
@@ -52,8 +52,10 @@ constexpr int kExtra = 6;
 template <int D>
 struct Cfg {
   static constexpr int kTile = kRows * D * 2;       // bytes of a Q, K or V operand
-  static constexpr int kStages = D == 128 ? 4 : 8;  // K and V operands
-  static constexpr int kSmem = 1024 + (2 + kStages) * kTile;
+  static constexpr int kStages = D == 128 ? 3 : 6;  // K and V operands
+  static constexpr int kRaw = kRows * D;            // bytes of an operand's codes
+  static constexpr int kRaws = D == 128 ? 3 : 6;    // codes in flight
+  static constexpr int kSmem = 1024 + (2 + kStages) * kTile + kRaws * kRaw;
 };
 
 struct Params {
@@ -175,6 +177,7 @@ struct Part {
 struct Shared {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], drain;
   uint64_t kv_full[8], kv_empty[8];  // by operand stage
+  uint64_t raw_full[6], raw_empty[6];  // by stage of codes
   uint64_t info_full[kInfo], info_empty[kInfo];
   uint64_t part_full[kParts], part_empty[kParts];
   uint64_t fix_ready[2], fix_free[2];  // by parity of the part: `first` written, read
@@ -192,9 +195,13 @@ struct Shared {
 // Waits last as long as a few tiles, but the walker's as long as a block.
 constexpr int kPolls = 8 * kWaitLimit, kLongPolls = 64 * kWaitLimit;
 
-// Whole warp: false where the wait gave up.
+// Whole warp: false where the wait gave up. (A rolled loop: unrolled, the many
+// waits of the roles were three quarters of the kernel's code, and its fetches
+// what the warps waited for.)
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* status, int polls = kPolls) {
-  const bool done = mbar_wait_limited(bar, parity, polls, kWaitHintNs);
+  bool done = false;
+#pragma unroll 1
+  for (int k = 0; k < polls && !done; ++k) done = mbar_try_wait_hint(bar, parity, kWaitHintNs);
   if (!done) raise_status(status, kStatusTimeout);
   return __all_sync(kFull, done);
 }
@@ -210,6 +217,21 @@ __device__ __forceinline__ void give_part(Shared* sh, int it) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) arrive(&sh->part_empty[it % kParts]);
 }
+
+// The operands of a part's tiles, numbered in the order in which the products take
+// them: K0 V0 K1 V1 ..., or, where units and tiles alternate, K0 K1 V0 K2 V1 ... . Stages
+// of codes and operands go round in this order, and whoever waits for one waits for all
+// of them, one after the other: of phases seen only now and then a parity would not tell which one it is.
+struct Order {
+  uint32_t base;  // operands before this part
+  int n;          // tiles
+  bool both;
+  __device__ __forceinline__ uint32_t keys(int j) const { return base + (both ? 2 * j : j == 0 ? 0 : 2 * j - 1); }
+  __device__ __forceinline__ uint32_t values(int j) const { return base + (both || j == n - 1 ? 2 * j + 1 : 2 * j + 2); }
+  // operand k of the part: whether it is values, and of which tile
+  __device__ __forceinline__ int which(int k) const { return both ? k & 1 : k == 2 * n - 1 || (k > 0 && (k & 1) == 0); }
+  __device__ __forceinline__ int tile(int k) const { return both || k == 2 * n - 1 || k == 0 ? k >> 1 : k & 1 ? (k + 1) >> 1 : (k >> 1) - 1; }
+};
 
 // --------------------------------------------------------------------------
 // Blocks and their queries
@@ -308,57 +330,95 @@ __device__ __forceinline__ float4 factors(float sk, float sv, float scale_log2, 
   return r;
 }
 
+// Four tiles at a time, a lane for each of their groups of 16 keys. The next
+// four's pages are looked up, and their codes called into L2, before these four go out.
 template <int D, int CODE, bool BF16>
-__device__ __forceinline__ void tile_role(const Params& p, Shared* sh) {
+__device__ __forceinline__ void tile_role(const Params& p, Shared* sh, unsigned char* raw) {
+  using C = Cfg<D>;
   const PagedDev& c = p.c;
   const int lane = threadIdx.x & 31, g = lane & 7, ahead = lane >> 3, P = 1 << c.page_shift;
-  int i = 0;  // tiles so far
-  for (int it = 0;; ++it) {
+  int i = 0;       // tiles so far
+  uint32_t x = 0;  // operands so far
+  bool ok = true;
+  for (int it = 0; ok; ++it) {
     const Part* at = take_part(sh, it, c.status);
-    if (!at) return;
-    const Part& x = *at;
-    const int full = x.n & ~(P - 1);
-    const int32_t* row = p.a.table + (int64_t)x.b * c.max_pages;
-    for (int t = x.t0; t < x.t1; t += 4) {  // four tiles at a time
-      const int pos = (t + ahead) * kRows + 16 * g, live = min(4, x.t1 - t);
-      float4 f = make_float4(p.a.scale_log2, 0.0f, 1.0f, 0.0f);
-      int page_k = -1, page_v = -1;
-      if (ahead < live && pos < full) {
-        const int page = row[pos >> c.page_shift];
-        if (page < 0 || page >= c.num_pages) {
-          raise_status(c.status, kStatusBadIndex);
-          page_k = page_v = -2;
-          f = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);
-        } else {
-          const int64_t ph = ((int64_t)page * c.heads + x.h) * 2;
-          if ((pos & (P - 1)) == 0)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.pages + (ph << c.page_shift) * D),
-                         "r"(2 * P * D)
-                         : "memory");
-          const float2 s = *reinterpret_cast<const float2*>(c.scales + ph);
-          bool zero;
-          f = factors<CODE, BF16>(s.x, s.y, p.a.scale_log2, zero);
-          page_k = page;
-          page_v = zero ? -2 : page;
-        }
+    if (!at) break;
+    const int full = at->n & ~(P - 1), t0 = at->t0, t1 = at->t1, head = at->h;
+    const bool both = at->both;
+    const int32_t* row = p.a.table + (int64_t)at->b * c.max_pages;
+    give_part(sh, it);
+    // -1: no page, -2: a bad one
+    auto page_of = [&](int t) {
+      const int pos = (t + ahead) * kRows + 16 * g;
+      if (t + ahead >= t1 || pos >= full) return -1;
+      const int page = row[pos >> c.page_shift];
+      return page >= 0 && page < c.num_pages ? page : -2;
+    };
+    auto scales_of = [&](int page) {
+      float2 s = make_float2(0.0f, 0.0f);
+      if (page >= 0) {
+        const int64_t ph = ((int64_t)page * c.heads + head) * 2;
+        if ((16 * g & (P - 1)) == 0)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(c.pages + (ph << c.page_shift) * D),
+                       "r"(2 * P * D)
+                       : "memory");
+        s = *reinterpret_cast<const float2*>(c.scales + ph);
       }
-      const uint32_t pages = __ballot_sync(kFull, page_k >= 0 && page_v >= 0);
-      for (int k = 0; k < live; ++k, ++i) {
+      return s;
+    };
+    // copies the codes of tile `tile`'s keys or values
+    auto call = [&](int tile, int which) {
+      const int id = sh->info[tile % kInfo].page[which][g], st = x % C::kRaws;
+      const bool copy = lane < 8 && id >= 0 && (16 * g & (P - 1)) == 0;
+      const uint32_t copies = __popc(__ballot_sync(kFull, copy));
+      if (!wait(&sh->raw_empty[st], ((x / C::kRaws) & 1) ^ 1, c.status)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&sh->raw_full[st], copies * P * D);
+      __syncwarp();
+      if (copy)
+        bulk_g2s(raw + st * C::kRaw + 16 * g * D, c.pages + ((((int64_t)id * c.heads + head) * 2 + which) << c.page_shift) * D,
+                 P * D, &sh->raw_full[st]);
+      ++x;
+      return true;
+    };
+    int page = page_of(t0);
+    float2 s = scales_of(page);
+    for (int t = t0; ok && t < t1; t += 4) {
+      float4 f = make_float4(p.a.scale_log2, 0.0f, 1.0f, 0.0f);
+      bool zero = true;
+      if (page >= 0) f = factors<CODE, BF16>(s.x, s.y, p.a.scale_log2, zero);
+      if (page == -2) {
+        raise_status(c.status, kStatusBadIndex);
+        f = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);
+      }
+      const int page_v = page >= 0 && zero ? -2 : page;
+      const uint32_t coded = __ballot_sync(kFull, page >= 0 && page_v >= 0);
+      const int live = min(4, t1 - t), now = page;
+      page = page_of(t + 4);
+#pragma unroll 1
+      for (int k = 0; ok && k < live; ++k, ++i) {
         const int slot = i % kInfo;
-        if (!wait(&sh->info_empty[slot], ((i / kInfo) & 1) ^ 1, c.status)) return;
+        ok = wait(&sh->info_empty[slot], ((i / kInfo) & 1) ^ 1, c.status);
+        if (!ok) break;
         if (ahead == k) {
           Info& o = sh->info[slot];
           o.f[g] = f;
-          o.page[0][g] = page_k;
+          o.page[0][g] = now;
           o.page[1][g] = page_v;
-          if (g == 0) o.coded = ((pages >> (8 * k)) & 255u) == 255u;
+          if (g == 0) o.coded = ((coded >> (8 * k)) & 255u) == 255u;
         }
         __syncwarp();
         if (lane == 0) arrive(&sh->info_full[slot]);
+        ok = call(i, 0);
+        if (ok && both) ok = call(i, 1);
+        if (ok && !both && t + k > t0) ok = call(i - 1, 1);
+        if (k == 0) s = scales_of(page);
       }
     }
-    give_part(sh, it);
+    if (ok && !both) ok = call(i - 1, 1);
   }
+  __syncwarp();
+  // nothing is in flight into this CTA's shared memory when it ends
+  for (uint32_t y = x > C::kRaws ? x - C::kRaws : 0; y < x; ++y) wait(&sh->raw_full[y % C::kRaws], (y / C::kRaws) & 1, c.status);
 }
 
 // --------------------------------------------------------------------------
@@ -409,33 +469,34 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t up, uint32_t& lo, ui
   if (VALUES) lo = mul2<BF16>(lo, up), hi = mul2<BF16>(hi, up);
 }
 
+// A thread's 16 channels of a row. Eight threads in a row read 128 bytes of codes side
+// by side and write to the operand tile, whose 16-byte chunks are swizzled; with 128
+// channels the two halves of a row fall into the same banks, so the threads of the second
+// half store their two chunks in the other order.
 template <int D>
-struct Place {  // of a thread in a tile: 16 channels of row 16 * pass * (128 / D) + row
+struct Place {
   int row, half, seg;
   __device__ __forceinline__ Place(int tid) {
-    // eight threads on two rows' halves: their 16-byte chunks fall into eight different bank groups
     seg = tid & 3;
-    half = D == 128 ? (tid >> 3) & 1 : 0;
-    row = D == 128 ? ((tid >> 4) << 1) + ((tid >> 2) & 1) : tid >> 2;
+    half = D == 128 ? (tid >> 2) & 1 : 0;
+    row = tid / (D / 16);
   }
   __device__ __forceinline__ int channel() const { return half * 64 + seg * 16; }
+  // the chunk that is stored first, and second
+  __device__ __forceinline__ uint32_t first(int r) const { return half * (kRows * 128) + r * 128 + (((2 * seg + half) ^ (r & 7)) << 4); }
+  __device__ __forceinline__ uint32_t second(int r) const { return first(r) ^ 16; }
 };
 
-// 16 channels of a row of the operand tile: two 16-byte chunks, swizzled.
-__device__ __forceinline__ void put16(unsigned char* tile, int row, int half, int seg, const uint4& a, const uint4& b) {
-  unsigned char* at = tile + half * (kRows * 128) + row * 128;
-  *reinterpret_cast<uint4*>(at + (((2 * seg) ^ (row & 7)) << 4)) = a;
-  *reinterpret_cast<uint4*>(at + (((2 * seg + 1) ^ (row & 7)) << 4)) = b;
-}
-
-template <int CODE, bool BF16, bool VALUES>
-__device__ __forceinline__ void put_codes(unsigned char* tile, int row, int half, int seg, const uint4& x, uint32_t up) {
+template <int D, int CODE, bool BF16, bool VALUES>
+__device__ __forceinline__ void put_codes(unsigned char* tile, const Place<D>& at, int row, const uint4& x, uint32_t up) {
   uint4 a, b;
-  widen4<CODE, BF16, VALUES>(x.x, up, a.x, a.y);
-  widen4<CODE, BF16, VALUES>(x.y, up, a.z, a.w);
-  widen4<CODE, BF16, VALUES>(x.z, up, b.x, b.y);
-  widen4<CODE, BF16, VALUES>(x.w, up, b.z, b.w);
-  put16(tile, row, half, seg, a, b);
+  const bool swap = D == 128 && at.half;
+  widen4<CODE, BF16, VALUES>(swap ? x.z : x.x, up, a.x, a.y);
+  widen4<CODE, BF16, VALUES>(swap ? x.w : x.y, up, a.z, a.w);
+  widen4<CODE, BF16, VALUES>(swap ? x.x : x.z, up, b.x, b.y);
+  widen4<CODE, BF16, VALUES>(swap ? x.y : x.w, up, b.z, b.w);
+  *reinterpret_cast<uint4*>(tile + at.first(row)) = a;
+  *reinterpret_cast<uint4*>(tile + at.second(row)) = b;
 }
 
 // Infinities and NaN of 8 values of an open row: 0 in their place, and where
@@ -459,92 +520,90 @@ __device__ __forceinline__ void finite8(uint4& x, int pos, int ch, int (*first)[
   x = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One of the two groups of four warps: keys (WHICH 0) or values (1). Each has a
-// tile's time for its operand, so that the codes' way from L2 (no load is left
-// on its way over the fence) hides behind the other group's work.
-template <int D, int CODE, bool BF16, int WHICH>
-__device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsigned char* ring) {
+// The codes of pass after pass of an operand that is all pages.
+template <int D, int CODE, bool BF16, bool VALUES>
+__device__ __forceinline__ void convert_codes(unsigned char* to, const Place<D>& at, const uint4* from, const Info& info) {
+  constexpr int kPasses = D / 32, kStep = 4096 / D;
+  uint4 x[kPasses];
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k) x[k] = from[k * 256];
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k) {
+    const int row = k * kStep + at.row;
+    put_codes<D, CODE, BF16, VALUES>(to, at, row, x[k], VALUES ? __float_as_uint(info.f[row >> 4].w) : 0u);
+  }
+}
+
+// Eight warps take every operand together, in the order of the products.
+template <int D, int CODE, bool BF16>
+__device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsigned char* ring, const unsigned char* raw) {
   using C = Cfg<D>;
-  constexpr int kPasses = D / 16, kStep = 2048 / D;  // passes over a tile, rows of one
+  constexpr int kPasses = D / 32, kStep = 4096 / D;  // passes over a tile, rows of one
   const PagedDev& c = p.c;
-  const int tid = threadIdx.x & 127, lane = threadIdx.x & 31, P = 1 << c.page_shift;
+  const int tid = threadIdx.x & 255, lane = threadIdx.x & 31, P = 1 << c.page_shift;
   const Place<D> at(tid);
-  const int ch = at.channel();
-  int tile = 0;  // tiles so far
+  int tiles = 0;  // before this part
   for (int it = 0;; ++it) {
     const Part* part = take_part(sh, it, c.status);
     if (!part) return;
-    const int par = it & 1, t1 = part->t1, head = part->h;
-    if (WHICH == 1) {
-      // the rows of the part before the last have read what this one may overwrite
-      if (!wait(&sh->fix_free[par], ((it >> 1) & 1) ^ 1, c.status)) return;
-      if (sh->any_nonfinite[par]) {
-        __syncwarp();
-        if (lane == 0) arrive(&sh->conv);
-        if (!wait(&sh->conv, 0, c.status)) return;
-        for (int k = tid; k < 3 * 128; k += 128) sh->first[par][k / 128][k % 128] = kNever;
-        if (tid == 0) sh->any_nonfinite[par] = 0;
-        __syncwarp();
-        if (lane == 0) arrive(&sh->conv);
-        if (!wait(&sh->conv, 1, c.status)) return;
-      }
+    const int par = it & 1;
+    const Order order = {2u * tiles, part->t1 - part->t0, part->both};
+    // the rows of the part before the last have read what this one may overwrite
+    if (!wait(&sh->fix_free[par], ((it >> 1) & 1) ^ 1, c.status)) return;
+    if (sh->any_nonfinite[par]) {
+      __syncwarp();
+      if (lane == 0) arrive(&sh->conv);
+      if (!wait(&sh->conv, 0, c.status)) return;
+      for (int k = tid; k < 3 * 128; k += 256) sh->first[par][k / 128][k % 128] = kNever;
+      if (tid == 0) sh->any_nonfinite[par] = 0;
+      __syncwarp();
+      if (lane == 0) arrive(&sh->conv);
+      if (!wait(&sh->conv, 1, c.status)) return;
     }
-    for (int t = part->t0; t < t1; ++t, ++tile) {
-      const int slot = tile % kInfo, i = 2 * tile + WHICH, st = i % C::kStages;
+#pragma unroll 1
+    for (int o = 0; o < 2 * order.n; ++o) {
+      const int which = order.which(o), j = order.tile(o), tile = tiles + j;
+      const uint32_t i = order.base + o, slot = tile % kInfo, st = i % C::kStages, rs = i % C::kRaws;
       const Info& info = sh->info[slot];
       unsigned char* to = ring + st * C::kTile;
-      if (!wait(&sh->info_full[slot], (tile / kInfo) & 1, c.status)) return;
-      // codes of pass k, where they are a page's
-      auto load = [&](int k) {
-        const int row = k * kStep + at.row;
-        const int64_t ph = ((int64_t)info.page[WHICH][row >> 4] * c.heads + head) * 2 + WHICH;
-        return *reinterpret_cast<const uint4*>(c.pages + ((ph << c.page_shift) + (row & (P - 1))) * D + ch);
-      };
-      auto put = [&](int k, const uint4& x) {
-        const int row = k * kStep + at.row;
-        put_codes<CODE, BF16, WHICH == 1>(to, row, at.half, at.seg, x,
-                                          WHICH ? __float_as_uint(info.f[row >> 4].w) : 0u);
-      };
+      const uint4* from = reinterpret_cast<const uint4*>(raw + rs * C::kRaw) + tid;  // of pass k: 256 k further on
+      if (which == 0 && !wait(&sh->info_full[slot], (tile / kInfo) & 1, c.status)) return;
+      if (!wait(&sh->raw_full[rs], (i / C::kRaws) & 1, c.status)) return;
+      if (!wait(&sh->kv_empty[st], ((i / C::kStages) & 1) ^ 1, c.status)) return;
       if (info.coded) {
-        uint4 x[kPasses];
-#pragma unroll
-        for (int k = 0; k < kPasses; ++k) x[k] = load(k);
-        if (!wait(&sh->kv_empty[st], ((i / C::kStages) & 1) ^ 1, c.status)) return;
-#pragma unroll
-        for (int k = 0; k < kPasses; ++k) put(k, x[k]);
+        if (which) convert_codes<D, CODE, BF16, true>(to, at, from, info);
+        else convert_codes<D, CODE, BF16, false>(to, at, from, info);
       } else {
-        const int n = part->n, full = n & ~(P - 1);
-        const uint16_t* tail = c.tails + (((((int64_t)part->b * c.heads + head) * 2 + WHICH) << c.page_shift)) * D + ch;
-        if (!wait(&sh->kv_empty[st], ((i / C::kStages) & 1) ^ 1, c.status)) return;
-#pragma unroll 1
-        for (int k0 = 0; k0 < kPasses; k0 += 2) {
-          uint4 a[2], b[2];
-          int page[2];
+        const int n = part->n, full = n & ~(P - 1), ch = at.channel(), t = part->t0 + j;
+        const uint16_t* tail =
+            c.tails + (((((int64_t)part->b * c.heads + part->h) * 2 + which) << c.page_shift)) * D + ch;
+        const bool swap = D == 128 && at.half;
+        uint4 a[kPasses], b[kPasses];
+        int page[kPasses];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int row = (k0 + k) * kStep + at.row, pos = t * kRows + row;
-            page[k] = info.page[WHICH][row >> 4];
-            a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (page[k] >= 0) {
-              a[k] = load(k0 + k);
-            } else if (page[k] == -1 && pos < n) {
-              const uint4* src = reinterpret_cast<const uint4*>(tail + (int64_t)(pos - full) * D);
-              a[k] = src[0];
-              b[k] = src[1];
-            }
+        for (int k = 0; k < kPasses; ++k) {
+          const int row = k * kStep + at.row, pos = t * kRows + row;
+          page[k] = info.page[which][row >> 4];
+          a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
+          if (page[k] == -1 && pos < n) {
+            const uint4* src = reinterpret_cast<const uint4*>(tail + (int64_t)(pos - full) * D);
+            a[k] = src[0];
+            b[k] = src[1];
           }
+        }
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int row = (k0 + k) * kStep + at.row, pos = t * kRows + row;
-            if (page[k] >= 0) {
-              put(k0 + k, a[k]);
-            } else {
-              if (WHICH == 1) {
-                finite8<BF16>(a[k], pos, ch, sh->first[par], &sh->any_nonfinite[par]);
-                finite8<BF16>(b[k], pos, ch + 8, sh->first[par], &sh->any_nonfinite[par]);
-              }
-              put16(to, row, at.half, at.seg, a[k], b[k]);
+        for (int k = 0; k < kPasses; ++k) {
+          const int row = k * kStep + at.row, pos = t * kRows + row;
+          if (page[k] >= 0) {
+            const uint32_t one = BF16 ? 0x3f803f80u : 0x3c003c00u;  // keys: times 1
+            put_codes<D, CODE, BF16, true>(to, at, row, from[k * 256], which ? __float_as_uint(info.f[row >> 4].w) : one);
+          } else {
+            if (which) {
+              finite8<BF16>(a[k], pos, ch, sh->first[par], &sh->any_nonfinite[par]);
+              finite8<BF16>(b[k], pos, ch + 8, sh->first[par], &sh->any_nonfinite[par]);
             }
+            *reinterpret_cast<uint4*>(to + at.first(row)) = swap ? b[k] : a[k];
+            *reinterpret_cast<uint4*>(to + at.second(row)) = swap ? a[k] : b[k];
           }
         }
       }
@@ -552,13 +611,13 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
       __syncwarp();
       if (lane == 0) {
         arrive(&sh->kv_full[st]);
-        arrive(&sh->info_empty[slot]);
+        arrive(&sh->raw_empty[rs]);
+        if (which) arrive(&sh->info_empty[slot]);
       }
     }
-    if (WHICH == 1) {
-      __syncwarp();
-      if (lane == 0) arrive(&sh->fix_ready[par]);
-    }
+    tiles += order.n;
+    __syncwarp();
+    if (lane == 0) arrive(&sh->fix_ready[par]);
     give_part(sh, it);
   }
 }
@@ -614,6 +673,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned c
     if (!at) break;
     const int n = at->t1 - at->t0;
     const bool both = at->both;
+    const Order order = {i, n, both};
     give_part(sh, it);
     // Steps of (unit, tile): with two units of rows each tile is both's in turn,
     // else unit and tile alternate. A step's products are PV of its tile, then S of
@@ -624,7 +684,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned c
       const uint32_t u = x & 1;  // -2: unit 0, -1: unit 1 (or, of one tile alone, unit 0)
       const uint32_t unit = ahead == 1 ? 0u : u;
       if (x >= 0) {
-        const uint32_t j = both ? x >> 1 : x, v = i + 2 * j + 1;
+        const uint32_t v = order.values(both ? x >> 1 : x);
         if (!both || u == 0) ok = full(v);
         ok = ok && weights(unit);
         if (ok && t5::elect_one()) {
@@ -636,7 +696,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned c
       }
       const int y = x + ahead;  // the step whose scores come now
       if (y < steps) {
-        const uint32_t j = both ? y >> 1 : y, k = i + 2 * j;
+        const uint32_t k = order.keys(both ? y >> 1 : y);
         if (x < 0) ok = ok && query(unit);
         if (!both || u == 0) ok = ok && full(k);
         t5::fence_after();
@@ -1063,7 +1123,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], 128);
       mbar_init(&sh.o_done[i], 1);
-      mbar_init(&sh.fix_ready[i], 4);
+      mbar_init(&sh.fix_ready[i], 8);
       mbar_init(&sh.fix_free[i], 8);
     }
     for (int i = 0; i < kParts; ++i) {
@@ -1073,10 +1133,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     mbar_init(&sh.drain, 1);
     mbar_init(&sh.join_ready, 256);
     mbar_init(&sh.join_done, 256);
-    mbar_init(&sh.conv, 4);
+    mbar_init(&sh.conv, 8);
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&sh.kv_full[i], 4);
+      mbar_init(&sh.kv_full[i], 8);
       mbar_init(&sh.kv_empty[i], 1);
+    }
+    for (int i = 0; i < C::kRaws; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], 8);
     }
     for (int i = 0; i < kInfo; ++i) {
       mbar_init(&sh.info_full[i], 1);
@@ -1104,11 +1168,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == 8) part_role<D>(p, &sh, smem);
     else if (warp == 9) mma_role<D, BF16>(p, &sh, smem);
-    else if (warp == 10) tile_role<D, CODE, BF16>(p, &sh);
+    else if (warp == 10) tile_role<D, CODE, BF16>(p, &sh, smem + (2 + C::kStages) * C::kTile);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp < 16) convert_role<D, CODE, BF16, 0>(p, &sh, smem + 2 * C::kTile);
-    else convert_role<D, CODE, BF16, 1>(p, &sh, smem + 2 * C::kTile);
+    unsigned char* ring = smem + 2 * C::kTile;
+    convert_role<D, CODE, BF16>(p, &sh, ring, ring + C::kStages * C::kTile);
   }
   __syncwarp();
   t5::fence_before();
