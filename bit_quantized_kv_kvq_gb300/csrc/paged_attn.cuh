@@ -852,9 +852,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
           // keys in descending order, a group's weights lie where scores already read were.
           auto weights32 = [&](uint32_t* x, int c) {
             uint32_t w[16];
+            float4 f = group_factors(info, 2 * c);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-              const float4 f = group_factors(info, 2 * c + g);
+              if (g && p.c.page_shift == 4) f = group_factors(info, 2 * c + 1);
               sum = f2_fma(to_weights<BF16>(x + 16 * g, ref.factor(f.x), off + f.y, w + 8 * g), f2_pack(f.z, f.z), sum);
             }
             t5::st16(tP + 16 * c, w);
@@ -949,7 +950,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
         }
         t5::wait_st();
         t5::fence_before();
-        arrive(&sh->p_full[unit]);
+        __syncwarp();
+        if (lane == 0) arrive(&sh->p_full[unit]);
         any = true;
       }
       __syncwarp();
@@ -974,7 +976,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
       if (!wait(&sh->o_done[0], (phase >> 1) & 1, status)) return;
       if (y.has(1) && !wait(&sh->o_done[1], (phase >> 2) & 1, status)) return;
       t5::fence_after();
-      arrive(&sh->join_ready);
+      __syncwarp();
+      if (lane == 0) arrive(&sh->join_ready);
       if (!wait(&sh->join_ready, (phase >> 3) & 1, status)) return;
       const float top2 = sh->join[1 - unit][r][0], l2 = sh->join[1 - unit][r][1];
       const float best = fmaxf(top, top2), base = best == -INFINITY ? 0.0f : best;
@@ -1041,7 +1044,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
     }
     if (!y.both) {
       t5::fence_before();
-      arrive(&sh->join_done);
+      __syncwarp();
+      if (lane == 0) arrive(&sh->join_done);
       if (!wait(&sh->join_done, (phase >> 3) & 1, status)) return;
       phase ^= 8;
     }
@@ -1121,7 +1125,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 128);
+      mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.o_done[i], 1);
       mbar_init(&sh.fix_ready[i], 8);
       mbar_init(&sh.fix_free[i], 8);
@@ -1131,8 +1135,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       mbar_init(&sh.part_empty[i], 18);  // every warp but the one that fills it and the idle one
     }
     mbar_init(&sh.drain, 1);
-    mbar_init(&sh.join_ready, 256);
-    mbar_init(&sh.join_done, 256);
+    mbar_init(&sh.join_ready, 8);
+    mbar_init(&sh.join_done, 8);
     mbar_init(&sh.conv, 8);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sh.kv_full[i], 8);
@@ -1160,12 +1164,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     if (blockIdx.x == gridDim.x - 1) p.pos[gridDim.x] = make_int4(p.a.requests, 0, 0, 0);
   }
 
-  // 256 threads x 152 + 128 x 48 + 256 x 64 registers = 640 x 96, what the launch holds
+  // 256 threads x 144 + 128 x 64 + 256 x 64 registers = 640 x 96, what the launch holds
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     softmax_role<D, BF16>(p, &sh, warp >> 2);
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 8) part_role<D>(p, &sh, smem);
     else if (warp == 9) mma_role<D, BF16>(p, &sh, smem);
     else if (warp == 10) tile_role<D, CODE, BF16>(p, &sh, smem + (2 + C::kStages) * C::kTile);
