@@ -159,10 +159,11 @@ __device__ __forceinline__ Pos locate(const Params& p, int b, const Req& r, long
 // --------------------------------------------------------------------------
 // Shared memory
 // --------------------------------------------------------------------------
-struct Info {
-  float4 f[kGroups];  // per 16 keys: score factor, log2 f, 1 / f, the pair 2^e
-  int page[2][kGroups];  // of keys, of values; -1: open rows or none, -2: zeros
-  int coded;             // all of them pages
+struct alignas(16) Info {  // per 16 keys
+  float2 a[kGroups], lg[kGroups], inv[kGroups];  // score factor, log2 f, 1 / f, twice each: operands of pairs
+  uint32_t up[kGroups];                          // 2^e, a pair of the input type
+  int page[2][kGroups];                          // of keys, of values; -1: open rows or none, -2: zeros
+  int coded;                                     // all of them pages
 };
 
 struct Part {
@@ -401,7 +402,10 @@ __device__ __forceinline__ void tile_role(const Params& p, Shared* sh, unsigned 
         if (!ok) break;
         if (ahead == k) {
           Info& o = sh->info[slot];
-          o.f[g] = f;
+          o.a[g] = make_float2(f.x, f.x);
+          o.lg[g] = make_float2(f.y, f.y);
+          o.inv[g] = make_float2(f.z, f.z);
+          o.up[g] = __float_as_uint(f.w);
           o.page[0][g] = now;
           o.page[1][g] = page_v;
           if (g == 0) o.coded = ((coded >> (8 * k)) & 255u) == 255u;
@@ -476,27 +480,28 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t up, uint32_t& lo, ui
 template <int D>
 struct Place {
   int row, half, seg;
+  uint32_t first, second;  // bytes of its chunks in the tile, in the order in which they are stored
   __device__ __forceinline__ Place(int tid) {
     seg = tid & 3;
     half = D == 128 ? (tid >> 2) & 1 : 0;
     row = tid / (D / 16);
+    first = half * (kRows * 128) + row * 128 + (((2 * seg + half) ^ (row & 7)) << 4);
+    second = first ^ 16;
   }
   __device__ __forceinline__ int channel() const { return half * 64 + seg * 16; }
-  // the chunk that is stored first, and second
-  __device__ __forceinline__ uint32_t first(int r) const { return half * (kRows * 128) + r * 128 + (((2 * seg + half) ^ (r & 7)) << 4); }
-  __device__ __forceinline__ uint32_t second(int r) const { return first(r) ^ 16; }
 };
 
+// Codes of the thread's channels in the row `down` further down (a multiple of 8).
 template <int D, int CODE, bool BF16, bool VALUES>
-__device__ __forceinline__ void put_codes(unsigned char* tile, const Place<D>& at, int row, const uint4& x, uint32_t up) {
+__device__ __forceinline__ void put_codes(unsigned char* tile, const Place<D>& at, int down, const uint4& x, uint32_t up) {
   uint4 a, b;
   const bool swap = D == 128 && at.half;
   widen4<CODE, BF16, VALUES>(swap ? x.z : x.x, up, a.x, a.y);
   widen4<CODE, BF16, VALUES>(swap ? x.w : x.y, up, a.z, a.w);
   widen4<CODE, BF16, VALUES>(swap ? x.x : x.z, up, b.x, b.y);
   widen4<CODE, BF16, VALUES>(swap ? x.y : x.w, up, b.z, b.w);
-  *reinterpret_cast<uint4*>(tile + at.first(row)) = a;
-  *reinterpret_cast<uint4*>(tile + at.second(row)) = b;
+  *reinterpret_cast<uint4*>(tile + at.first + down * 128) = a;
+  *reinterpret_cast<uint4*>(tile + at.second + down * 128) = b;
 }
 
 // Infinities and NaN of 8 values of an open row: 0 in their place, and where
@@ -529,8 +534,7 @@ __device__ __forceinline__ void convert_codes(unsigned char* to, const Place<D>&
   for (int k = 0; k < kPasses; ++k) x[k] = from[k * 256];
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {
-    const int row = k * kStep + at.row;
-    put_codes<D, CODE, BF16, VALUES>(to, at, row, x[k], VALUES ? __float_as_uint(info.f[row >> 4].w) : 0u);
+    put_codes<D, CODE, BF16, VALUES>(to, at, k * kStep, x[k], VALUES ? info.up[(k * kStep + at.row) >> 4] : 0u);
   }
 }
 
@@ -596,14 +600,14 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
           const int row = k * kStep + at.row, pos = t * kRows + row;
           if (page[k] >= 0) {
             const uint32_t one = BF16 ? 0x3f803f80u : 0x3c003c00u;  // keys: times 1
-            put_codes<D, CODE, BF16, true>(to, at, row, from[k * 256], which ? __float_as_uint(info.f[row >> 4].w) : one);
+            put_codes<D, CODE, BF16, true>(to, at, k * kStep, from[k * 256], which ? info.up[row >> 4] : one);
           } else {
             if (which) {
               finite8<BF16>(a[k], pos, ch, sh->first[par], &sh->any_nonfinite[par]);
               finite8<BF16>(b[k], pos, ch + 8, sh->first[par], &sh->any_nonfinite[par]);
             }
-            *reinterpret_cast<uint4*>(to + at.first(row)) = swap ? b[k] : a[k];
-            *reinterpret_cast<uint4*>(to + at.second(row)) = swap ? a[k] : b[k];
+            *reinterpret_cast<uint4*>(to + at.first + k * kStep * 128) = swap ? b[k] : a[k];
+            *reinterpret_cast<uint4*>(to + at.second + k * kStep * 128) = swap ? a[k] : b[k];
           }
         }
       }
@@ -625,90 +629,141 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
 // --------------------------------------------------------------------------
 // Products
 // --------------------------------------------------------------------------
-// Operand descriptors differ in the lower word only (address, stride); the
-// upper one says 1024 bytes between groups of eight rows and the 128-byte swizzle.
-__device__ __forceinline__ uint64_t operand(uint32_t lower) {
-  return (uint64_t)lower | ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32);
+// Tells the compiler that a value is the whole warp's: what the products' operands
+// are made of stays in uniform registers then.
+template <typename T>
+__device__ __forceinline__ T uniform(T x) {
+  return (T)__shfl_sync(kFull, x, 0);
 }
 
+// The issue of the products is as long as the products themselves where it takes
+// more than 64 clocks each, so the two orders are written out, a unit being a constant
+// in each step.
 template <int D, bool BF16>
 __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned char* smem) {
   using C = Cfg<D>;
   constexpr uint32_t kQK = t5::instr_desc(128, 128, BF16, false), kPV = t5::instr_desc(128, D, BF16, true);
-  const uint32_t tmem = sh->tmem, base = smem_u32(smem) >> 4;
+  const uint32_t tmem = uniform(sh->tmem);
   uint32_t* status = p.c.status;
-  uint32_t phase = 0;  // bits 0, 1: of the units' queries, 2, 3: of their weights
-  // S of unit u from the keys in stage st
-  auto scores = [&](uint32_t u, uint32_t st) {
-    const uint32_t q = (base + u * (C::kTile >> 4)) | (1u << 16), k = (base + (2 + st) * (C::kTile >> 4)) | (1u << 16);
+  const unsigned char* ring = smem + 2 * C::kTile;
+  const uint64_t dq = t5::smem_desc(smem_u32(smem), 16), dk = t5::smem_desc(smem_u32(ring), 16);
+  const uint64_t dv = t5::smem_desc(smem_u32(ring), kRows * 128);
+  uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+  uint32_t st = 0, st_phase = 0;  // the next operand's stage
+  bool ok = true;
+  auto next = [&]() {  // waits for the next operand; its stage
+    const uint32_t at = st;
+    ok = ok && wait(&sh->kv_full[at], st_phase, status);
+    if (++st == C::kStages) st = 0, st_phase ^= 1;
+    return at;
+  };
+  // S of unit u from the keys in stage at
+  auto scores = [&](const int u, uint32_t at) {
+    const uint64_t q = dq + (uint32_t)(u * C::kTile >> 4), k = dk + at * (uint32_t)(C::kTile >> 4);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       const uint32_t off = ((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4;
-      t5::mma_ss(tmem + u * 128, operand(q + off), operand(k + off), kQK, kk > 0);
+      t5::mma_ss(tmem + u * 128, q + off, k + off, kQK, kk > 0);
     }
     t5::commit(&sh->s_full[u]);
   };
-  auto values = [&](uint32_t u, uint32_t st, bool first) {
-    const uint32_t v = (base + (2 + st) * (C::kTile >> 4)) | ((kRows * 128 >> 4) << 16);
+  auto values = [&](const int u, uint32_t at, bool first) {
+    const uint64_t v = dv + at * (uint32_t)(C::kTile >> 4);
 #pragma unroll
     for (int kk = 0; kk < kRows / 16; ++kk)
-      t5::mma_ts(tmem + 256 + u * D, tmem + u * 128 + 64 + kk * 8, operand(v + kk * (2048 >> 4)), kPV, !first || kk > 0);
+      t5::mma_ts(tmem + 256 + u * D, tmem + u * 128 + 64 + kk * 8, v + kk * (2048 >> 4), kPV, kk > 0 || !first);
   };
-  auto full = [&](uint32_t x) { return wait(&sh->kv_full[x % C::kStages], (x / C::kStages) & 1, status); };
-  auto query = [&](uint32_t u) {
-    const bool ok = wait(&sh->q_full[u], (phase >> u) & 1, status);
-    phase ^= 1u << u;
-    return ok;
+  auto query = [&](const int u) {
+    ok = ok && wait(&sh->q_full[u], q_phase[u], status);
+    q_phase[u] ^= 1;
   };
-  auto weights = [&](uint32_t u) {
-    const bool ok = wait(&sh->p_full[u], (phase >> (2 + u)) & 1, status);
-    phase ^= 4u << u;
+  auto weights = [&](const int u) {
+    ok = ok && wait(&sh->p_full[u], p_phase[u], status);
+    p_phase[u] ^= 1;
     t5::fence_after();
-    return ok;
   };
-  uint32_t i = 0;  // operands before this part
-  bool ok = true;
   for (int it = 0; ok; ++it) {
-    const Part* at = take_part(sh, it, status);
-    if (!at) break;
-    const int n = at->t1 - at->t0;
-    const bool both = at->both;
-    const Order order = {i, n, both};
+    const Part* part = take_part(sh, it, status);
+    if (!part) break;
+    const int n = uniform(part->t1 - part->t0);
+    const bool both = uniform(part->both);
     give_part(sh, it);
-    // Steps of (unit, tile): with two units of rows each tile is both's in turn,
-    // else unit and tile alternate. A step's products are PV of its tile, then S of
-    // the unit's next one; the first S of each unit come before.
-    const int steps = both ? 2 * n : n, ahead = both ? 2 : (n > 1 ? 2 : 1);
-#pragma unroll 1
-    for (int x = -ahead; x < steps && ok; ++x) {
-      const uint32_t u = x & 1;  // -2: unit 0, -1: unit 1 (or, of one tile alone, unit 0)
-      const uint32_t unit = ahead == 1 ? 0u : u;
-      if (x >= 0) {
-        const uint32_t v = order.values(both ? x >> 1 : x);
-        if (!both || u == 0) ok = full(v);
-        ok = ok && weights(unit);
-        if (ok && t5::elect_one()) {
-          values(unit, v % C::kStages, x < 2);
-          if (x + 2 >= steps) t5::commit(&sh->o_done[unit]);
-          if (!both || u) t5::commit(&sh->kv_empty[v % C::kStages]);
-        }
-        __syncwarp();
-      }
-      const int y = x + ahead;  // the step whose scores come now
-      if (y < steps) {
-        const uint32_t k = order.keys(both ? y >> 1 : y);
-        if (x < 0) ok = ok && query(unit);
-        if (!both || u == 0) ok = ok && full(k);
+    if (both) {
+      uint32_t k = next();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        query(u);
         t5::fence_after();
         if (ok && t5::elect_one()) {
-          scores(unit, k % C::kStages);
-          if (y + 2 >= steps) t5::commit(&sh->q_empty[unit]);
-          if (!both || u) t5::commit(&sh->kv_empty[k % C::kStages]);
+          scores(u, k);
+          if (n == 1) t5::commit(&sh->q_empty[u]);
+          if (u) t5::commit(&sh->kv_empty[k]);
         }
         __syncwarp();
       }
+#pragma unroll 1
+      for (int j = 0; j < n && ok; ++j) {
+        const bool more = j + 1 < n;
+        const uint32_t v = next();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          weights(u);
+          if (ok && t5::elect_one()) {
+            values(u, v, j == 0);
+            if (u) t5::commit(&sh->kv_empty[v]);
+            if (!more) t5::commit(&sh->o_done[u]);
+          }
+          __syncwarp();
+          if (!more) continue;
+          if (u == 0) k = next();
+          if (ok && t5::elect_one()) {
+            scores(u, k);
+            if (u) t5::commit(&sh->kv_empty[k]);
+            if (j + 2 == n) t5::commit(&sh->q_empty[u]);
+          }
+          __syncwarp();
+        }
+      }
+    } else {  // tile j is unit j & 1's
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (u >= n) continue;
+        query(u);
+        const uint32_t k = next();
+        t5::fence_after();
+        if (ok && t5::elect_one()) {
+          scores(u, k);
+          t5::commit(&sh->kv_empty[k]);
+          if (u + 2 >= n) t5::commit(&sh->q_empty[u]);
+        }
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int j0 = 0; j0 < n && ok; j0 += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int j = j0 + u;
+          if (j >= n) continue;
+          const bool more = j + 2 < n;
+          const uint32_t v = next();
+          weights(u);
+          if (ok && t5::elect_one()) {
+            values(u, v, j0 == 0);
+            t5::commit(&sh->kv_empty[v]);
+            if (!more) t5::commit(&sh->o_done[u]);
+          }
+          __syncwarp();
+          if (!more) continue;
+          const uint32_t k = next();
+          if (ok && t5::elect_one()) {
+            scores(u, k);
+            t5::commit(&sh->kv_empty[k]);
+            if (j + 4 >= n) t5::commit(&sh->q_empty[u]);
+          }
+          __syncwarp();
+        }
+      }
     }
-    i += 2 * n;
   }
   __syncwarp();
   if (t5::elect_one()) t5::commit(&sh->drain);
@@ -719,10 +774,9 @@ __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned c
 // --------------------------------------------------------------------------
 // Softmax
 // --------------------------------------------------------------------------
-// 16 scores to weights: p = 2^(s a + off), packed; their sum.
+// 16 scores to weights: p = 2^(s a + off), packed; their sum. a2, off2: each twice.
 template <bool BF16>
-__device__ __forceinline__ uint64_t to_weights(const uint32_t* s, float a, float off, uint32_t* p) {
-  const uint64_t a2 = f2_pack(a, a), off2 = f2_pack(off, off);
+__device__ __forceinline__ uint64_t to_weights(const uint32_t* s, uint64_t a2, uint64_t off2, uint32_t* p) {
   uint64_t sum0, sum1;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -787,18 +841,21 @@ struct Reference {
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = far ? __float_as_uint(__fmul_rn(__uint_as_float(s[i]), a) - m) : s[i];
   }
-  __device__ __forceinline__ float factor(float a) const { return far ? 1.0f : a; }
 };
 
-// A group's factors, read here and not earlier (the compiler would keep all eight
-// groups' in registers, and the scores out of them).
-__device__ __forceinline__ float4 group_factors(const Info& info, int g) {
-  float4 f;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w)
-               : "r"(smem_u32(&info.f[g])));
-  return f;
-}
+// The factors of 32 keys, in pairs, read here and not earlier (the compiler would
+// keep all groups' in registers, and the scores out of them).
+struct Factors {
+  uint64_t a[2], lg[2], inv[2];
+  __device__ __forceinline__ Factors(const Info& info, int c) {
+    two(&info.a[2 * c], a);
+    two(&info.lg[2 * c], lg);
+    two(&info.inv[2 * c], inv);
+  }
+  static __device__ __forceinline__ void two(const float2* from, uint64_t (&to)[2]) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(to[0]), "=l"(to[1]) : "r"(smem_u32(from)));
+  }
+};
 
 // What row r of a unit is: its token of the block, its head of the unit.
 struct RowOf {
@@ -846,19 +903,20 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
         if (!warp_live) {
           // nothing reads these rows' weights
         } else {
-          float off;
-          uint64_t sum = 0;
+          uint64_t sum = 0, off2;
           // 32 scores to weights. P takes the upper half of the scores' place: of the
           // keys in descending order, a group's weights lie where scores already read were.
-          auto weights32 = [&](uint32_t* x, int c) {
+          auto weights32 = [&](uint32_t* x, int c, Factors& f) {
             uint32_t w[16];
-            float4 f = group_factors(info, 2 * c);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              if (g && p.c.page_shift == 4) f = group_factors(info, 2 * c + 1);
-              sum = f2_fma(to_weights<BF16>(x + 16 * g, ref.factor(f.x), off + f.y, w + 8 * g), f2_pack(f.z, f.z), sum);
-            }
+            for (int g = 0; g < 2; ++g)
+              sum = f2_fma(to_weights<BF16>(x + 16 * g, f.a[g], f2_add(off2, f.lg[g]), w + 8 * g), f.inv[g], sum);
+            if (c > 0) f = Factors(info, c - 1);  // the next group's, on their way meanwhile
             t5::st16(tP + 16 * c, w);
+          };
+          auto reference = [&]() {
+            const float off = ref.off();
+            off2 = f2_pack(off, off);
           };
           if (__all_sync(kFull, seen >= kRows)) {
             // The lower half of the scores is read twice: for the maximum, and again
@@ -873,13 +931,13 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
               t5::wait_ld32(lo);
               t5::wait_ld32(lo + 32);
               t5::wait_ld32(s);
-              top = fmaxf(max_of<16>(lo) * info.f[0].x, max_of<16>(lo + 16) * info.f[1].x);
+              top = fmaxf(max_of<16>(lo) * info.a[0].x, max_of<16>(lo + 16) * info.a[1].x);
               t5::ld32(tS + 96, s + 32);
-              top = fmaxf(top, fmaxf(max_of<16>(lo + 32) * info.f[2].x, max_of<16>(lo + 48) * info.f[3].x));
+              top = fmaxf(top, fmaxf(max_of<16>(lo + 32) * info.a[2].x, max_of<16>(lo + 48) * info.a[3].x));
             }
-            top = fmaxf(top, fmaxf(max_of<16>(s) * info.f[4].x, max_of<16>(s + 16) * info.f[5].x));
+            top = fmaxf(top, fmaxf(max_of<16>(s) * info.a[4].x, max_of<16>(s + 16) * info.a[5].x));
             t5::wait_ld32(s + 32);
-            top = fmaxf(top, fmaxf(max_of<16>(s + 32) * info.f[6].x, max_of<16>(s + 48) * info.f[7].x));
+            top = fmaxf(top, fmaxf(max_of<16>(s + 32) * info.a[6].x, max_of<16>(s + 48) * info.a[7].x));
             // (s_full came after the unit's last PV.) Read again after a rescale of
             // O: held over it, the scores' registers would push others out of every tile.
             if (ref.raise(limit != kNever ? top : -INFINITY, l, tO, any)) {
@@ -888,25 +946,30 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
               t5::wait_ld32(s);
               t5::wait_ld32(s + 32);
             }
-            off = ref.off();
+            reference();
             if (!ref.any_far) {
               uint32_t a[32];
-              weights32(s + 32, 3);
+              Factors f(info, 3);
+              weights32(s + 32, 3, f);
               t5::ld32(tS + 32, a);
-              weights32(s, 2);
+              weights32(s, 2, f);
               t5::wait_ld32(a);
               t5::ld32(tS, s);
-              weights32(a, 1);
+              weights32(a, 1, f);
               t5::wait_ld32(s);
-              weights32(s, 0);
+              weights32(s, 0, f);
             } else {
 #pragma unroll 1
               for (int c = 3; c >= 0; --c) {
                 t5::ld32(tS + 32 * c, s);
                 t5::wait_ld32(s);
-                ref.settle(s, info.f[2 * c].x);
-                ref.settle(s + 16, info.f[2 * c + 1].x);
-                weights32(s, c);
+                Factors f(info, c);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                  ref.settle(s + 16 * g, info.a[2 * c + g].x);
+                  if (ref.far) f.a[g] = f2_pack(1.0f, 1.0f);
+                }
+                weights32(s, c, f);
               }
             }
           } else {
@@ -921,10 +984,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
               for (int i = 0; i < 32; ++i)
                 if (32 * c + i >= seen) s[i] = 0xff800000u;
 #pragma unroll
-              for (int g = 0; g < 2; ++g) top = fmaxf(top, max_of<16>(s + 16 * g) * info.f[2 * c + g].x);
+              for (int g = 0; g < 2; ++g) top = fmaxf(top, max_of<16>(s + 16 * g) * info.a[2 * c + g].x);
             }
             ref.raise(limit != kNever ? top : -INFINITY, l, tO, any);
-            off = ref.off();
+            const float off = ref.off();
 #pragma unroll 1
             for (int c = 3; c >= 0; --c) {
               uint32_t s[32], w[16];
@@ -932,14 +995,15 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
               t5::wait_ld32(s);
 #pragma unroll
               for (int g = 0; g < 2; ++g) {
-                const float4 f = info.f[2 * c + g];
-                if (ref.any_far) ref.settle(s + 16 * g, f.x);
-                const float a = ref.factor(f.x);
+                const int k = 2 * c + g;
+                if (ref.any_far) ref.settle(s + 16 * g, info.a[k].x);
+                const float a = ref.far ? 1.0f : info.a[k].x, lg = info.lg[k].x;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)  // masked after the factor: -inf * 0 is NaN
                   s[16 * g + i] = 32 * c + 16 * g + i >= seen ? 0xff800000u
-                                                              : __float_as_uint(fmaf(__uint_as_float(s[16 * g + i]), a, off + f.y));
-                sum = f2_fma(to_weights<BF16>(s + 16 * g, 1.0f, 0.0f, w + 8 * g), f2_pack(f.z, f.z), sum);
+                                                              : __float_as_uint(fmaf(__uint_as_float(s[16 * g + i]), a, off + lg));
+                sum = f2_fma(to_weights<BF16>(s + 16 * g, f2_pack(1.0f, 1.0f), f2_pack(0.0f, 0.0f), w + 8 * g),
+                             f2_pack(info.inv[k].x, info.inv[k].x), sum);
               }
               t5::st16(tP + 16 * c, w);
             }
