@@ -27,7 +27,7 @@
 //
 // Warps 0-3 and 4-7: softmax of the units; 8: the range's blocks and their
 // queries; 9: tensor core issue; 10: tiles (page ids, scales, copies of their codes);
-// 12-19: codes and open rows to operands.
+// 11: the gate, which follows the operands (gate_role); 12-19: codes and open rows to operands.
 #pragma once
 
 #include "attn_common.cuh"
@@ -45,9 +45,9 @@ constexpr int kNever = 0x7fffffff;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kFar = 0x1p20f;
 
-// Places on the line: 2 a tile of two units' rows, 1 where the units take every other
-// tile, and kExtra a block for its queries, ends and merge.
-constexpr int kExtra = 6;
+// Places on the line, about 700 clocks each: of a tile of two units' rows, of one that a
+// unit takes alone, and of a block for its queries, ends and merge.
+constexpr int kBoth = 6, kAlone = 5, kExtra = 18;
 
 template <int D>
 struct Cfg {
@@ -108,9 +108,10 @@ struct Blocks {
     rest = r.m % bt;
   }
   __device__ __forceinline__ long long count() const { return whole + (rest > 0); }
-  __device__ __forceinline__ int last_weight() const { return rest <= ut ? 1 : 2; }
+  __device__ __forceinline__ int last_weight() const { return rest <= ut ? kAlone : kBoth; }
   __device__ __forceinline__ long long before(long long i) const {
-    return i * kExtra + ((i * old + bt * (i * (i + 1) / 2)) >> 6);
+    const long long ends = i * old + bt * (i * (i + 1) / 2);
+    return i * kExtra + (ends >> 7) * kBoth + (((ends & 127) * kBoth) >> 7);
   }
   __device__ __forceinline__ long long all() const {
     return before(whole) + (rest > 0 ? kExtra + (long long)last_weight() * ((n + kRows - 1) / kRows) : 0);
@@ -636,6 +637,12 @@ __device__ __forceinline__ T uniform(T x) {
   return (T)__shfl_sync(kFull, x, 0);
 }
 
+// Operand descriptors differ in the lower word only (address, and in bits 16 up the
+// stride); the upper one says 1024 bytes between groups of eight rows and the 128-byte swizzle.
+__device__ __forceinline__ uint64_t operand(uint32_t lower) {
+  return (uint64_t)lower | ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32);
+}
+
 // The issue of the products is as long as the products themselves where it takes
 // more than 64 clocks each, so the two orders are written out, a unit being a constant
 // in each step.
@@ -645,33 +652,38 @@ __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned c
   constexpr uint32_t kQK = t5::instr_desc(128, 128, BF16, false), kPV = t5::instr_desc(128, D, BF16, true);
   const uint32_t tmem = uniform(sh->tmem);
   uint32_t* status = p.c.status;
-  const unsigned char* ring = smem + 2 * C::kTile;
-  const uint64_t dq = t5::smem_desc(smem_u32(smem), 16), dk = t5::smem_desc(smem_u32(ring), 16);
-  const uint64_t dv = t5::smem_desc(smem_u32(ring), kRows * 128);
+  const uint32_t base = smem_u32(smem) >> 4;
   uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
   uint32_t st = 0, st_phase = 0;  // the next operand's stage
   bool ok = true;
-  auto next = [&]() {  // waits for the next operand; its stage
+  auto next = [&]() {  // the next operand's stage
     const uint32_t at = st;
-    ok = ok && wait(&sh->kv_full[at], st_phase, status);
     if (++st == C::kStages) st = 0, st_phase ^= 1;
     return at;
   };
+  auto next_ready = [&]() {  // ... once it is there
+    ok = ok && wait(&sh->kv_full[st], st_phase, status);
+    return next();
+  };
   // S of unit u from the keys in stage at
   auto scores = [&](const int u, uint32_t at) {
-    const uint64_t q = dq + (uint32_t)(u * C::kTile >> 4), k = dk + at * (uint32_t)(C::kTile >> 4);
+    uint32_t b = base;
+    asm volatile("" : "+r"(b));  // made here each time: sixteen operands kept over the loop spill
+    const uint32_t q = b + (1u << 16) + u * (C::kTile >> 4), k = b + (1u << 16) + (2 + at) * (C::kTile >> 4);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       const uint32_t off = ((kk / 4) * (kRows * 128) + (kk % 4) * 32) >> 4;
-      t5::mma_ss(tmem + u * 128, q + off, k + off, kQK, kk > 0);
+      t5::mma_ss(tmem + u * 128, operand(q + off), operand(k + off), kQK, kk > 0);
     }
     t5::commit(&sh->s_full[u]);
   };
   auto values = [&](const int u, uint32_t at, bool first) {
-    const uint64_t v = dv + at * (uint32_t)(C::kTile >> 4);
+    uint32_t b = base;
+    asm volatile("" : "+r"(b));
+    const uint32_t v = b + ((kRows * 128 >> 4) << 16) + (2 + at) * (C::kTile >> 4);
 #pragma unroll
     for (int kk = 0; kk < kRows / 16; ++kk)
-      t5::mma_ts(tmem + 256 + u * D, tmem + u * 128 + 64 + kk * 8, v + kk * (2048 >> 4), kPV, kk > 0 || !first);
+      t5::mma_ts(tmem + 256 + u * D, tmem + u * 128 + 64 + kk * 8, operand(v + kk * (2048 >> 4)), kPV, kk > 0 || !first);
   };
   auto query = [&](const int u) {
     ok = ok && wait(&sh->q_full[u], q_phase[u], status);
@@ -689,7 +701,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned c
     const bool both = uniform(part->both);
     give_part(sh, it);
     if (both) {
-      uint32_t k = next();
+      uint32_t k = next_ready();
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         query(u);
@@ -705,21 +717,20 @@ __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned c
       for (int j = 0; j < n && ok; ++j) {
         const bool more = j + 1 < n;
         const uint32_t v = next();
+        k = more ? next() : 0;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          weights(u);
+          weights(u);  // says that these operands are there, too (gate_role)
           if (ok && t5::elect_one()) {
             values(u, v, j == 0);
             if (u) t5::commit(&sh->kv_empty[v]);
-            if (!more) t5::commit(&sh->o_done[u]);
-          }
-          __syncwarp();
-          if (!more) continue;
-          if (u == 0) k = next();
-          if (ok && t5::elect_one()) {
-            scores(u, k);
-            if (u) t5::commit(&sh->kv_empty[k]);
-            if (j + 2 == n) t5::commit(&sh->q_empty[u]);
+            if (more) {
+              scores(u, k);
+              if (u) t5::commit(&sh->kv_empty[k]);
+              if (j + 2 == n) t5::commit(&sh->q_empty[u]);
+            } else {
+              t5::commit(&sh->o_done[u]);
+            }
           }
           __syncwarp();
         }
@@ -729,7 +740,7 @@ __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned c
       for (int u = 0; u < 2; ++u) {
         if (u >= n) continue;
         query(u);
-        const uint32_t k = next();
+        const uint32_t k = next_ready();
         t5::fence_after();
         if (ok && t5::elect_one()) {
           scores(u, k);
@@ -745,20 +756,18 @@ __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned c
           const int j = j0 + u;
           if (j >= n) continue;
           const bool more = j + 2 < n;
-          const uint32_t v = next();
+          const uint32_t v = next(), k = more ? next() : 0;
           weights(u);
           if (ok && t5::elect_one()) {
             values(u, v, j0 == 0);
             t5::commit(&sh->kv_empty[v]);
-            if (!more) t5::commit(&sh->o_done[u]);
-          }
-          __syncwarp();
-          if (!more) continue;
-          const uint32_t k = next();
-          if (ok && t5::elect_one()) {
-            scores(u, k);
-            t5::commit(&sh->kv_empty[k]);
-            if (j + 4 >= n) t5::commit(&sh->q_empty[u]);
+            if (more) {
+              scores(u, k);
+              t5::commit(&sh->kv_empty[k]);
+              if (j + 4 >= n) t5::commit(&sh->q_empty[u]);
+            } else {
+              t5::commit(&sh->o_done[u]);
+            }
           }
           __syncwarp();
         }
@@ -769,6 +778,47 @@ __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned c
   if (t5::elect_one()) t5::commit(&sh->drain);
   __syncwarp();
   wait(&sh->drain, 0, status);
+}
+
+// Follows the operands and lets each step's products go on: its values and the
+// unit's next keys are there. (Waited for by the issuing warp they cost the products' queue.)
+template <int D>
+__device__ __forceinline__ void gate_role(const Params& p, Shared* sh) {
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31;
+  uint32_t* status = p.c.status;
+  uint32_t st = 0, st_phase = 0, p_phase = 0, opened = 0;  // by unit: parity of its last arrival, whether there was one
+  auto next = [&]() {
+    if (!wait(&sh->kv_full[st], st_phase, status)) return false;
+    if (lane == 0) arrive(&sh->kv_empty[st]);  // seen: the ring cannot run two phases ahead
+    __syncwarp();
+    if (++st == C::kStages) st = 0, st_phase ^= 1;
+    return true;
+  };
+  auto open = [&](int u) {  // one arrival a phase: the one before is complete
+    if ((opened >> u) & 1)
+      if (!wait(&sh->p_full[u], ((p_phase >> u) & 1) ^ 1, status)) return false;
+    opened |= 1u << u;
+    p_phase ^= 1u << u;
+    if (lane == 0) arrive(&sh->p_full[u]);
+    __syncwarp();
+    return true;
+  };
+  for (int it = 0;; ++it) {
+    const Part* part = take_part(sh, it, status);
+    if (!part) return;
+    const int n = part->t1 - part->t0;
+    const bool both = part->both;
+    give_part(sh, it);
+    if (!next()) return;
+    if (!both && n > 1 && !next()) return;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      if (!next()) return;
+      if (j + (both ? 1 : 2) < n && !next()) return;
+      if (both ? !(open(0) && open(1)) : !open(j & 1)) return;
+    }
+  }
 }
 
 // --------------------------------------------------------------------------
@@ -1189,14 +1239,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.p_full[i], 5);  // the unit's warps, and the gate
       mbar_init(&sh.o_done[i], 1);
       mbar_init(&sh.fix_ready[i], 8);
       mbar_init(&sh.fix_free[i], 8);
     }
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&sh.part_full[i], 1);
-      mbar_init(&sh.part_empty[i], 18);  // every warp but the one that fills it and the idle one
+      mbar_init(&sh.part_empty[i], 19);  // every warp but the one that fills it
     }
     mbar_init(&sh.drain, 1);
     mbar_init(&sh.join_ready, 8);
@@ -1204,7 +1254,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     mbar_init(&sh.conv, 8);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sh.kv_full[i], 8);
-      mbar_init(&sh.kv_empty[i], 1);
+      mbar_init(&sh.kv_empty[i], 2);  // the products have read it, the gate has seen it
     }
     for (int i = 0; i < C::kRaws; ++i) {
       mbar_init(&sh.raw_full[i], 1);
@@ -1237,6 +1287,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     if (warp == 8) part_role<D>(p, &sh, smem);
     else if (warp == 9) mma_role<D, BF16>(p, &sh, smem);
     else if (warp == 10) tile_role<D, CODE, BF16>(p, &sh, smem + (2 + C::kStages) * C::kTile);
+    else gate_role<D>(p, &sh);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     unsigned char* ring = smem + 2 * C::kTile;
