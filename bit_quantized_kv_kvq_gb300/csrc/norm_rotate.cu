@@ -34,49 +34,26 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // `passes`: passes over 256 / D heads each that a warp makes of its token;
-// `parts`: warps of a token.
+// `parts`: warps of a token. The first rows' loads go out before anything else is
+// known, so that a small call takes one memory latency and not four.
 template <int D, bool BF16, bool INTERLEAVED>
-__global__ void __launch_bounds__(kWarps * 32) norm_rotate_kernel(const RotateArgs a, const int passes, const int parts) {
+__global__ void __launch_bounds__(kWarps * 32, 7) norm_rotate_kernel(const RotateArgs a, const int passes, const int parts) {
   constexpr int kLanes = D / 8, kHeads = 32 / kLanes;  // lanes of a head, heads of a pass
+  constexpr int kBatch = 4;                            // passes whose loads are in flight together
   const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
   const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int token = (int)(task / parts), part = (int)(task % parts);
   if (token >= a.tokens) return;
-  const int position = a.positions[token];
-  if (position < 0) return;
   const int heads = a.q_heads + a.k_heads;
 
   // the lane's channels: ch0 .. + 3 and ch1 .. + 3
-  const int rotated = a.rot / 8;  // lanes that hold pairs
-  const bool turn = l < rotated;
-  int ch0, ch1;
-  if (INTERLEAVED) {
-    ch0 = 8 * l, ch1 = 8 * l + 4;
-  } else if (turn) {
-    ch0 = 4 * l, ch1 = a.rot / 2 + 4 * l;
-  } else {
-    ch0 = 8 * l, ch1 = 8 * l + 4;
-  }
-  float c[4], s[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    c[j] = 1.0f, s[j] = 0.0f;
-    if (turn) {
-      const uint64_t t = (uint64_t)(uint32_t)position * a.turns[4 * l + j] + (1ull << 31);
-      sincospif((float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f, &s[j], &c[j]);
-      c[j] *= a.magnitude, s[j] *= a.magnitude;
-    }
-  }
-  float wq[8], wk[8];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    wq[j] = a.q_weight ? a.q_weight[ch0 + j] : 1.0f, wq[4 + j] = a.q_weight ? a.q_weight[ch1 + j] : 1.0f;
-    wk[j] = a.k_weight ? a.k_weight[ch0 + j] : 1.0f, wk[4 + j] = a.k_weight ? a.k_weight[ch1 + j] : 1.0f;
-  }
-  constexpr int kBatch = 4;  // passes whose loads are in flight together
-  const int last = min(heads, (part + 1) * passes * kHeads);
-  for (int h0 = part * passes * kHeads; h0 < last; h0 += kBatch * kHeads) {
-    uint2 x[kBatch][2];
+  const bool turn = l < a.rot / 8;
+  const bool apart = !INTERLEAVED && turn;
+  const int ch0 = apart ? 4 * l : 8 * l, ch1 = apart ? a.rot / 2 + 4 * l : 8 * l + 4;
+
+  const int first = part * passes * kHeads, last = min(heads, first + passes * kHeads);
+  uint2 x[kBatch][2];
+  auto load = [&](int h0) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int h = h0 + i * kHeads + sub;
@@ -86,6 +63,23 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rotate_kernel(const RotateAr
       x[i][0] = *reinterpret_cast<const uint2*>(row + ch0);
       x[i][1] = *reinterpret_cast<const uint2*>(row + ch1);
     }
+  };
+  load(first);
+  const int position = a.positions[token];
+  uint64_t turns[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) turns[j] = turn ? a.turns[4 * l + j] : 0;
+  if (position < 0) return;
+  float c[4], s[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t t = (uint64_t)(uint32_t)position * turns[j] + (1ull << 31);
+    sincospif((float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f, &s[j], &c[j]);
+    c[j] *= a.magnitude, s[j] *= a.magnitude;
+  }
+#pragma unroll 1
+  for (int h0 = first; h0 < last; h0 += kBatch * kHeads) {
+    if (h0 > first) load(h0);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int h = h0 + i * kHeads + sub;
@@ -102,10 +96,12 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rotate_kernel(const RotateAr
 #pragma unroll
       for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (h >= last) continue;
-      if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
+      const float* weight = is_q ? a.q_weight : a.k_weight;
+      if (weight) {
         const float r = rsqrtf(sum * (1.0f / D) + a.eps);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] * r * (is_q ? wq[j] : wk[j]);
+        const float4 w0 = *reinterpret_cast<const float4*>(weight + ch0), w1 = *reinterpret_cast<const float4*>(weight + ch1);
+        v[0] = v[0] * r * w0.x, v[1] = v[1] * r * w0.y, v[2] = v[2] * r * w0.z, v[3] = v[3] * r * w0.w;
+        v[4] = v[4] * r * w1.x, v[5] = v[5] * r * w1.y, v[6] = v[6] * r * w1.z, v[7] = v[7] * r * w1.w;
       }
       if (turn) {
 #pragma unroll
@@ -129,8 +125,8 @@ template <int D, bool BF16>
 cudaError_t launch(const RotateArgs& a, cudaStream_t st) {
   constexpr int kHeads = 256 / D;
   const int all = (a.q_heads + a.k_heads + kHeads - 1) / kHeads;
-  // few tokens: a warp a pass, for latency; many: the sines of a token serve all its heads
-  const int parts = a.tokens < 1024 ? (all + 3) / 4 : 1, passes = (all + parts - 1) / parts;
+  // few tokens: a warp for every pass, for latency; many: the sines of a token serve all its heads
+  const int parts = a.tokens < 256 ? all : a.tokens < 2048 ? (all + 3) / 4 : 1, passes = (all + parts - 1) / parts;
   const int64_t grid = ((int64_t)a.tokens * parts + kWarps - 1) / kWarps;
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   if (a.interleaved) norm_rotate_kernel<D, BF16, true><<<(unsigned)grid, kWarps * 32, 0, st>>>(a, passes, parts);

@@ -7,6 +7,8 @@
 // request's tail, so a fork copies those rows and takes a page of its own.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "paged_internal.h"
 
 namespace kvq {
@@ -179,7 +181,11 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
 // --------------------------------------------------------------------------
 // Release
 // --------------------------------------------------------------------------
-constexpr int kCluster = 8;
+constexpr int kCluster = 16;  // CTAs of the large form
+constexpr int kRun = 8;       // and consecutive entries of its threads
+// Table entries (of all rows) that one CTA releases alone. us for release of 8 requests
+// of 900 tokens, 464 entries: alone 5, a cluster of eight 10.6 (its barriers).
+constexpr int64_t kAlone = 8192;
 
 // The last index b in [0, n) with key[b] <= x (keys ascending, key[0] <= x).
 __device__ __forceinline__ int last_le(const int* key, int n, int x) {
@@ -192,18 +198,23 @@ __device__ __forceinline__ int last_le(const int* key, int n, int x) {
   return lo;
 }
 
-// One cluster. The released entries, numbered in order of request and
-// position, are cut into a run for each CTA; three passes over them with a barrier
-// between: every entry takes one off its page's count; of the entries whose
-// page's count went below zero, the last one leaves its number there (smaller
-// numbers than any count); and that entry puts the page on the stack, at the
-// place that a prefix sum over such entries gives.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) release_shared_kernel(const ReleaseSharedArgs args) {
+// The released entries, numbered in order of request and position, are cut into a
+// run for each CTA of a cluster; three passes over them with a barrier between: every
+// entry takes one off its page's count; of the entries whose page's count went below
+// zero, the last one leaves its number there (smaller numbers than any count); and
+// that entry puts the page on the stack, at the place that a prefix sum over such
+// entries gives. A thread takes RUN entries side by side, so that their loads
+// and counts are on their way together, and keeps the pages of its first ones.
+template <int CTAS, int RUN>
+__global__ void __launch_bounds__(kThreads) release_shared_kernel(const ReleaseSharedArgs args) {
   const ReleaseArgs& a = args.r;
-  cg::cluster_group cluster = cg::this_cluster();
   __shared__ int first[kMaxRequests + 1];
   __shared__ int pushes, base_s;
   const int R = a.requests, P = 1 << a.page_shift, rank = blockIdx.x;
+  auto sync = [&]() {
+    if (CTAS > 1) cg::this_cluster().sync();
+    else __syncthreads();
+  };
   const int count = *a.free_count;
   int g[kPer];
   bool bad = count < 0 || count > a.num_pages;
@@ -233,42 +244,82 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) rel
     if (b == R - 1) first[R] = (int)at;
   }
   __syncthreads();
-  const int run = ((int)total + kCluster - 1) / kCluster, k0 = min(rank * run, (int)total), k1 = min(k0 + run, (int)total);
-  auto page_of = [&](int k) {
-    const int b = last_le(first, R + 1, k);
-    return a.table[(int64_t)b * a.max_pages + (k - first[b])];
+  // runs of whole groups of RUN entries
+  const int groups = ((int)total + RUN - 1) / RUN, per = (groups + CTAS - 1) / CTAS;
+  const int g0 = min(rank * per, groups), g1 = min(g0 + per, groups);
+  // the pages of group q, -1 where there is none or no such page
+  auto look_up = [&](int q, int (&page)[RUN], bool raise) {
+    int b = q < g1 ? last_le(first, R + 1, q * RUN) : R;
+#pragma unroll
+    for (int k = 0; k < RUN; ++k) {
+      page[k] = -1;
+      const int e = q * RUN + k;
+      if (q >= g1 || e >= (int)total) continue;
+      while (first[b + 1] <= e) ++b;
+      page[k] = a.table[(int64_t)b * a.max_pages + (e - first[b])];
+    }
+#pragma unroll
+    for (int k = 0; k < RUN; ++k) {
+      if (q >= g1 || q * RUN + k >= (int)total) continue;
+      if (page[k] < 0 || page[k] >= a.num_pages) {
+        page[k] = -1;
+        if (raise) raise_status(a.status, kStatusBadIndex);
+      }
+    }
   };
-  auto in_cache = [&](int page) { return page >= 0 && page < a.num_pages; };
+  int kept[RUN];  // of the thread's first group
+  look_up(g0 + threadIdx.x, kept, true);
+  auto pages_of = [&](int q, int (&page)[RUN], bool raise) {
+    if (q != g0 + (int)threadIdx.x) return look_up(q, page, raise);
+#pragma unroll
+    for (int k = 0; k < RUN; ++k) page[k] = kept[k];
+  };
   auto number = [](int k) { return INT32_MIN + ((1 << 30) - k); };  // later entries: lower, all below any count
-  for (int k = k0 + threadIdx.x; k < k1; k += kThreads) {
-    const int page = page_of(k);
-    if (in_cache(page)) atomicAdd(args.shared + page, -1);
-    else raise_status(a.status, kStatusBadIndex);
+  for (int q = g0 + threadIdx.x; q < g1; q += kThreads) {
+    int page[RUN];
+    pages_of(q, page, true);
+#pragma unroll
+    for (int k = 0; k < RUN; ++k)
+      if (page[k] >= 0) atomicAdd(args.shared + page[k], -1);
   }
-  cluster.sync();
-  for (int k = k0 + threadIdx.x; k < k1; k += kThreads) {
-    const int page = page_of(k);
-    if (!in_cache(page) || __ldcg(args.shared + page) >= 0) continue;
-    const int was = atomicMin(args.shared + page, number(k));
-    if (was < -1 && was > INT32_MIN + (1 << 30)) raise_status(a.status, kStatusBadIndex);  // released more often than held
+  sync();
+  for (int q = g0 + threadIdx.x; q < g1; q += kThreads) {
+    int page[RUN], held[RUN];
+    pages_of(q, page, false);
+#pragma unroll
+    for (int k = 0; k < RUN; ++k) held[k] = page[k] >= 0 ? __ldcg(args.shared + page[k]) : 0;
+#pragma unroll
+    for (int k = 0; k < RUN; ++k) {
+      if (held[k] >= 0) continue;
+      // released more often than held (who comes first sees it: others may see a number)
+      if (held[k] < -1 && held[k] > INT32_MIN + (1 << 30)) raise_status(a.status, kStatusBadIndex);
+      atomicMin(args.shared + page[k], number(q * RUN + k));
+    }
   }
-  cluster.sync();
-  auto last_of_page = [&](int k) {
-    if (k >= k1) return -1;
-    const int page = page_of(k);
-    return in_cache(page) && __ldcg(args.shared + page) == number(k) ? page : -1;
+  sync();
+  // which of group q's entries are their page's last: bits, and the pages
+  auto last_of = [&](int q, int (&page)[RUN]) {
+    pages_of(q, page, false);
+    uint32_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < RUN; ++k)
+      if (page[k] >= 0 && __ldcg(args.shared + page[k]) == number(q * RUN + k)) bits |= 1u << k;
+    return bits;
   };
   if (threadIdx.x == 0) pushes = 0;
   __syncthreads();
   int here = 0;
-  for (int k = k0 + threadIdx.x; k < k1; k += kThreads) here += last_of_page(k) >= 0;
+  for (int q = g0 + threadIdx.x; q < g1; q += kThreads) {
+    int page[RUN];
+    here += __popc(last_of(q, page));
+  }
   here = __reduce_add_sync(0xffffffffu, here);
   if ((threadIdx.x & 31) == 0) atomicAdd(&pushes, here);
-  cluster.sync();
+  sync();
   if (threadIdx.x == 0) {
     int before = 0, all = 0;
-    for (int r = 0; r < kCluster; ++r) {
-      const int p = *cluster.map_shared_rank(&pushes, r);
+    for (int r = 0; r < CTAS; ++r) {
+      const int p = CTAS > 1 ? *cg::this_cluster().map_shared_rank(&pushes, r) : pushes;
       before += r < rank ? p : 0;
       all += p;
     }
@@ -278,15 +329,19 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) rel
       *a.free_count = min(count + all, a.num_pages);
     }
   }
-  cluster.sync();
+  sync();
   long long base = (long long)count + base_s;
-  for (int c0 = k0; c0 < k1; c0 += kThreads) {
-    const int page = last_of_page(c0 + threadIdx.x);
+  for (int q0 = g0; q0 < g1; q0 += kThreads) {
+    int page[RUN];
+    const uint32_t bits = last_of(q0 + threadIdx.x, page);
     long long pushed;
-    const long long place = base + block_scan(page >= 0, &pushed);
-    if (page >= 0) {
-      if (place < a.num_pages) a.free_pages[place] = page;
-      args.shared[page] = 0;
+    long long place = base + block_scan(__popc(bits), &pushed);
+#pragma unroll
+    for (int k = 0; k < RUN; ++k) {
+      if (!((bits >> k) & 1)) continue;
+      if (place < a.num_pages) a.free_pages[place] = page[k];
+      args.shared[page[k]] = 0;
+      ++place;
     }
     base += pushed;
   }
@@ -327,8 +382,32 @@ cudaError_t launch_fork(const ForkArgs& a, int sm_count, cudaStream_t st) {
 }
 
 cudaError_t launch_release_shared(const ReleaseSharedArgs& a, cudaStream_t st) {
-  release_shared_kernel<<<kCluster, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  if ((int64_t)a.r.requests * a.r.max_pages <= kAlone) {
+    release_shared_kernel<1, 1><<<1, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  // 16 CTAs a cluster are more than every device must take: asked for once a device
+  static std::atomic<unsigned long long> asked{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+  if (!(bit && (asked.load(std::memory_order_acquire) & bit))) {
+    e = cudaFuncSetAttribute(release_shared_kernel<kCluster, kRun>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    asked.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = kCluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, release_shared_kernel<kCluster, kRun>, a);
 }
 
 }  // namespace kvq
