@@ -126,13 +126,18 @@ struct Pos {
   int b, lot, i, t;
 };
 
+// n / d, in 32 bits where both fit (a 64-bit division takes half a microsecond).
+__device__ __forceinline__ long long quotient(unsigned long long n, unsigned long long d) {
+  return (n | d) >> 32 ? (long long)(n / d) : (long long)((uint32_t)n / (uint32_t)d);
+}
+
 // The place v of a request's line.
 __device__ __forceinline__ Pos locate(const Params& p, int b, const Req& r, long long v) {
   const Blocks k(p, r);
   const long long all = k.all();
   Pos x;
   x.b = b;
-  x.lot = (int)(v / all);
+  x.lot = (int)quotient(v, all);
   const long long w = v - x.lot * all;
   long long i = k.whole, lo = k.before(k.whole), hi = all;
   if (w < lo) {
@@ -146,7 +151,7 @@ __device__ __forceinline__ Pos locate(const Params& p, int b, const Req& r, long
     hi = k.before(i + 1);
   }
   const int tiles = k.tiles(i);
-  long long t = (w - lo) * tiles / (hi - lo);
+  long long t = quotient((w - lo) * tiles, hi - lo);
   // no slivers: a cut near an end is none
   const int least = tiles >= 16 ? 2 : 1;
   if (t < least) t = 0;
@@ -1023,10 +1028,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
               }
             }
           } else {
-            // a tile that ends past some row's own key
+            // a tile that ends past some row's own key; keys from `none` on no row attends
+            const int none = __reduce_max_sync(kFull, limit != kNever ? seen : 0);
             float top = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 4 && 32 * c < none; ++c) {
               uint32_t s[32];
               t5::ld32(tS + 32 * c, s);
               t5::wait_ld32(s);
@@ -1041,6 +1047,12 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
 #pragma unroll 1
             for (int c = 3; c >= 0; --c) {
               uint32_t s[32], w[16];
+              if (32 * c >= none) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = 0u;
+                t5::st16(tP + 16 * c, w);
+                continue;
+              }
               t5::ld32(tS + 32 * c, s);
               t5::wait_ld32(s);
 #pragma unroll
@@ -1205,8 +1217,9 @@ __device__ __forceinline__ void find_range(const Params& p, Shared* sh) {
   }
   const int ctas = places < p.ctas ? (int)places : p.ctas;
   if ((int)blockIdx.x >= ctas) return;
-  const long long v[2] = {places / ctas * blockIdx.x + places % ctas * blockIdx.x / ctas,
-                          places / ctas * (blockIdx.x + 1) + places % ctas * (blockIdx.x + 1) / ctas};
+  const long long share = quotient(places, ctas), rest = places - share * ctas;  // rest < ctas
+  const long long v[2] = {share * blockIdx.x + (uint32_t)rest * blockIdx.x / (uint32_t)ctas,
+                          share * (blockIdx.x + 1) + (uint32_t)rest * (blockIdx.x + 1) / (uint32_t)ctas};
   for (int e = 0; e < 2; ++e) {
     if (v[e] < at || v[e] >= at + sum) continue;
     long long a = at;
@@ -1302,24 +1315,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 
 // Merges the partial sums of the blocks that a range's end cuts, in the order of
 // the CTAs. CTA x: the block that range x + 1 starts inside, if no earlier range
-// does; y: which 32 of its rows.
-constexpr int kMergeThreads = 256;
+// does; y: which of its units' rows. A warp takes four rows side by side.
+constexpr int kMergeThreads = 1024;
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const __grid_constant__ Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kPer = D / 32;
-  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int4 at = p.pos[c], prev = p.pos[c - 1];
+  constexpr int kPer = D / 32, kSide = kRows / 32;
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, unit = blockIdx.y;
+  // where ranges c - 1 + lane start: these first, all at once
+  const int4 none = make_int4(p.a.requests, 0, 0, 0);
+  int4 mine = c - 1 + lane <= p.ctas ? p.pos[c - 1 + lane] : none;
+  auto pos_of = [&](int k) {
+    return make_int4(__shfl_sync(kFull, mine.x, k), __shfl_sync(kFull, mine.y, k), __shfl_sync(kFull, mine.z, k),
+                     __shfl_sync(kFull, mine.w, k));
+  };
+  const int4 prev = pos_of(0), at = pos_of(1);
   if (at.w == 0) return;
   auto same = [&](const int4& x) { return x.x == at.x && x.y == at.y && x.z == at.z; };
   if (same(prev) && prev.w > 0) return;
-  int last = c;  // the last CTA with a part of the block
-  while (last + 1 <= p.ctas) {
-    const int4 q = p.pos[last + 1];
-    if (!same(q) || q.w == 0) break;
-    ++last;
-  }
   bool bad = false;
   const Req r = load_req(p, at.x, bad);
   const Blocks k(p, r);
@@ -1327,42 +1341,72 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const _
   const int heads = min(p.unit_heads, p.a.group - chunk * kRows);
   const long long first = (long long)at.z * k.bt;
   const int tokens = (int)min((long long)k.bt, r.m - first);
-#pragma unroll 1
-  for (int i = warp; i < 32; i += kMergeThreads / 32) {
-    const int row = blockIdx.y * 32 + i, unit = row / kRows, in = row % kRows, tok = in / p.unit_heads;
-    const int head = in - tok * p.unit_heads, token = unit * p.unit_tokens + tok;
-    if (tok >= p.unit_tokens || head >= heads || token >= tokens) continue;
-    float top = -INFINITY, l = 0.0f, o[kPer];
+  int token[kSide], head[kSide];
+  bool live[kSide], any = false;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) o[e] = 0.0f;
-    int4 from = prev;
-    for (int x = c - 1; x <= last; ++x) {
-      const int4 to = p.pos[x + 1];
-      const bool empty = x >= c && same(to) && to.w == from.w;
-      from = to;
-      if (empty) continue;
-      const int64_t pr = ((int64_t)(x * 2 + (x >= c ? 0 : 1)) * 2 + unit) * kRows + in;
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + pr * 2);
-      float v[kPer];
-      const float* src = p.part_o + pr * D + lane * kPer;
-      if (D == 128) {
-        const float4 w = *reinterpret_cast<const float4*>(src);
-        v[0] = w.x, v[1] = w.y, v[2 % kPer] = w.z, v[3 % kPer] = w.w;
-      } else {
-        const float2 w = *reinterpret_cast<const float2*>(src);
-        v[0] = w.x, v[1] = w.y;
-      }
-      const float now = fmaxf(top, ml.x), base = now == -INFINITY ? 0.0f : now;
-      const float fo = exp2_fast(top - base), fn = exp2_fast(ml.x - base);
+  for (int i = 0; i < kSide; ++i) {
+    const int in = warp + 32 * i, tok = in / p.unit_heads;
+    head[i] = in - tok * p.unit_heads;
+    token[i] = unit * p.unit_tokens + tok;
+    live[i] = tok < p.unit_tokens && head[i] < heads && token[i] < tokens;
+    any |= live[i];
+  }
+  if (!any) return;
+  float top[kSide], l[kSide], o[kSide][kPer];
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] = o[e] * fo + v[e] * fn;
-      l = l * fo + ml.y * fn;
-      top = now;
+  for (int i = 0; i < kSide; ++i) {
+    top[i] = -INFINITY;
+    l[i] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[i][e] = 0.0f;
+  }
+  int4 from = prev;
+  int base = c - 1;  // the CTA of mine in lane 0
+  for (int x = c - 1; x < p.ctas; ++x) {
+    if (x + 1 - base == 32) {
+      base += 31;
+      mine = base + lane <= p.ctas ? p.pos[base + lane] : none;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t* out = p.a.out + ((int64_t)(r.c0 + first + token) * p.a.q_heads + hq0 + head) * D + lane * kPer;
+    const int4 to = pos_of(x + 1 - base);
+    const bool inside = same(to) && to.w > 0;  // the block goes on in the next range
+    const bool empty = x >= c && inside && to.w == from.w;
+    from = to;
+    if (!empty) {
+      float2 ml[kSide];
+      float v[kSide][kPer];
 #pragma unroll
-    for (int e = 0; e < kPer; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack2<BF16>(o[e] * inv, o[e + 1] * inv);
+      for (int i = 0; i < kSide; ++i) {
+        const int64_t pr = ((int64_t)(x * 2 + (x >= c ? 0 : 1)) * 2 + unit) * kRows + warp + 32 * i;
+        const float* src = p.part_o + pr * D + lane * kPer;
+        ml[i] = live[i] ? *reinterpret_cast<const float2*>(p.part_ml + pr * 2) : make_float2(-INFINITY, 0.0f);
+        if (D == 128) {
+          const float4 w = live[i] ? *reinterpret_cast<const float4*>(src) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          v[i][0] = w.x, v[i][1] = w.y, v[i][2 % kPer] = w.z, v[i][3 % kPer] = w.w;
+        } else {
+          const float2 w = live[i] ? *reinterpret_cast<const float2*>(src) : make_float2(0.0f, 0.0f);
+          v[i][0] = w.x, v[i][1] = w.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kSide; ++i) {
+        const float now = fmaxf(top[i], ml[i].x), ref = now == -INFINITY ? 0.0f : now;
+        const float fo = exp2_fast(top[i] - ref), fn = exp2_fast(ml[i].x - ref);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) o[i][e] = o[i][e] * fo + v[i][e] * fn;
+        l[i] = l[i] * fo + ml[i].y * fn;
+        top[i] = now;
+      }
+    }
+    if (!inside) break;
+  }
+#pragma unroll
+  for (int i = 0; i < kSide; ++i) {
+    if (!live[i]) continue;
+    const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
+    uint16_t* out = p.a.out + ((int64_t)(r.c0 + first + token[i]) * p.a.q_heads + hq0 + head[i]) * D + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2)
+      *reinterpret_cast<uint32_t*>(out + e) = pack2<BF16>(o[i][e] * inv, o[i][e + 1] * inv);
   }
 }
 
@@ -1389,7 +1433,7 @@ cudaError_t launch(const PagedDev& c, const PagedAttnArgs& a, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess || p.ctas < 2) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ctas - 1, 8);
+  cfg.gridDim = dim3(p.ctas - 1, 2);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute at;
