@@ -479,35 +479,28 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t up, uint32_t& lo, ui
   if (VALUES) lo = mul2<BF16>(lo, up), hi = mul2<BF16>(hi, up);
 }
 
-// A thread's 16 channels of a row. Eight threads in a row read 128 bytes of codes side
-// by side and write to the operand tile, whose 16-byte chunks are swizzled; with 128
-// channels the two halves of a row fall into the same banks, so the threads of the second
-// half store their two chunks in the other order.
+// A thread's eight channels of a row: eight threads side by side read 64 bytes of
+// codes and write the eight 16-byte chunks of a 128-byte row of the operand tile,
+// which the swizzle puts into different banks.
 template <int D>
 struct Place {
-  int row, half, seg;
-  uint32_t first, second;  // bytes of its chunks in the tile, in the order in which they are stored
+  int row, channel;
+  uint32_t at;  // bytes of its chunk in the tile
   __device__ __forceinline__ Place(int tid) {
-    seg = tid & 3;
-    half = D == 128 ? (tid >> 2) & 1 : 0;
-    row = tid / (D / 16);
-    first = half * (kRows * 128) + row * 128 + (((2 * seg + half) ^ (row & 7)) << 4);
-    second = first ^ 16;
+    const int chunk = tid % (D / 8);
+    row = tid / (D / 8);
+    channel = chunk * 8;
+    at = (chunk >> 3) * (kRows * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
   }
-  __device__ __forceinline__ int channel() const { return half * 64 + seg * 16; }
 };
 
 // Codes of the thread's channels in the row `down` further down (a multiple of 8).
 template <int D, int CODE, bool BF16, bool VALUES>
-__device__ __forceinline__ void put_codes(unsigned char* tile, const Place<D>& at, int down, const uint4& x, uint32_t up) {
-  uint4 a, b;
-  const bool swap = D == 128 && at.half;
-  widen4<CODE, BF16, VALUES>(swap ? x.z : x.x, up, a.x, a.y);
-  widen4<CODE, BF16, VALUES>(swap ? x.w : x.y, up, a.z, a.w);
-  widen4<CODE, BF16, VALUES>(swap ? x.x : x.z, up, b.x, b.y);
-  widen4<CODE, BF16, VALUES>(swap ? x.y : x.w, up, b.z, b.w);
-  *reinterpret_cast<uint4*>(tile + at.first + down * 128) = a;
-  *reinterpret_cast<uint4*>(tile + at.second + down * 128) = b;
+__device__ __forceinline__ void put_codes(unsigned char* tile, const Place<D>& at, int down, const uint2& x, uint32_t up) {
+  uint4 a;
+  widen4<CODE, BF16, VALUES>(x.x, up, a.x, a.y);
+  widen4<CODE, BF16, VALUES>(x.y, up, a.z, a.w);
+  *reinterpret_cast<uint4*>(tile + at.at + down * 128) = a;
 }
 
 // Infinities and NaN of 8 values of an open row: 0 in their place, and where
@@ -533,14 +526,16 @@ __device__ __forceinline__ void finite8(uint4& x, int pos, int ch, int (*first)[
 
 // The codes of pass after pass of an operand that is all pages.
 template <int D, int CODE, bool BF16, bool VALUES>
-__device__ __forceinline__ void convert_codes(unsigned char* to, const Place<D>& at, const uint4* from, const Info& info) {
-  constexpr int kPasses = D / 32, kStep = 4096 / D;
-  uint4 x[kPasses];
+__device__ __forceinline__ void convert_codes(unsigned char* to, const Place<D>& at, const uint2* from, const Info& info) {
+  constexpr int kPasses = D / 16, kStep = 2048 / D;
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k) x[k] = from[k * 256];
+  for (int k0 = 0; k0 < kPasses; k0 += 4) {
+    uint2 x[4];
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    put_codes<D, CODE, BF16, VALUES>(to, at, k * kStep, x[k], VALUES ? info.up[(k * kStep + at.row) >> 4] : 0u);
+    for (int k = 0; k < 4; ++k) x[k] = from[(k0 + k) * 256];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      put_codes<D, CODE, BF16, VALUES>(to, at, (k0 + k) * kStep, x[k], VALUES ? info.up[((k0 + k) * kStep + at.row) >> 4] : 0u);
   }
 }
 
@@ -548,7 +543,7 @@ __device__ __forceinline__ void convert_codes(unsigned char* to, const Place<D>&
 template <int D, int CODE, bool BF16>
 __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsigned char* ring, const unsigned char* raw) {
   using C = Cfg<D>;
-  constexpr int kPasses = D / 32, kStep = 4096 / D;  // passes over a tile, rows of one
+  constexpr int kPasses = D / 16, kStep = 2048 / D;  // passes over a tile, rows of one
   const PagedDev& c = p.c;
   const int tid = threadIdx.x & 255, lane = threadIdx.x & 31, P = 1 << c.page_shift;
   const Place<D> at(tid);
@@ -576,7 +571,7 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
       const uint32_t i = order.base + o, slot = tile % kInfo, st = i % C::kStages, rs = i % C::kRaws;
       const Info& info = sh->info[slot];
       unsigned char* to = ring + st * C::kTile;
-      const uint4* from = reinterpret_cast<const uint4*>(raw + rs * C::kRaw) + tid;  // of pass k: 256 k further on
+      const uint2* from = reinterpret_cast<const uint2*>(raw + rs * C::kRaw) + tid;  // of pass k: 256 k further on
       if (which == 0 && !wait(&sh->info_full[slot], (tile / kInfo) & 1, c.status)) return;
       if (!wait(&sh->raw_full[rs], (i / C::kRaws) & 1, c.status)) return;
       if (!wait(&sh->kv_empty[st], ((i / C::kStages) & 1) ^ 1, c.status)) return;
@@ -584,36 +579,30 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
         if (which) convert_codes<D, CODE, BF16, true>(to, at, from, info);
         else convert_codes<D, CODE, BF16, false>(to, at, from, info);
       } else {
-        const int n = part->n, full = n & ~(P - 1), ch = at.channel(), t = part->t0 + j;
+        const int n = part->n, full = n & ~(P - 1), t = part->t0 + j;
         const uint16_t* tail =
-            c.tails + (((((int64_t)part->b * c.heads + part->h) * 2 + which) << c.page_shift)) * D + ch;
-        const bool swap = D == 128 && at.half;
-        uint4 a[kPasses], b[kPasses];
-        int page[kPasses];
+            c.tails + (((((int64_t)part->b * c.heads + part->h) * 2 + which) << c.page_shift)) * D + at.channel;
+#pragma unroll 1
+        for (int k0 = 0; k0 < kPasses; k0 += 4) {
+          uint4 a[4];
+          int page[4];
 #pragma unroll
-        for (int k = 0; k < kPasses; ++k) {
-          const int row = k * kStep + at.row, pos = t * kRows + row;
-          page[k] = info.page[which][row >> 4];
-          a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
-          if (page[k] == -1 && pos < n) {
-            const uint4* src = reinterpret_cast<const uint4*>(tail + (int64_t)(pos - full) * D);
-            a[k] = src[0];
-            b[k] = src[1];
+          for (int k = 0; k < 4; ++k) {
+            const int row = (k0 + k) * kStep + at.row, pos = t * kRows + row;
+            page[k] = info.page[which][row >> 4];
+            a[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (page[k] == -1 && pos < n) a[k] = *reinterpret_cast<const uint4*>(tail + (int64_t)(pos - full) * D);
           }
-        }
 #pragma unroll
-        for (int k = 0; k < kPasses; ++k) {
-          const int row = k * kStep + at.row, pos = t * kRows + row;
-          if (page[k] >= 0) {
-            const uint32_t one = BF16 ? 0x3f803f80u : 0x3c003c00u;  // keys: times 1
-            put_codes<D, CODE, BF16, true>(to, at, k * kStep, from[k * 256], which ? info.up[row >> 4] : one);
-          } else {
-            if (which) {
-              finite8<BF16>(a[k], pos, ch, sh->first[par], &sh->any_nonfinite[par]);
-              finite8<BF16>(b[k], pos, ch + 8, sh->first[par], &sh->any_nonfinite[par]);
+          for (int k = 0; k < 4; ++k) {
+            const int down = (k0 + k) * kStep, row = down + at.row, pos = t * kRows + row;
+            if (page[k] >= 0) {
+              const uint32_t one = BF16 ? 0x3f803f80u : 0x3c003c00u;  // keys: times 1
+              put_codes<D, CODE, BF16, true>(to, at, down, from[(k0 + k) * 256], which ? info.up[row >> 4] : one);
+            } else {
+              if (which) finite8<BF16>(a[k], pos, at.channel, sh->first[par], &sh->any_nonfinite[par]);
+              *reinterpret_cast<uint4*>(to + at.at + down * 128) = a[k];
             }
-            *reinterpret_cast<uint4*>(to + at.first + k * kStep * 128) = swap ? b[k] : a[k];
-            *reinterpret_cast<uint4*>(to + at.second + k * kStep * 128) = swap ? a[k] : b[k];
           }
         }
       }
@@ -1291,12 +1280,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     if (blockIdx.x == gridDim.x - 1) p.pos[gridDim.x] = make_int4(p.a.requests, 0, 0, 0);
   }
 
-  // 256 threads x 144 + 128 x 64 + 256 x 64 registers = 640 x 96, what the launch holds
+  // 256 threads x 152 + 128 x 48 + 256 x 64 registers = 640 x 96, what the launch holds
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     softmax_role<D, BF16>(p, &sh, warp >> 2);
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == 8) part_role<D>(p, &sh, smem);
     else if (warp == 9) mma_role<D, BF16>(p, &sh, smem);
     else if (warp == 10) tile_role<D, CODE, BF16>(p, &sh, smem + (2 + C::kStages) * C::kTile);
