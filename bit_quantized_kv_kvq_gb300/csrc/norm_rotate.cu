@@ -13,6 +13,9 @@
 // The angle is kept in turns as a 64-bit fraction: position * turns[j] mod 2^64
 // is exact, its upper half goes to sincospif (2^-25 of half a turn off), so a
 // position of a million is as good as one of ten.
+//
+// 32768 tokens of 40 heads of 128 (671 MB): 123 us, 5460 GB/s, 0.82 of the copy rate (127.6
+// with the loads behind the sines). 16 tokens: 4.9 us, one launch (6.2).
 #include "paged_internal.h"
 
 namespace kvq {
@@ -125,7 +128,8 @@ template <int D, bool BF16>
 cudaError_t launch(const RotateArgs& a, cudaStream_t st) {
   constexpr int kHeads = 256 / D;
   const int all = (a.q_heads + a.k_heads + kHeads - 1) / kHeads;
-  // few tokens: a warp for every pass, for latency; many: the sines of a token serve all its heads
+  // few tokens: a warp for every pass, for latency (16 tokens 4.9 us against 6.2 with a warp for
+  // four); many: the sines of a token serve all its heads (at 4099 tokens both take 8.2 us)
   const int parts = a.tokens < 256 ? all : a.tokens < 2048 ? (all + 3) / 4 : 1, passes = (all + parts - 1) / parts;
   const int64_t grid = ((int64_t)a.tokens * parts + kWarps - 1) / kWarps;
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;

@@ -5,6 +5,10 @@
 // of single requests are 0 and planning knows nothing of it. A complete page
 // never changes and can be named by several rows; the open page's rows are in the
 // request's tail, so a fork copies those rows and takes a page of its own.
+//
+// 60 forks in 8 layers of 8 heads of 128 (116 MB read and written): 22 us, 0.8 of the copy rate. Release
+// of 184000 entries 52 us (sixteen CTAs, eight entries a thread side by side; eight CTAs, one
+// by one, 134 us): scattered counts from sixteen SMs. Release of 464 entries 7 us, latency.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -183,8 +187,8 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
 // --------------------------------------------------------------------------
 constexpr int kCluster = 16;  // CTAs of the large form
 constexpr int kRun = 8;       // and consecutive entries of its threads
-// Table entries (of all rows) that one CTA releases alone. us for release of 8 requests
-// of 900 tokens, 464 entries: alone 5, a cluster of eight 10.6 (its barriers).
+// Table entries (of all rows) that one CTA releases alone: 464 entries take it 7 us,
+// a cluster of eight 10.6 (its barriers).
 constexpr int64_t kAlone = 8192;
 
 // The last index b in [0, n) with key[b] <= x (keys ascending, key[0] <= x).

@@ -10,7 +10,7 @@
 // consecutive tokens, so that the group shares each key tile and the diagonal cuts few.
 //
 // Codes are exact numbers of the input type (fp16 or bf16, int8 or e4m3), so the
-// operands are the codes themselves, converted on the way from L2 to shared memory by four
+// operands are the codes themselves, copied to shared memory and converted there by eight
 // warps, and the scales stay out of them: a score's factor is c s_k of its page;
 // a value's scale s_v = f 2^e goes half into the weight (2^(s - m + log2 f), f in
 // [1, 2)) and half into the operand (code 2^e, exact), which bounds both
@@ -28,6 +28,19 @@
 // Warps 0-3 and 4-7: softmax of the units; 8: the range's blocks and their
 // queries; 9: tensor core issue; 10: tiles (page ids, scales, copies of their codes);
 // 11: the gate, which follows the operands (gate_role); 12-19: codes and open rows to operands.
+//
+// 2048 tokens at 65536, 32/8 heads of 128, int8, fp16: 1743 us, 1242 TFLOP/s, 0.66 of the
+// measured bf16 rate. A pair of units takes 4000 clocks a key tile, of which the products are
+// 2048: what bounds it is a unit's chain (scores, 2000 clocks of softmax beside the
+// conversion on the same schedulers, products at 80 to 90 clocks each for 64, as operands,
+// copies and conversion share the bandwidth of shared memory). 4 requests of 8 draft tokens on
+// up to 110000, 64/8 heads, bf16: 230 us, 2670 GB/s, 0.40 of the copy rate: an operand takes
+// the converting warps 900 clocks. Eight requests of 1 to 5 tokens on 1000: 31 us, latency
+// of the first tile of cold code, the ends and the merge.
+// Tried: codes loaded straight into registers (their latency shows at every fence: 2.4 ms
+// for the first case), keys and values in rings of their own with two groups of four
+// converting warps (2.17 ms), pieces of half an operand (1.92 ms), one issue loop for
+// both orders of the units (1.87 ms), no gate (1.87 ms).
 #pragma once
 
 #include "attn_common.cuh"
@@ -356,8 +369,9 @@ __device__ __forceinline__ void tile_role(const Params& p, Shared* sh, unsigned 
     give_part(sh, it);
     // -1: no page, -2: a bad one
     auto page_of = [&](int t) {
+      if (t + ahead >= t1) return -1;
       const int pos = (t + ahead) * kRows + 16 * g;
-      if (t + ahead >= t1 || pos >= full) return -1;
+      if (pos >= full) return -1;
       const int page = row[pos >> c.page_shift];
       return page >= 0 && page < c.num_pages ? page : -2;
     };
