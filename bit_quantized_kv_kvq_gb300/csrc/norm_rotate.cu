@@ -128,9 +128,12 @@ template <int D, bool BF16>
 cudaError_t launch(const RotateArgs& a, cudaStream_t st) {
   constexpr int kHeads = 256 / D;
   const int all = (a.q_heads + a.k_heads + kHeads - 1) / kHeads;
-  // few tokens: a warp for every pass, for latency (16 tokens 4.9 us against 6.2 with a warp for
-  // four); many: the sines of a token serve all its heads (at 4099 tokens both take 8.2 us)
-  const int parts = a.tokens < 256 ? all : a.tokens < 2048 ? (all + 3) / 4 : 1, passes = (all + parts - 1) / parts;
+  // Few passes: a warp for each, for latency; many: the sines of a token serve all its
+  // heads. us with a warp a pass / for four / for the token, 40 heads of 128 (20 passes a token):
+  //   tokens    16           64           128          256          512          2048           4096           8192
+  //          2.2/2.7/7.6  2.5/2.7/7.7  2.9/2.9/7.7  4.6/3.4/7.9  7.1/4.2/8.0  22.6/10.4/10.9  44.5/19.1/17.2  91/38.4/33.8
+  const int64_t work = (int64_t)a.tokens * all;
+  const int parts = work < 2560 ? all : work < 51200 ? (all + 3) / 4 : 1, passes = (all + parts - 1) / parts;
   const int64_t grid = ((int64_t)a.tokens * parts + kWarps - 1) / kWarps;
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   if (a.interleaved) norm_rotate_kernel<D, BF16, true><<<(unsigned)grid, kWarps * 32, 0, st>>>(a, passes, parts);

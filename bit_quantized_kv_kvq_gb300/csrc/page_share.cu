@@ -8,7 +8,7 @@
 //
 // 60 forks in 8 layers of 8 heads of 128 (116 MB read and written): 22 us, 0.8 of the copy rate. Release
 // of 184000 entries 52 us (sixteen CTAs, eight entries a thread side by side; eight CTAs, one
-// by one, 134 us): scattered counts from sixteen SMs. Release of 464 entries 7 us, latency.
+// by one, 134 us): scattered counts from sixteen SMs. Release of 464 entries 4 us, latency.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -61,7 +61,9 @@ __device__ __forceinline__ long long block_scan(long long x, long long* all) {
 constexpr int kCopy = 1, kState = 2;
 constexpr int kEntries = 256;      // table entries of a unit of work
 constexpr int kTailBytes = 4096;   // bytes of a tail slab of a unit of work
-constexpr int64_t kOneLaunchBytes = 64 << 10;  // of tails, at most, that one CTA copies alone
+// Room of the pairs' tails, in bytes, up to which one CTA copies alone. us alone / by two launches:
+// 16 KB 4.5/5.4, 64 KB 5.1/6.3, 128 KB 6.8/7.6, 256 KB 9.1/7.6, 1 MB 22/7.6.
+constexpr int64_t kOneLaunchBytes = 128 << 10;
 
 template <int WHAT>
 __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
@@ -187,9 +189,9 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a) {
 // --------------------------------------------------------------------------
 constexpr int kCluster = 16;  // CTAs of the large form
 constexpr int kRun = 8;       // and consecutive entries of its threads
-// Table entries (of all rows) that one CTA releases alone: 464 entries take it 7 us,
-// a cluster of eight 10.6 (its barriers).
-constexpr int64_t kAlone = 8192;
+// Table entries (of all rows) up to which one CTA releases alone. us alone / by the cluster:
+// 456 entries 4.0/8.2, 2048 8.0/9.2, 4032 15.6/10.1, 8000 28/10.1, 32000 111/14.
+constexpr int64_t kAlone = 2048;
 
 // The last index b in [0, n) with key[b] <= x (keys ascending, key[0] <= x).
 __device__ __forceinline__ int last_le(const int* key, int n, int x) {

@@ -500,7 +500,7 @@ KVQ_API kvq_status kvq_paged_release_shared(kvq_paged_cache* cache, int32_t requ
  * the stack is too short, nothing changes and the status word is set. (A source's
  * table entry out of range is copied as it is, counts no holder and sets the status
  * word.) Entries past the copied ones stay as they are. All arrays int32 on
- * the device. One launch, two where the pairs' tails have room for more than 64 KiB. */
+ * the device. One launch, two where the pairs' tails have room for more than 128 KiB. */
 KVQ_API kvq_status kvq_paged_fork(kvq_paged_cache* cache, int32_t requests, int32_t pairs, const int32_t* src,
                                   const int32_t* dst, int32_t* lens, int32_t* table, const int32_t* free_pages,
                                   int32_t* free_count, int32_t* shared, void* stream);

@@ -87,7 +87,7 @@ def test_fork(r, page, longest, empty, layers, heads, dim, dtype):
     n = bk.lens.copy()
     bk.fork(src, dst)
     tails = len(src) * layers * heads * 2 * page * dim * 2
-    assert kvq.kernel_launches() == launches + (1 if tails <= 65536 else 2)
+    assert kvq.kernel_launches() == launches + (1 if tails <= 131072 else 2)
     bk.check()
     for i in range(layers):
         want = before[i]
