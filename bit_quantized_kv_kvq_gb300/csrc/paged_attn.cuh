@@ -9,13 +9,14 @@
 // O += P V. A unit is 128 rows: every query head of one kv-head on 128 / group
 // consecutive tokens, so that the group shares each key tile and the diagonal cuts few.
 //
-// Codes are exact numbers of the input type (fp16 or bf16, int8 or e4m3), so the
-// operands are the codes themselves, copied to shared memory and converted there by eight
-// warps, and the scales stay out of them: a score's factor is c s_k of its page;
-// a value's scale s_v = f 2^e goes half into the weight (2^(s - m + log2 f), f in
-// [1, 2)) and half into the operand (code 2^e, exact), which bounds both
-// whatever the scales; the sum of weights takes 1 / f off again. All of this is per
-// group of 16 keys, so pages of any size cost the same.
+// Codes are exact numbers of the input type (fp16 or bf16, int8 or e4m3; values and
+// weights are fp16 in both where they can, see Scales), so the operands are the codes
+// themselves, copied to shared memory and converted there by eight warps, and the
+// scales stay out of them: a score's factor is c s_k of its page; a value's scale s_v =
+// f 2^e goes half into the weight (2^(s - m + log2 f), f in [1, 2)) and half into the
+// operand (code 2^e, exact), which bounds both whatever the scales; the sum of weights
+// takes 1 / f off again. All of this is per group of 16 keys, so pages of any size cost
+// the same.
 //
 // A block is two units: consecutive tokens of a request on the same key tiles, or,
 // where the tokens left fit one unit, the same rows on every other tile (their sums
@@ -29,12 +30,12 @@
 // queries; 9: tensor core issue; 10: tiles (page ids, scales, copies of their codes);
 // 11: the gate, which follows the operands (gate_role); 12-19: codes and open rows to operands.
 //
-// 2048 tokens at 65536, 32/8 heads of 128, int8, fp16: 1743 us, 1242 TFLOP/s, 0.66 of the
+// 2048 tokens at 65536, 32/8 heads of 128, int8, fp16: 1730 us, 1251 TFLOP/s, 0.66 of the
 // measured bf16 rate. A pair of units takes 4000 clocks a key tile, of which the products are
 // 2048: what bounds it is a unit's chain (scores, 2000 clocks of softmax beside the
 // conversion on the same schedulers, products at 80 to 90 clocks each for 64, as operands,
 // copies and conversion share the bandwidth of shared memory). 4 requests of 8 draft tokens on
-// up to 110000, 64/8 heads, bf16: 230 us, 2670 GB/s, 0.40 of the copy rate: an operand takes
+// up to 110000, 64/8 heads, bf16: 254 us, 2420 GB/s, 0.36 of the copy rate: an operand takes
 // the converting warps 900 clocks. Eight requests of 1 to 5 tokens on 1000: 31 us, latency
 // of the first tile of cold code, the ends and the merge.
 // Tried: codes loaded straight into registers (their latency shows at every fence: 2.4 ms
@@ -180,9 +181,10 @@ __device__ __forceinline__ Pos locate(const Params& p, int b, const Req& r, long
 // --------------------------------------------------------------------------
 struct alignas(16) Info {  // per 16 keys
   float2 a[kGroups], lg[kGroups], inv[kGroups];  // score factor, log2 f, 1 / f, twice each: operands of pairs
-  uint32_t up[kGroups];                          // 2^e, a pair of the input type
+  uint32_t up[kGroups];                          // 2^e, a pair of the values' operand type
   int page[2][kGroups];                          // of keys, of values; -1: open rows or none, -2: zeros
   int coded;                                     // all of them pages
+  int half;                                      // values and weights in fp16
 };
 
 struct Part {
@@ -204,6 +206,7 @@ struct Shared {
   uint64_t join_ready, join_done, conv;
   Info info[kInfo];
   Part part[kParts];
+  int half[8];  // by operand stage: its values are fp16
   uint32_t tmem;
   int any_nonfinite[2];
   int first[2][3][128];  // first position in the open page whose value is NaN, +inf, -inf, per channel
@@ -328,26 +331,36 @@ __device__ __forceinline__ void part_role(const Params& p, Shared* sh, unsigned 
 // --------------------------------------------------------------------------
 // Tiles: pages, scales, prefetch
 // --------------------------------------------------------------------------
+struct Scales {
+  float a, lg, inv;  // of Info
+  int e;
+  bool zero, half;  // values' operand is zeros; code 2^e is an exact fp16 number
+};
+
+// 2^e stays a number of the operand's type, with products code 2^e exact (e4m3: multiples of 2^-9).
 template <int CODE, bool BF16>
-__device__ __forceinline__ float4 factors(float sk, float sv, float scale_log2, bool& zero_values) {
-  // 2^e stays a number of the type, with products code 2^e exact (e4m3: multiples of 2^-9)
-  constexpr int kMin = BF16 ? -126 : CODE == KVQ_PAGE_INT8 ? -24 : -15;
+__device__ __forceinline__ Scales scales_to(float sk, float sv, float scale_log2) {
+  constexpr int kMinHalf = CODE == KVQ_PAGE_INT8 ? -24 : -15, kMaxHalf = CODE == KVQ_PAGE_INT8 ? 8 : 7;
+  constexpr int kMin = BF16 ? -126 : kMinHalf;
+  const bool finite = fabsf(sv) <= 3.0e38f;
   const uint32_t bits = __float_as_uint(sv);
-  int e = (int)((bits >> 23) & 255) - 127;
+  Scales r;
+  r.e = (int)((bits >> 23) & 255) - 127;
   float f = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);
-  if (e < kMin) e = kMin, f = sv * (BF16 ? 0x1p126f : CODE == KVQ_PAGE_INT8 ? 0x1p24f : 0x1p15f);  // exact
-  zero_values = !(fabsf(sv) <= 3.0e38f) || sv == 0.0f;
-  if (sv == 0.0f) e = 0, f = 1.0f;
-  if (!(fabsf(sv) <= 3.0e38f)) e = 0, f = NAN;
-  uint32_t w;
-  if (BF16) w = (uint32_t)(e + 127) << 7;
-  else w = e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24);
-  float4 r;
-  r.x = fabsf(sk) <= 3.0e38f ? sk * scale_log2 : NAN;
-  r.y = log2f(f);
-  r.z = f == f ? 1.0f / f : 1.0f;  // a masked weight's share stays 0
-  r.w = __uint_as_float(w | (w << 16));
+  if (r.e < kMin) r.e = kMin, f = sv * (BF16 ? 0x1p126f : CODE == KVQ_PAGE_INT8 ? 0x1p24f : 0x1p15f);  // exact
+  r.zero = !finite || sv == 0.0f;
+  if (r.zero) r.e = 0, f = finite ? 1.0f : NAN;
+  r.half = !BF16 || (r.e >= kMinHalf && r.e <= kMaxHalf);
+  r.a = fabsf(sk) <= 3.0e38f ? sk * scale_log2 : NAN;
+  r.lg = log2f(f);
+  r.inv = f == f ? 1.0f / f : 1.0f;  // a masked weight's share stays 0
   return r;
+}
+
+// The pair 2^e.
+__device__ __forceinline__ uint32_t power_pair(int e, bool half) {
+  const uint32_t w = !half ? (uint32_t)(e + 127) << 7 : e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24);
+  return w | (w << 16);
 }
 
 // Four tiles at a time, a lane for each of their groups of 16 keys. The next
@@ -404,15 +417,18 @@ __device__ __forceinline__ void tile_role(const Params& p, Shared* sh, unsigned 
     int page = page_of(t0);
     float2 s = scales_of(page);
     for (int t = t0; ok && t < t1; t += 4) {
-      float4 f = make_float4(p.a.scale_log2, 0.0f, 1.0f, 0.0f);
-      bool zero = true;
-      if (page >= 0) f = factors<CODE, BF16>(s.x, s.y, p.a.scale_log2, zero);
+      Scales f = {p.a.scale_log2, 0.0f, 1.0f, 0, true, true};
+      if (page >= 0) f = scales_to<CODE, BF16>(s.x, s.y, p.a.scale_log2);
       if (page == -2) {
         raise_status(c.status, kStatusBadIndex);
-        f = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);
+        f.a = 0.0f, f.lg = -INFINITY;
       }
-      const int page_v = page >= 0 && zero ? -2 : page;
-      const uint32_t coded = __ballot_sync(kFull, page >= 0 && page_v >= 0);
+      const int page_v = page >= 0 && f.zero ? -2 : page;
+      const uint32_t own = 255u << (lane & 24);  // the lanes of the tile
+      const bool coded = (__ballot_sync(kFull, page >= 0 && page_v >= 0) & own) == own;
+      // The values' products take fp16 in either type, where they can: weights of 11 bits.
+      const uint32_t halves = __ballot_sync(kFull, f.half);  // of all lanes: not behind a lane's own condition
+      const bool half = !BF16 || (coded && (halves & own) == own);
       const int live = min(4, t1 - t), now = page;
       page = page_of(t + 4);
 #pragma unroll 1
@@ -422,13 +438,13 @@ __device__ __forceinline__ void tile_role(const Params& p, Shared* sh, unsigned 
         if (!ok) break;
         if (ahead == k) {
           Info& o = sh->info[slot];
-          o.a[g] = make_float2(f.x, f.x);
-          o.lg[g] = make_float2(f.y, f.y);
-          o.inv[g] = make_float2(f.z, f.z);
-          o.up[g] = __float_as_uint(f.w);
+          o.a[g] = make_float2(f.a, f.a);
+          o.lg[g] = make_float2(f.lg, f.lg);
+          o.inv[g] = make_float2(f.inv, f.inv);
+          o.up[g] = power_pair(f.e, half);
           o.page[0][g] = now;
           o.page[1][g] = page_v;
-          if (g == 0) o.coded = ((coded >> (8 * k)) & 255u) == 255u;
+          if (g == 0) o.coded = coded, o.half = half;
         }
         __syncwarp();
         if (lane == 0) arrive(&sh->info_full[slot]);
@@ -590,8 +606,9 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
       if (!wait(&sh->raw_full[rs], (i / C::kRaws) & 1, c.status)) return;
       if (!wait(&sh->kv_empty[st], ((i / C::kStages) & 1) ^ 1, c.status)) return;
       if (info.coded) {
-        if (which) convert_codes<D, CODE, BF16, true>(to, at, from, info);
-        else convert_codes<D, CODE, BF16, false>(to, at, from, info);
+        if (which == 0) convert_codes<D, CODE, BF16, false>(to, at, from, info);
+        else if (!BF16 || info.half) convert_codes<D, CODE, false, true>(to, at, from, info);
+        else convert_codes<D, CODE, BF16, true>(to, at, from, info);
       } else {
         const int n = part->n, full = n & ~(P - 1), t = part->t0 + j;
         const uint16_t* tail =
@@ -623,6 +640,7 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
       fence_proxy_async_smem();  // the tensor cores read what was written here
       __syncwarp();
       if (lane == 0) {
+        if (BF16 && which) sh->half[st] = info.half;  // all warps the same
         arrive(&sh->kv_full[st]);
         arrive(&sh->raw_empty[rs]);
         if (which) arrive(&sh->info_empty[slot]);
@@ -658,6 +676,7 @@ template <int D, bool BF16>
 __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned char* smem) {
   using C = Cfg<D>;
   constexpr uint32_t kQK = t5::instr_desc(128, 128, BF16, false), kPV = t5::instr_desc(128, D, BF16, true);
+  constexpr uint32_t kHalfPV = t5::instr_desc(128, D, false, true);
   const uint32_t tmem = uniform(sh->tmem);
   uint32_t* status = p.c.status;
   const uint32_t base = smem_u32(smem) >> 4;
@@ -685,13 +704,13 @@ __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned c
     }
     t5::commit(&sh->s_full[u]);
   };
-  auto values = [&](const int u, uint32_t at, bool first) {
+  auto values = [&](const int u, uint32_t at, bool first, uint32_t kind) {
     uint32_t b = base;
     asm volatile("" : "+r"(b));
     const uint32_t v = b + ((kRows * 128 >> 4) << 16) + (2 + at) * (C::kTile >> 4);
 #pragma unroll
     for (int kk = 0; kk < kRows / 16; ++kk)
-      t5::mma_ts(tmem + 256 + u * D, tmem + u * 128 + 64 + kk * 8, operand(v + kk * (2048 >> 4)), kPV, kk > 0 || !first);
+      t5::mma_ts(tmem + 256 + u * D, tmem + u * 128 + 64 + kk * 8, operand(v + kk * (2048 >> 4)), kind, kk > 0 || !first);
   };
   auto query = [&](const int u) {
     ok = ok && wait(&sh->q_full[u], q_phase[u], status);
@@ -729,8 +748,9 @@ __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned c
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           weights(u);  // says that these operands are there, too (gate_role)
+          const uint32_t kind = BF16 && uniform(sh->half[v]) ? kHalfPV : kPV;
           if (ok && t5::elect_one()) {
-            values(u, v, j == 0);
+            values(u, v, j == 0, kind);
             if (u) t5::commit(&sh->kv_empty[v]);
             if (more) {
               scores(u, k);
@@ -766,8 +786,9 @@ __device__ __forceinline__ void mma_role(const Params& p, Shared* sh, unsigned c
           const bool more = j + 2 < n;
           const uint32_t v = next(), k = more ? next() : 0;
           weights(u);
+          const uint32_t kind = BF16 && uniform(sh->half[v]) ? kHalfPV : kPV;
           if (ok && t5::elect_one()) {
-            values(u, v, j0 == 0);
+            values(u, v, j0 == 0, kind);
             t5::commit(&sh->kv_empty[v]);
             if (more) {
               scores(u, k);
@@ -855,13 +876,13 @@ __device__ __forceinline__ uint64_t to_weights(const uint32_t* s, uint64_t a2, u
 // The reference of a row's exponentials: it moves only when a score (by its
 // page's factor, in units of log 2) passes it by 8, so that few tiles scale O.
 // Each row goes by its own scores. A weight is 2^(s a + log2 f - m), one multiply-add.
-// In fp16 m lies 6 below the score that set it: weights with f stay below 2^15, and
+// m lies 6 below the score that set it: weights with f stay below 2^15, and in fp16
 // those 2^-20 of it above the type's subnormal numbers. Past 2^20 m's own
 // rounding would be a factor without limit: such a row (`far`) rounds its scaled scores and
 // subtracts the score itself, which is exact near the largest ones.
-template <int D, bool BF16>
+template <int D>
 struct Reference {
-  static constexpr float kLift = BF16 ? 0.0f : 6.0f;
+  static constexpr float kLift = 6.0f;
   float m;       // far: the score, else what is subtracted
   bool far, any_far;
 
@@ -934,7 +955,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
   uint32_t* status = p.c.status;
   const uint32_t lanes = sh->tmem + ((uint32_t)(warp * 32) << 16);
   const uint32_t tS = lanes + unit * 128, tP = tS + 64, tO = lanes + 256 + unit * D, tO_other = lanes + 256 + (1 - unit) * D;
-  Reference<D, BF16> ref;
+  Reference<D> ref;
   uint32_t phase = 0;  // bits 0: scores, 1, 2: the units' outputs, 3: joins
   int tile = 0;
   for (int it = 0;; ++it) {
@@ -964,13 +985,48 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
           uint64_t sum = 0, off2;
           // 32 scores to weights. P takes the upper half of the scores' place: of the
           // keys in descending order, a group's weights lie where scores already read were.
+          // (In bf16 weights, of 8 bits, only those of a tile whose values fp16 does not
+          // hold: open rows, scales out of its range.)
+          const bool half = !BF16 || info.half != 0;
           auto weights32 = [&](uint32_t* x, int c, Factors& f) {
             uint32_t w[16];
 #pragma unroll
             for (int g = 0; g < 2; ++g)
-              sum = f2_fma(to_weights<BF16>(x + 16 * g, f.a[g], f2_add(off2, f.lg[g]), w + 8 * g), f.inv[g], sum);
+              sum = f2_fma(to_weights<false>(x + 16 * g, f.a[g], f2_add(off2, f.lg[g]), w + 8 * g), f.inv[g], sum);
             if (c > 0) f = Factors(info, c - 1);  // the next group's, on their way meanwhile
             t5::st16(tP + 16 * c, w);
+          };
+          // The same for rows that do not see all keys, far ones, and bf16 weights; keys
+          // from `none` on no row attends.
+          auto slow = [&](uint32_t* x, int none) {
+            const float off = ref.off();
+#pragma unroll 1
+            for (int c = 3; c >= 0; --c) {
+              uint32_t w[16];
+              if (32 * c >= none) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = 0u;
+                t5::st16(tP + 16 * c, w);
+                continue;
+              }
+              t5::ld32(tS + 32 * c, x);
+              t5::wait_ld32(x);
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const int k = 2 * c + g;
+                if (ref.any_far) ref.settle(x + 16 * g, info.a[k].x);
+                const float a = ref.far ? 1.0f : info.a[k].x, lg = info.lg[k].x;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)  // masked after the factor: -inf * 0 is NaN
+                  x[16 * g + i] = 32 * c + 16 * g + i >= seen ? 0xff800000u
+                                                              : __float_as_uint(fmaf(__uint_as_float(x[16 * g + i]), a, off + lg));
+                const uint64_t one = f2_pack(1.0f, 1.0f), zero = f2_pack(0.0f, 0.0f);
+                const uint64_t part = half ? to_weights<false>(x + 16 * g, one, zero, w + 8 * g)
+                                           : to_weights<BF16>(x + 16 * g, one, zero, w + 8 * g);
+                sum = f2_fma(part, f2_pack(info.inv[k].x, info.inv[k].x), sum);
+              }
+              t5::st16(tP + 16 * c, w);
+            }
           };
           auto reference = [&]() {
             const float off = ref.off();
@@ -1005,7 +1061,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
               t5::wait_ld32(s + 32);
             }
             reference();
-            if (!ref.any_far) {
+            if (!ref.any_far && half) {
               uint32_t a[32];
               Factors f(info, 3);
               weights32(s + 32, 3, f);
@@ -1017,18 +1073,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
               t5::wait_ld32(s);
               weights32(s, 0, f);
             } else {
-#pragma unroll 1
-              for (int c = 3; c >= 0; --c) {
-                t5::ld32(tS + 32 * c, s);
-                t5::wait_ld32(s);
-                Factors f(info, c);
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                  ref.settle(s + 16 * g, info.a[2 * c + g].x);
-                  if (ref.far) f.a[g] = f2_pack(1.0f, 1.0f);
-                }
-                weights32(s, c, f);
-              }
+              slow(s, kRows);
             }
           } else {
             // a tile that ends past some row's own key; keys from `none` on no row attends
@@ -1046,32 +1091,8 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
               for (int g = 0; g < 2; ++g) top = fmaxf(top, max_of<16>(s + 16 * g) * info.a[2 * c + g].x);
             }
             ref.raise(limit != kNever ? top : -INFINITY, l, tO, any);
-            const float off = ref.off();
-#pragma unroll 1
-            for (int c = 3; c >= 0; --c) {
-              uint32_t s[32], w[16];
-              if (32 * c >= none) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = 0u;
-                t5::st16(tP + 16 * c, w);
-                continue;
-              }
-              t5::ld32(tS + 32 * c, s);
-              t5::wait_ld32(s);
-#pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                const int k = 2 * c + g;
-                if (ref.any_far) ref.settle(s + 16 * g, info.a[k].x);
-                const float a = ref.far ? 1.0f : info.a[k].x, lg = info.lg[k].x;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)  // masked after the factor: -inf * 0 is NaN
-                  s[16 * g + i] = 32 * c + 16 * g + i >= seen ? 0xff800000u
-                                                              : __float_as_uint(fmaf(__uint_as_float(s[16 * g + i]), a, off + lg));
-                sum = f2_fma(to_weights<BF16>(s + 16 * g, f2_pack(1.0f, 1.0f), f2_pack(0.0f, 0.0f), w + 8 * g),
-                             f2_pack(info.inv[k].x, info.inv[k].x), sum);
-              }
-              t5::st16(tP + 16 * c, w);
-            }
+            uint32_t s[32];
+            slow(s, none);
           }
           float u, v;
           f2_unpack(sum, u, v);

@@ -60,7 +60,7 @@ class Filled:
             out.append(torch.cat([x.reshape(-1, self.d), self.cache.tails(0)[b, head, i, :n % self.page].double()]))
         return out
 
-    def check(self, out, q=None, scale=None, requests=None):
+    def check(self, out, q=None, scale=None, requests=None, weight=None):
         q, scale = (self.q if q is None else q).double(), self.scale if scale is None else scale
         u = torch.finfo(self.dtype).eps / 2
         g = self.hq // self.h
@@ -81,7 +81,7 @@ class Filled:
                     # numbers to 2^-25, beside a sum of 2^6 or more), the
                     # scores' fp32 sums (256 roundings of 2^-23 of the sum of magnitudes), exponentials
                     # and sums, the output's own rounding
-                    tol = (u + 2 * 256 * 2.0 ** -23 * size + 2.0 ** -18) * w * 1.01 + u * ref.abs()
+                    tol = ((weight or u) + 2 * 256 * 2.0 ** -23 * size + 2.0 ** -18) * w * 1.01 + u * ref.abs()
                     if self.dtype == F16:
                         tol += n * 2.0 ** -31 * v.abs().amax()
                     err = (out[lo:lo + m, a].double() - ref).abs()
@@ -121,6 +121,17 @@ def test_attend(case):
     f.check(out)
     assert torch.equal(out, f.attend())  # the same bits every time
     assert f.cache.status() == 0
+
+
+@pytest.mark.parametrize("code,d", [("int8", 128), ("e4m3", 64)])
+def test_weights_of_11_bits_in_bf16(code, d):
+    """Tiles of complete pages take fp16 weights in a bf16 cache too."""
+    f = Filled([2944, 640, 128], [100, 64, 1], 8, 2, d, 64, code, BF16, seed=12)
+    f.check(f.attend(), weight=2.0 ** -11)
+    # a scale beyond fp16 in one page: the bound of bf16 weights
+    f.cache.scales(0)[f.table[0, 3].item(), :, 1] *= 2.0 ** 40
+    f.check(f.attend())
+    f.check(f.attend(), weight=2.0 ** -11, requests=[1, 2])
 
 
 def test_single_tokens_agree_with_decode():
