@@ -30,12 +30,12 @@
 // queries; 9: tensor core issue; 10: tiles (page ids, scales, copies of their codes);
 // 11: the gate, which follows the operands (gate_role); 12-19: codes and open rows to operands.
 //
-// 2048 tokens at 65536, 32/8 heads of 128, int8, fp16: 1730 us, 1251 TFLOP/s, 0.66 of the
+// 2048 tokens at 65536, 32/8 heads of 128, int8, fp16: 1725 us, 1255 TFLOP/s, 0.67 of the
 // measured bf16 rate. A pair of units takes 4000 clocks a key tile, of which the products are
 // 2048: what bounds it is a unit's chain (scores, 2000 clocks of softmax beside the
 // conversion on the same schedulers, products at 80 to 90 clocks each for 64, as operands,
 // copies and conversion share the bandwidth of shared memory). 4 requests of 8 draft tokens on
-// up to 110000, 64/8 heads, bf16: 254 us, 2420 GB/s, 0.36 of the copy rate: an operand takes
+// up to 110000, 64/8 heads, bf16: 241 us, 2540 GB/s, 0.38 of the copy rate: an operand takes
 // the converting warps 900 clocks. Eight requests of 1 to 5 tokens on 1000: 31 us, latency
 // of the first tile of cold code, the ends and the merge.
 // Tried: codes loaded straight into registers (their latency shows at every fence: 2.4 ms
@@ -605,9 +605,11 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
       if (which == 0 && !wait(&sh->info_full[slot], (tile / kInfo) & 1, c.status)) return;
       if (!wait(&sh->raw_full[rs], (i / C::kRaws) & 1, c.status)) return;
       if (!wait(&sh->kv_empty[st], ((i / C::kStages) & 1) ^ 1, c.status)) return;
-      if (info.coded) {
+      const bool coded = info.coded != 0, half = info.half != 0;
+      if (BF16 && which && lane == 0) sh->half[st] = half;  // all warps the same
+      if (coded) {
         if (which == 0) convert_codes<D, CODE, BF16, false>(to, at, from, info);
-        else if (!BF16 || info.half) convert_codes<D, CODE, false, true>(to, at, from, info);
+        else if (!BF16 || half) convert_codes<D, CODE, false, true>(to, at, from, info);
         else convert_codes<D, CODE, BF16, true>(to, at, from, info);
       } else {
         const int n = part->n, full = n & ~(P - 1), t = part->t0 + j;
@@ -640,7 +642,6 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
       fence_proxy_async_smem();  // the tensor cores read what was written here
       __syncwarp();
       if (lane == 0) {
-        if (BF16 && which) sh->half[st] = info.half;  // all warps the same
         arrive(&sh->kv_full[st]);
         arrive(&sh->raw_empty[rs]);
         if (which) arrive(&sh->info_empty[slot]);

@@ -228,12 +228,13 @@ def test_release_of_bad_books():
         c.status()
 
 
-def test_fork_and_release_from_a_graph():
-    """A captured branch and end, replayed on the books as they are."""
-    bk = Books(6, 16, 90, 3, 2)
+@pytest.mark.parametrize("r,longest", [(6, 90), (300, 400)])
+def test_fork_and_release_from_a_graph(r, longest):
+    """A captured branch and end, replayed on the books as they are; a release by one CTA and by a cluster."""
+    bk = Books(r, 16, longest, 3, 2)
     c = bk.cache(2, 2)
     e, f = np.flatnonzero(bk.lens == 0), np.flatnonzero(bk.lens > 0)
-    src, dst, done = ints([f[0], f[1], -1]), ints(e), ints((np.arange(6) == e[0]) | (np.arange(6) == f[0]))
+    src, dst, done = ints([f[0], f[1], -1]), ints(e), ints((np.arange(r) == e[0]) | (np.arange(r) % 2 == f[0] % 2))
     keep = {k: v.clone() for k, v in bk.d.items()}
     d = bk.d
     gr = torch.cuda.CUDAGraph()
