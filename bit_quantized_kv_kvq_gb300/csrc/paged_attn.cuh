@@ -215,7 +215,8 @@ struct Shared {
   Pos from, to;
 };
 
-// Waits last as long as a few tiles, but the walker's as long as a block.
+// Waits last as long as a few tiles, but those of the warp that hands out the parts as
+// long as a block (four and 32 seconds, a poll that finds nothing taking 3.8 us).
 constexpr int kPolls = 8 * kWaitLimit, kLongPolls = 64 * kWaitLimit;
 
 // Whole warp: false where the wait gave up. (A rolled loop: unrolled, the many
@@ -249,8 +250,6 @@ struct Order {
   uint32_t base;  // operands before this part
   int n;          // tiles
   bool both;
-  __device__ __forceinline__ uint32_t keys(int j) const { return base + (both ? 2 * j : j == 0 ? 0 : 2 * j - 1); }
-  __device__ __forceinline__ uint32_t values(int j) const { return base + (both || j == n - 1 ? 2 * j + 1 : 2 * j + 2); }
   // operand k of the part: whether it is values, and of which tile
   __device__ __forceinline__ int which(int k) const { return both ? k & 1 : k == 2 * n - 1 || (k > 0 && (k & 1) == 0); }
   __device__ __forceinline__ int tile(int k) const { return both || k == 2 * n - 1 || k == 0 ? k >> 1 : k & 1 ? (k + 1) >> 1 : (k >> 1) - 1; }
