@@ -180,7 +180,8 @@ __device__ __forceinline__ Pos locate(const Params& p, int b, const Req& r, long
 // Shared memory
 // --------------------------------------------------------------------------
 struct alignas(16) Info {  // per 16 keys
-  float2 a[kGroups], lg[kGroups], inv[kGroups];  // score factor, log2 f, 1 / f, twice each: operands of pairs
+  float2 a[kGroups], lg[kGroups];  // score factor, log2 f, twice each: operands of pairs
+  float inv[kGroups];              // 1 / f
   uint32_t up[kGroups];                          // 2^e, a pair of the values' operand type
   int page[2][kGroups];                          // of keys, of values; -1: open rows or none, -2: zeros
   int coded;                                     // all of them pages
@@ -426,8 +427,8 @@ __device__ __forceinline__ void tile_role(const Params& p, Shared* sh, unsigned 
       const uint32_t own = 255u << (lane & 24);  // the lanes of the tile
       const bool coded = (__ballot_sync(kFull, page >= 0 && page_v >= 0) & own) == own;
       // The values' products take fp16 in either type, where they can: weights of 11 bits.
-      const uint32_t halves = __ballot_sync(kFull, f.half);  // of all lanes: not behind a lane's own condition
-      const bool half = !BF16 || (coded && (halves & own) == own);
+      // (A page of zeros or NaN is no reason against it: its neighbours' rows keep their bits.)
+      const bool half = (__ballot_sync(kFull, !BF16 || (page >= 0 && f.half)) & own) == own;
       const int live = min(4, t1 - t), now = page;
       page = page_of(t + 4);
 #pragma unroll 1
@@ -439,7 +440,7 @@ __device__ __forceinline__ void tile_role(const Params& p, Shared* sh, unsigned 
           Info& o = sh->info[slot];
           o.a[g] = make_float2(f.a, f.a);
           o.lg[g] = make_float2(f.lg, f.lg);
-          o.inv[g] = make_float2(f.inv, f.inv);
+          o.inv[g] = f.inv;
           o.up[g] = power_pair(f.e, half);
           o.page[0][g] = now;
           o.page[1][g] = page_v;
@@ -630,7 +631,8 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
             const int down = (k0 + k) * kStep, row = down + at.row, pos = t * kRows + row;
             if (page[k] >= 0) {
               const uint32_t one = BF16 ? 0x3f803f80u : 0x3c003c00u;  // keys: times 1
-              put_codes<D, CODE, BF16, true>(to, at, down, from[(k0 + k) * 256], which ? info.up[row >> 4] : one);
+              if (BF16 && which && half) put_codes<D, CODE, false, true>(to, at, down, from[(k0 + k) * 256], info.up[row >> 4]);
+              else put_codes<D, CODE, BF16, true>(to, at, down, from[(k0 + k) * 256], which ? info.up[row >> 4] : one);
             } else {
               if (which) finite8<BF16>(a[k], pos, at.channel, sh->first[par], &sh->any_nonfinite[par]);
               *reinterpret_cast<uint4*>(to + at.at + down * 128) = a[k];
@@ -853,24 +855,34 @@ __device__ __forceinline__ void gate_role(const Params& p, Shared* sh) {
 // --------------------------------------------------------------------------
 // Softmax
 // --------------------------------------------------------------------------
-// 16 scores to weights: p = 2^(s a + off), packed; their sum. a2, off2: each twice.
+// lo + hi of the pair w, added to two sums.
 template <bool BF16>
-__device__ __forceinline__ uint64_t to_weights(const uint32_t* s, uint64_t a2, uint64_t off2, uint32_t* p) {
-  uint64_t sum0, sum1;
+__device__ __forceinline__ void add_pair(uint32_t w, float& lo, float& hi) {
+  if (BF16)
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.f32.bf16 %0, a, %0;\n\tadd.f32.bf16 %1, b, %1;\n\t}"
+        : "+f"(lo), "+f"(hi)
+        : "r"(w));
+  else
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.f32.f16 %0, a, %0;\n\tadd.f32.f16 %1, b, %1;\n\t}"
+        : "+f"(lo), "+f"(hi)
+        : "r"(w));
+}
+
+// 16 scores to weights: p = 2^(s a + off), packed; their sum, as rounded: what a
+// large weight's rounding adds to the output it then takes off again (outputs are 1.2 to
+// 1.35 times a rounding away from 64 bits, 1.4 to 1.5 with a sum of unrounded
+// weights). a2, off2: each twice.
+template <bool BF16>
+__device__ __forceinline__ float to_weights(const uint32_t* s, uint64_t a2, uint64_t off2, uint32_t* p) {
+  float lo = 0.0f, hi = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float x, y;
     f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), a2, off2), x, y);
-    x = exp2_fast(x);
-    y = exp2_fast(y);
-    const uint64_t xy = f2_pack(x, y);
-    if (i == 0) sum0 = xy;
-    else if (i == 1) sum1 = xy;
-    else if (i & 1) sum1 = f2_add(sum1, xy);
-    else sum0 = f2_add(sum0, xy);
-    p[i] = pack2<BF16>(x, y);
+    p[i] = pack2<BF16>(exp2_fast(x), exp2_fast(y));
+    add_pair<BF16>(p[i], lo, hi);
   }
-  return f2_add(sum0, sum1);
+  return lo + hi;
 }
 
 // The reference of a row's exponentials: it moves only when a score (by its
@@ -925,11 +937,12 @@ struct Reference {
 // The factors of 32 keys, in pairs, read here and not earlier (the compiler would
 // keep all groups' in registers, and the scores out of them).
 struct Factors {
-  uint64_t a[2], lg[2], inv[2];
+  uint64_t a[2], lg[2];
+  float inv[2];
   __device__ __forceinline__ Factors(const Info& info, int c) {
     two(&info.a[2 * c], a);
     two(&info.lg[2 * c], lg);
-    two(&info.inv[2 * c], inv);
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(inv[0]), "=f"(inv[1]) : "r"(smem_u32(&info.inv[2 * c])));
   }
   static __device__ __forceinline__ void two(const float2* from, uint64_t (&to)[2]) {
     asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(to[0]), "=l"(to[1]) : "r"(smem_u32(from)));
@@ -982,7 +995,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
         if (!warp_live) {
           // nothing reads these rows' weights
         } else {
-          uint64_t sum = 0, off2;
+          uint64_t off2;
           // 32 scores to weights. P takes the upper half of the scores' place: of the
           // keys in descending order, a group's weights lie where scores already read were.
           // (In bf16 weights, of 8 bits, only those of a tile whose values fp16 does not
@@ -992,7 +1005,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
             uint32_t w[16];
 #pragma unroll
             for (int g = 0; g < 2; ++g)
-              sum = f2_fma(to_weights<false>(x + 16 * g, f.a[g], f2_add(off2, f.lg[g]), w + 8 * g), f.inv[g], sum);
+              l = fmaf(to_weights<false>(x + 16 * g, f.a[g], f2_add(off2, f.lg[g]), w + 8 * g), f.inv[g], l);
             if (c > 0) f = Factors(info, c - 1);  // the next group's, on their way meanwhile
             t5::st16(tP + 16 * c, w);
           };
@@ -1021,9 +1034,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
                   x[16 * g + i] = 32 * c + 16 * g + i >= seen ? 0xff800000u
                                                               : __float_as_uint(fmaf(__uint_as_float(x[16 * g + i]), a, off + lg));
                 const uint64_t one = f2_pack(1.0f, 1.0f), zero = f2_pack(0.0f, 0.0f);
-                const uint64_t part = half ? to_weights<false>(x + 16 * g, one, zero, w + 8 * g)
-                                           : to_weights<BF16>(x + 16 * g, one, zero, w + 8 * g);
-                sum = f2_fma(part, f2_pack(info.inv[k].x, info.inv[k].x), sum);
+                const float part = half ? to_weights<false>(x + 16 * g, one, zero, w + 8 * g)
+                                        : to_weights<BF16>(x + 16 * g, one, zero, w + 8 * g);
+                l = fmaf(part, info.inv[k], l);
               }
               t5::st16(tP + 16 * c, w);
             }
@@ -1094,9 +1107,6 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
             uint32_t s[32];
             slow(s, none);
           }
-          float u, v;
-          f2_unpack(sum, u, v);
-          l += u + v;
         }
         t5::wait_st();
         t5::fence_before();
