@@ -30,8 +30,9 @@
 // queries; 9: tensor core issue; 10: tiles (page ids, scales, copies of their codes);
 // 11: the gate, which follows the operands (gate_role); 12-19: codes and open rows to operands.
 //
-// 2048 tokens at 65536, 32/8 heads of 128, int8, fp16: 1725 us, 1255 TFLOP/s, 0.67 of the
-// measured bf16 rate. A pair of units takes 4000 clocks a key tile, of which the products are
+// 2048 tokens at 65536, 32/8 heads of 128, int8, fp16: 1964 us, 1102 TFLOP/s, 0.58 of the
+// measured bf16 rate (1725 us with a sum of unrounded weights, see to_weights). A pair of
+// units takes 4500 clocks a key tile, of which the products are
 // 2048: what bounds it is a unit's chain (scores, 2000 clocks of softmax beside the
 // conversion on the same schedulers, products at 80 to 90 clocks each for 64, as operands,
 // copies and conversion share the bandwidth of shared memory). 4 requests of 8 draft tokens on
