@@ -36,8 +36,8 @@
 // 2048: what bounds it is a unit's chain (scores, 2000 clocks of softmax beside the
 // conversion on the same schedulers, products at 80 to 90 clocks each for 64, as operands,
 // copies and conversion share the bandwidth of shared memory). 4 requests of 8 draft tokens on
-// up to 110000, 64/8 heads, bf16: 241 us, 2540 GB/s, 0.38 of the copy rate: an operand takes
-// the converting warps 900 clocks. Eight requests of 1 to 5 tokens on 1000: 31 us, latency
+// up to 110000, 64/8 heads, bf16: 229 us, 2600 GB/s, 0.40 of the copy rate: an operand takes
+// the converting warps 900 clocks. Eight requests of 1 to 5 tokens on 1000: 30 us, latency
 // of the first tile of cold code, the ends and the merge.
 // Tried: codes loaded straight into registers (their latency shows at every fence: 2.4 ms
 // for the first case), keys and values in rings of their own with two groups of four
