@@ -205,13 +205,15 @@ struct Shared {
   uint64_t info_full[kInfo], info_empty[kInfo];
   uint64_t part_full[kParts], part_empty[kParts];
   uint64_t fix_ready[2], fix_free[2];  // by parity of the part: `first` written, read
-  uint64_t join_ready, join_done, conv;
+  uint64_t join_ready, join_done;
   Info info[kInfo];
   Part part[kParts];
   int half[8];  // by operand stage: its values are fp16
   uint32_t tmem;
+  // By parity of the part: the number of the last part with a value in the open page that is
+  // not finite (from 1 on), and the first position of a NaN, +inf, -inf per channel, under the part it is of (first_key).
   int any_nonfinite[2];
-  int first[2][3][128];  // first position in the open page whose value is NaN, +inf, -inf, per channel
+  unsigned long long first[2][3][128];
   float join[2][kRows][3];  // of a unit's row: reference, sum, factor of its O
   long long scan[kThreads / 32];
   Pos from, to;
@@ -534,10 +536,17 @@ __device__ __forceinline__ void put_codes(unsigned char* tile, const Place<D>& a
   *reinterpret_cast<uint4*>(tile + at.at + down * 128) = a;
 }
 
+// Position `pos` of part `it`. A later part's keys are below all of an earlier one, so that the
+// smallest key is the last part's first position, whatever an earlier part left there: nothing is put
+// back between parts, and no warp has to know how far the others are.
+__device__ __forceinline__ unsigned long long first_key(int it, int pos) {
+  return ((unsigned long long)(uint32_t)~it << 32) | (uint32_t)pos;
+}
+
 // Infinities and NaN of 8 values of an open row: 0 in their place, and where
 // they were, in sh->first (0 * inf would carry them to rows that do not see them).
 template <bool BF16>
-__device__ __forceinline__ void finite8(uint4& x, int pos, int ch, int (*first)[128], int* any) {
+__device__ __forceinline__ void finite8(uint4& x, int pos, int ch, int it, unsigned long long (*first)[128], int* any) {
   constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
   uint32_t acc = fma_zero<BF16>(x.w, fma_zero<BF16>(x.z, fma_zero<BF16>(x.y, fma_zero<BF16>(x.x, 0u))));
   if ((acc & 0x7fff7fffu) == 0) return;
@@ -547,8 +556,8 @@ __device__ __forceinline__ void finite8(uint4& x, int pos, int ch, int (*first)[
     const uint32_t v = (w[j >> 1] >> (16 * (j & 1))) & 0xffffu;
     if ((v & kInf) == kInf) {
       const int kind = (v & 0x7fffu) != kInf ? 0 : (v >> 15) ? 2 : 1;
-      atomicMin(&first[kind][ch + j], pos);
-      *any = 1;
+      atomicMin(&first[kind][ch + j], first_key(it, pos));
+      *any = it + 1;
       w[j >> 1] &= j & 1 ? 0x0000ffffu : 0xffff0000u;
     }
   }
@@ -586,16 +595,6 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
     const Order order = {2u * tiles, part->t1 - part->t0, part->both};
     // the rows of the part before the last have read what this one may overwrite
     if (!wait(&sh->fix_free[par], ((it >> 1) & 1) ^ 1, c.status)) return;
-    if (sh->any_nonfinite[par]) {
-      __syncwarp();
-      if (lane == 0) arrive(&sh->conv);
-      if (!wait(&sh->conv, 0, c.status)) return;
-      for (int k = tid; k < 3 * 128; k += 256) sh->first[par][k / 128][k % 128] = kNever;
-      if (tid == 0) sh->any_nonfinite[par] = 0;
-      __syncwarp();
-      if (lane == 0) arrive(&sh->conv);
-      if (!wait(&sh->conv, 1, c.status)) return;
-    }
 #pragma unroll 1
     for (int o = 0; o < 2 * order.n; ++o) {
       const int which = order.which(o), j = order.tile(o), tile = tiles + j;
@@ -635,7 +634,7 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
               if (BF16 && which && half) put_codes<D, CODE, false, true>(to, at, down, from[(k0 + k) * 256], info.up[row >> 4]);
               else put_codes<D, CODE, BF16, true>(to, at, down, from[(k0 + k) * 256], which ? info.up[row >> 4] : one);
             } else {
-              if (which) finite8<BF16>(a[k], pos, at.channel, sh->first[par], &sh->any_nonfinite[par]);
+              if (which) finite8<BF16>(a[k], pos, at.channel, it, sh->first[par], &sh->any_nonfinite[par]);
               *reinterpret_cast<uint4*>(to + at.at + down * 128) = a[k];
             }
           }
@@ -1124,7 +1123,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
     const int head = end.head, my_token = end.token, pos = y.pos0 + my_token;
     const int par = it & 1;
     if (!wait(&sh->fix_ready[par], (it >> 1) & 1, status)) return;
-    const bool fix = sh->any_nonfinite[par] != 0;
+    const bool fix = sh->any_nonfinite[par] == it + 1;
     // sums by the reference itself
     float top = ref.m;
     l *= ref.far ? exp2_fast(-ref.kLift) : 1.0f;
@@ -1180,12 +1179,13 @@ __device__ __forceinline__ void softmax_role(const Params& p, Shared* sh, const 
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * scale);
         if (fix) {
+          const unsigned long long key = first_key(it, pos);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             float x = __uint_as_float(o[i]);
-            if (pos >= sh->first[par][1][c + i]) x += INFINITY;
-            if (pos >= sh->first[par][2][c + i]) x -= INFINITY;
-            if (pos >= sh->first[par][0][c + i]) x = NAN;
+            if (key >= sh->first[par][1][c + i]) x += INFINITY;
+            if (key >= sh->first[par][2][c + i]) x -= INFINITY;
+            if (key >= sh->first[par][0][c + i]) x = NAN;
             o[i] = __float_as_uint(x);
           }
         }
@@ -1299,7 +1299,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     mbar_init(&sh.drain, 1);
     mbar_init(&sh.join_ready, 8);
     mbar_init(&sh.join_done, 8);
-    mbar_init(&sh.conv, 8);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sh.kv_full[i], 8);
       mbar_init(&sh.kv_empty[i], 2);  // the products have read it, the gate has seen it
@@ -1315,7 +1314,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     mbar_fence_init();
     sh.any_nonfinite[0] = sh.any_nonfinite[1] = 0;
   }
-  for (int k = threadIdx.x; k < 2 * 3 * 128; k += kThreads) (&sh.first[0][0][0])[k] = kNever;
+  for (int k = threadIdx.x; k < 2 * 3 * 128; k += kThreads) (&sh.first[0][0][0])[k] = ~0ull;
   find_range(p, &sh);
   if (warp == 9) t5::alloc(&sh.tmem, 512);
   t5::fence_before();
