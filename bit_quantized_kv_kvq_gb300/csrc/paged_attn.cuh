@@ -14,9 +14,9 @@
 // themselves, copied to shared memory and converted there by eight warps, and the
 // scales stay out of them: a score's factor is c s_k of its page; a value's scale s_v =
 // f 2^e goes half into the weight (2^(s - m + log2 f), f in [1, 2)) and half into the
-// operand (code 2^e, exact), which bounds both whatever the scales; the sum of weights
-// takes 1 / f off again. All of this is per group of 16 keys, so pages of any size cost
-// the same.
+// operand (code 2^e, exact), so that weights stay in their range whatever the scales; the sum
+// of weights takes 1 / f off again. Scales below fp16's numbers round the operand, not the
+// weight (scales_to). All of this is per group of 16 keys, so pages of any size cost the same.
 //
 // A block is two units: consecutive tokens of a request on the same key tiles, or,
 // where the tokens left fit one unit, the same rows on every other tile (their sums
@@ -184,8 +184,9 @@ struct alignas(16) Info {  // per 16 keys
   float2 a[kGroups], lg[kGroups];  // score factor, log2 f, twice each: operands of pairs
   float inv[kGroups];              // 1 / f
   uint32_t up[kGroups];                          // 2^e, a pair of the values' operand type
+  uint32_t low[kGroups];                         // what is left of 2^e where fp16 does not hold it, else 1
   int page[2][kGroups];                          // of keys, of values; -1: open rows or none, -2: zeros
-  int coded;                                     // all of them pages
+  int coded;                                     // all of them pages, with low 1
   int half;                                      // values and weights in fp16
 };
 
@@ -340,29 +341,44 @@ struct Scales {
   bool zero, half;  // values' operand is zeros; code 2^e is an exact fp16 number
 };
 
-// 2^e stays a number of the operand's type, with products code 2^e exact (e4m3: multiples of 2^-9).
+// The least e with an exact fp16 product code 2^e (e4m3: multiples of 2^-9), and the least 2^e of fp16.
+template <int CODE>
+constexpr int kExactHalf = CODE == KVQ_PAGE_INT8 ? -24 : -15;
+constexpr int kLeastHalf = -24;
+
+// 2^e stays a number of the operand's type, with products code 2^e exact. An fp16 cache may
+// have smaller scales (e4m3: values below 2^-6.2, int8: below 2^-17): there f is taken from
+// [1/2, 1) and the product is rounded, once, to fp16's subnormal numbers: f times at most 2^-25, half
+// of the output's smallest step. (A smaller f would take the tokens' weights below fp16's numbers, and
+// with them their share of the sum.) A bf16 weight holds the f of scales below 2^-126.
 template <int CODE, bool BF16>
 __device__ __forceinline__ Scales scales_to(float sk, float sv, float scale_log2) {
-  constexpr int kMinHalf = CODE == KVQ_PAGE_INT8 ? -24 : -15, kMaxHalf = CODE == KVQ_PAGE_INT8 ? 8 : 7;
-  constexpr int kMin = BF16 ? -126 : kMinHalf;
+  constexpr int kMaxHalf = CODE == KVQ_PAGE_INT8 ? 8 : 7;
   const bool finite = fabsf(sv) <= 3.0e38f;
   const uint32_t bits = __float_as_uint(sv);
   Scales r;
   r.e = (int)((bits >> 23) & 255) - 127;
   float f = __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);
-  if (r.e < kMin) r.e = kMin, f = sv * (BF16 ? 0x1p126f : CODE == KVQ_PAGE_INT8 ? 0x1p24f : 0x1p15f);  // exact
+  if (BF16) {
+    if (r.e < -126) r.e = -126, f = sv * 0x1p126f;  // exact
+  } else if (r.e < kExactHalf<CODE>) {
+    ++r.e, f *= 0.5f;
+  }
   r.zero = !finite || sv == 0.0f;
   if (r.zero) r.e = 0, f = finite ? 1.0f : NAN;
-  r.half = !BF16 || (r.e >= kMinHalf && r.e <= kMaxHalf);
+  r.half = !BF16 || (r.e >= kExactHalf<CODE> && r.e <= kMaxHalf);
   r.a = fabsf(sk) <= 3.0e38f ? sk * scale_log2 : NAN;
   r.lg = log2f(f);
   r.inv = f == f ? 1.0f / f : 1.0f;  // a masked weight's share stays 0
   return r;
 }
 
-// The pair 2^e.
+// The pair 2^e (0 below the type's numbers).
 __device__ __forceinline__ uint32_t power_pair(int e, bool half) {
-  const uint32_t w = !half ? (uint32_t)(e + 127) << 7 : e >= -14 ? (uint32_t)(e + 15) << 10 : 1u << (e + 24);
+  const uint32_t w = !half              ? (uint32_t)(e + 127) << 7
+                     : e >= -14         ? (uint32_t)(e + 15) << 10
+                     : e >= kLeastHalf  ? 1u << (e - kLeastHalf)
+                                        : 0u;
   return w | (w << 16);
 }
 
@@ -428,7 +444,8 @@ __device__ __forceinline__ void tile_role(const Params& p, Shared* sh, unsigned 
       }
       const int page_v = page >= 0 && f.zero ? -2 : page;
       const uint32_t own = 255u << (lane & 24);  // the lanes of the tile
-      const bool coded = (__ballot_sync(kFull, page >= 0 && page_v >= 0) & own) == own;
+      const bool down = !BF16 && f.e < kLeastHalf;  // 2^e in two factors, the first with exact products
+      const bool coded = (__ballot_sync(kFull, page >= 0 && page_v >= 0 && !down) & own) == own;
       // The values' products take fp16 in either type, where they can: weights of 11 bits.
       // (A page of zeros or NaN is no reason against it: its neighbours' rows keep their bits.)
       const bool half = (__ballot_sync(kFull, !BF16 || (page >= 0 && f.half)) & own) == own;
@@ -444,7 +461,8 @@ __device__ __forceinline__ void tile_role(const Params& p, Shared* sh, unsigned 
           o.a[g] = make_float2(f.a, f.a);
           o.lg[g] = make_float2(f.lg, f.lg);
           o.inv[g] = f.inv;
-          o.up[g] = power_pair(f.e, half);
+          o.up[g] = power_pair(down ? kExactHalf<CODE> : f.e, half);
+          o.low[g] = power_pair(down ? f.e - kExactHalf<CODE> : 0, true);
           o.page[0][g] = now;
           o.page[1][g] = page_v;
           if (g == 0) o.coded = coded, o.half = half;
@@ -527,12 +545,15 @@ struct Place {
   }
 };
 
-// Codes of the thread's channels in the row `down` further down (a multiple of 8).
-template <int D, int CODE, bool BF16, bool VALUES>
-__device__ __forceinline__ void put_codes(unsigned char* tile, const Place<D>& at, int down, const uint2& x, uint32_t up) {
+// Codes of the thread's channels in the row `down` further down (a multiple of 8). LOW: times the
+// pair `low` too.
+template <int D, int CODE, bool BF16, bool VALUES, bool LOW = false>
+__device__ __forceinline__ void put_codes(unsigned char* tile, const Place<D>& at, int down, const uint2& x, uint32_t up,
+                                          uint32_t low = 0) {
   uint4 a;
   widen4<CODE, BF16, VALUES>(x.x, up, a.x, a.y);
   widen4<CODE, BF16, VALUES>(x.y, up, a.z, a.w);
+  if (LOW) a.x = mul2<BF16>(a.x, low), a.y = mul2<BF16>(a.y, low), a.z = mul2<BF16>(a.z, low), a.w = mul2<BF16>(a.w, low);
   *reinterpret_cast<uint4*>(tile + at.at + down * 128) = a;
 }
 
@@ -632,7 +653,8 @@ __device__ __forceinline__ void convert_role(const Params& p, Shared* sh, unsign
             if (page[k] >= 0) {
               const uint32_t one = BF16 ? 0x3f803f80u : 0x3c003c00u;  // keys: times 1
               if (BF16 && which && half) put_codes<D, CODE, false, true>(to, at, down, from[(k0 + k) * 256], info.up[row >> 4]);
-              else put_codes<D, CODE, BF16, true>(to, at, down, from[(k0 + k) * 256], which ? info.up[row >> 4] : one);
+              else put_codes<D, CODE, BF16, true, !BF16>(to, at, down, from[(k0 + k) * 256],
+                                                         which ? info.up[row >> 4] : one, which ? info.low[row >> 4] : one);
             } else {
               if (which) finite8<BF16>(a[k], pos, at.channel, it, sh->first[par], &sh->any_nonfinite[par]);
               *reinterpret_cast<uint4*>(to + at.at + down * 128) = a[k];
@@ -889,7 +911,7 @@ __device__ __forceinline__ float to_weights(const uint32_t* s, uint64_t a2, uint
 // page's factor, in units of log 2) passes it by 8, so that few tiles scale O.
 // Each row goes by its own scores. A weight is 2^(s a + log2 f - m), one multiply-add.
 // m lies 6 below the score that set it: weights with f stay below 2^15, and in fp16
-// those 2^-20 of it above the type's subnormal numbers. Past 2^20 m's own
+// those 2^-20 of it (2^-19 where f is below 1) above the type's subnormal numbers. Past 2^20 m's own
 // rounding would be a factor without limit: such a row (`far`) rounds its scaled scores and
 // subtracts the score itself, which is exact near the largest ones.
 template <int D>
