@@ -395,7 +395,7 @@ __device__ __forceinline__ void tile_role(const Params& p, Shared* sh, unsigned 
   for (int it = 0; ok; ++it) {
     const Part* at = take_part(sh, it, c.status);
     if (!at) break;
-    const int full = at->n & ~(P - 1), t0 = at->t0, t1 = at->t1, head = at->h;
+    const int n = at->n, full = n & ~(P - 1), t0 = at->t0, t1 = at->t1, head = at->h;
     const bool both = at->both;
     const int32_t* row = p.a.table + (int64_t)at->b * c.max_pages;
     give_part(sh, it);
@@ -447,8 +447,10 @@ __device__ __forceinline__ void tile_role(const Params& p, Shared* sh, unsigned 
       const bool down = !BF16 && f.e < kLeastHalf;  // 2^e in two factors, the first with exact products
       const bool coded = (__ballot_sync(kFull, page >= 0 && page_v >= 0 && !down) & own) == own;
       // The values' products take fp16 in either type, where they can: weights of 11 bits.
-      // (A page of zeros or NaN is no reason against it: its neighbours' rows keep their bits.)
-      const bool half = (__ballot_sync(kFull, !BF16 || (page >= 0 && f.half)) & own) == own;
+      // (A page of zeros or NaN, one out of range and what lies past the request's end are
+      // zeros as operands, and no reason against it: their neighbours' rows keep their bits.)
+      const bool open = page == -1 && (t + ahead) * kRows + 16 * g < n;
+      const bool half = (__ballot_sync(kFull, !BF16 || (!open && f.half)) & own) == own;
       const int live = min(4, t1 - t), now = page;
       page = page_of(t + 4);
 #pragma unroll 1
