@@ -1420,7 +1420,9 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const _
   }
   int4 from = prev;
   int base = c - 1;  // the CTA of mine in lane 0
-  for (int x = c - 1; x < p.ctas; ++x) {
+  int x = c - 1;
+  uint32_t gone = 0;  // by row: the last part's factor is 0
+  for (; x < p.ctas; ++x) {
     if (x + 1 - base == 32) {
       base += 31;
       mine = base + lane <= p.ctas ? p.pos[base + lane] : none;
@@ -1429,6 +1431,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const _
     const bool inside = same(to) && to.w > 0;  // the block goes on in the next range
     const bool empty = x >= c && inside && to.w == from.w;
     from = to;
+    gone = 0;
     if (!empty) {
       float2 ml[kSide];
       float v[kSide][kPer];
@@ -1449,6 +1452,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const _
       for (int i = 0; i < kSide; ++i) {
         const float now = fmaxf(top[i], ml[i].x), ref = now == -INFINITY ? 0.0f : now;
         const float fo = exp2_fast(top[i] - ref), fn = exp2_fast(ml[i].x - ref);
+        gone |= (fn == 0.0f ? 1u : 0u) << i;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) o[i][e] = o[i][e] * fo + v[i][e] * fn;
         l[i] = l[i] * fo + ml[i].y * fn;
@@ -1457,10 +1461,21 @@ __global__ void __launch_bounds__(kMergeThreads) paged_attn_merge_kernel(const _
     }
     if (!inside) break;
   }
+  // A factor of 0 is too small for a number, but not for the open page's infinities, which are in the last part.
+#pragma unroll
+  for (int i = 0; i < kSide; ++i) {
+    if (!live[i] || !((gone >> i) & 1)) continue;
+    const float* src = p.part_o + (((int64_t)(x * 2 + (x >= c ? 0 : 1)) * 2 + unit) * kRows + warp + 32 * i) * D + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const float v = src[e];
+      if (!(fabsf(v) < INFINITY)) o[i][e] = v;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < kSide; ++i) {
     if (!live[i]) continue;
-    const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
+    const float inv = l[i] == 0.0f ? 1.0f : 1.0f / l[i];  // no weight at all: o is 0, or the open page's
     uint16_t* out = p.a.out + ((int64_t)(r.c0 + first + token[i]) * p.a.q_heads + hq0 + head[i]) * D + lane * kPer;
 #pragma unroll
     for (int e = 0; e < kPer; e += 2)
