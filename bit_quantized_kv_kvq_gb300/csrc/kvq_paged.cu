@@ -125,6 +125,13 @@ kvq_status check_row(const char* what, const void* p, int64_t stride, int64_t ro
   return KVQ_OK;
 }
 
+// Whether n rows of `row` bytes, `stride` >= row bytes apart, meet the `bytes` from `block` on.
+bool rows_meet(const void* rows, int64_t stride, int64_t row, int64_t n, const void* block, int64_t bytes) {
+  const int64_t to = static_cast<const char*>(block) - static_cast<const char*>(rows);
+  const int64_t i = to < row ? 0 : (to - row) / stride + 1;  // the first row that ends behind the block's start
+  return i < n && i * stride < to + bytes;
+}
+
 kvq_status check_ints(std::initializer_list<const void*> arrays) {
   for (const void* p : arrays) {
     if (!p) return fail(KVQ_ERR_INVALID_ARG, "the arrays must not be NULL");
@@ -488,6 +495,9 @@ kvq_status kvq_paged_attention(kvq_paged_cache* h, int32_t layer, int32_t reques
   if (!out || !workspace) return fail(KVQ_ERR_INVALID_ARG, "out and workspace must not be NULL");
   if (!aligned(out, 16) || !aligned(workspace, 16))
     return fail(KVQ_ERR_INVALID_ARG, "out and workspace must be 16-byte aligned");
+  const int64_t row = 2 * (int64_t)num_q_heads * h->cfg.head_dim;
+  if (rows_meet(q, 2 * q_stride, row, max_tokens, out, row * max_tokens))
+    return fail(KVQ_ERR_INVALID_ARG, "out must not overlap q");
   if (ws_bytes < need) return fail(KVQ_ERR_BUFFER_TOO_SMALL, "workspace has %zu bytes, needs %zu", ws_bytes, need);
   kvq::PagedAttnArgs a;
   a.q = static_cast<const uint16_t*>(q);

@@ -306,8 +306,8 @@ class PagedKVCache:
         """Attention of a step's packed new tokens, any number of each request, over
         all that the cache holds of it with them, causally (kvq_paged_attention; call
         after write()): q [tokens][H_q][D] -> out [tokens][H_q][D]. cu_tokens, lens: as
-        reserve() planned the step. Rows of ``out`` outside every request are left
-        as they are (uninitialised where ``out`` is not given). ``workspace``: as in decode()."""
+        reserve() planned the step. ``out`` must not overlap q; its rows outside every request are
+        left as they are (uninitialised where ``out`` is not given). ``workspace``: as in decode()."""
         lib = _lib or _bind()
         dev = self.device
         qp, qs = _rows(q, "q", self.dtype, dev, dim=self._dim)

@@ -553,8 +553,8 @@ KVQ_API kvq_status kvq_paged_attention_workspace_bytes(const kvq_paged_cache* ca
  * q: [max_tokens][H_q][D] in the config's dtype, token rows q_stride elements apart
  * (a multiple of 8, >= H_q * D); H_q any multiple of H_kv. cu_tokens
  * [requests + 1], table, lens as kvq_paged_reserve left them (lens AFTER the step);
- * cu_tokens need not start at 0. out: [max_tokens][H_q][D] in the config's dtype;
- * rows outside every request are left as they are. A request with a length
+ * cu_tokens need not start at 0. out: [max_tokens][H_q][D] in the config's dtype, not over
+ * q (KVQ_ERR_INVALID_ARG); rows outside every request are left as they are. A request with a length
  * or range out of bounds is left out and sets the status word; so is a page out of range.
  * In the open page a later token does not reach an earlier one, not even by an
  * infinity or NaN; a complete page that took one in reads as NaN for every token that
