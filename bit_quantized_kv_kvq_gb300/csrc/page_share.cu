@@ -388,21 +388,6 @@ cudaError_t launch_fork(const ForkArgs& a, int sm_count, cudaStream_t st) {
 }
 
 cudaError_t launch_release_shared(const ReleaseSharedArgs& a, cudaStream_t st) {
-  if ((int64_t)a.r.requests * a.r.max_pages <= kAlone) {
-    release_shared_kernel<1, 1><<<1, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
-  }
-  // 16 CTAs a cluster are more than every device must take: asked for once a device
-  static std::atomic<unsigned long long> asked{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
-  if (!(bit && (asked.load(std::memory_order_acquire) & bit))) {
-    e = cudaFuncSetAttribute(release_shared_kernel<kCluster, kRun>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    asked.fetch_or(bit, std::memory_order_acq_rel);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCluster);
   cfg.blockDim = dim3(kThreads);
@@ -413,6 +398,31 @@ cudaError_t launch_release_shared(const ReleaseSharedArgs& a, cudaStream_t st) {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
+  bool cluster = (int64_t)a.r.requests * a.r.max_pages > kAlone;
+  if (cluster) {
+    // 16 CTAs a cluster are more than every device must take, and more than a part of one may hold:
+    // asked for once a device; where there is no room for one, a CTA releases alone, whatever the size
+    static std::atomic<unsigned long long> asked{0}, has{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+    if (asked.load(std::memory_order_acquire) & bit) {
+      cluster = has.load(std::memory_order_relaxed) & bit;
+    } else {
+      int clusters = 0;
+      e = cudaFuncSetAttribute(release_shared_kernel<kCluster, kRun>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, release_shared_kernel<kCluster, kRun>, &cfg);
+      if (e != cudaSuccess) cudaGetLastError();  // no such clusters either
+      cluster = e == cudaSuccess && clusters > 0;
+      if (cluster) has.fetch_or(bit, std::memory_order_relaxed);
+      asked.fetch_or(bit, std::memory_order_release);
+    }
+  }
+  if (!cluster) {
+    release_shared_kernel<1, 1><<<1, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
   return cudaLaunchKernelEx(&cfg, release_shared_kernel<kCluster, kRun>, a);
 }
 
