@@ -17,6 +17,9 @@ Requests may branch: ``cache.fork(src, dst, plan.lens, table, free_pages,
 plan.free_count, shared)`` makes requests ``dst`` of requests ``src``, on the same complete
 pages, and ``release(..., shared=shared)`` gives a page back with its last holder.
 
+Rejected drafts are taken back by a smaller length, no further than the start of the request's
+open page (kvq.h has the rule); where drafts may complete a page, a fork takes them.
+
 Lengths, tables, slots and the free list are int32 tensors on the cache's
 device; no call copies them to the host, so a step can be captured into a CUDA
 graph and replayed.

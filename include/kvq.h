@@ -382,6 +382,14 @@ KVQ_API kvq_status kvq_cache_status(kvq_cache* cache, void* stream, uint32_t* wo
  * arrays, must be ordered on the GPU; decodes of one layer may overlap, each
  * with a workspace of its own.
  *
+ * The last tokens of a request can be taken back (rejected drafts) as far as its open page goes:
+ * with k = lens[b] / page_tokens complete pages, to any n' > k * page_tokens by lens[b] = n'
+ * alone, as the rows are still in the tail and the row's pages stay the request's. To n' =
+ * k * page_tokens the open page goes too (free_pages[*free_count] = table[b][k], *free_count
+ * += 1), or the next reserve would take another in its place. No further: a complete page was
+ * coded, and its rows are no longer in the tail. Where drafts may complete a page, fork the request
+ * (kvq_paged_fork), draft in the fork, and release the fork, or, all being accepted, the other.
+ *
  * A step: kvq_paged_reserve once; then per layer kvq_norm_rotate (by the step's
  * positions) and kvq_paged_write, and kvq_prompt_attention for whole prompts,
  * kvq_paged_decode_attention for single tokens or kvq_paged_attention for any
