@@ -30,15 +30,16 @@
 // queries; 9: tensor core issue; 10: tiles (page ids, scales, copies of their codes);
 // 11: the gate, which follows the operands (gate_role); 12-19: codes and open rows to operands.
 //
-// 2048 tokens at 65536, 32/8 heads of 128, int8, fp16: 1964 us, 1102 TFLOP/s, 0.58 of the
+// 2048 tokens at 65536, 32/8 heads of 128, int8, fp16: 1933 us, 1120 TFLOP/s, 0.59 of the
 // measured bf16 rate (1725 us with a sum of unrounded weights, see to_weights). A pair of
 // units takes 4500 clocks a key tile, of which the products are
 // 2048: what bounds it is a unit's chain (scores, 2000 clocks of softmax beside the
 // conversion on the same schedulers, products at 80 to 90 clocks each for 64, as operands,
 // copies and conversion share the bandwidth of shared memory). 4 requests of 8 draft tokens on
-// up to 110000, 64/8 heads, bf16: 229 us, 2600 GB/s, 0.40 of the copy rate: an operand takes
-// the converting warps 900 clocks. Eight requests of 1 to 5 tokens on 1000: 30 us, latency
-// of the first tile of cold code, the ends and the merge.
+// up to 110000, 64/8 heads, bf16: 204 us, 2870 GB/s, 0.43 of the copy rate: about 3300 clocks a
+// tile, of which conversion of its two operands takes 1800 and the products 1024. What a tile waits
+// for besides has not been measured (no unit of the SM is busy more than 0.6 of the time). Eight
+// requests of 1 to 5 tokens on 1000: 29 us, latency of the first tile of cold code, the ends and the merge.
 // Tried: codes loaded straight into registers (their latency shows at every fence: 2.4 ms
 // for the first case), keys and values in rings of their own with two groups of four
 // converting warps (2.17 ms), pieces of half an operand (1.92 ms), one issue loop for
@@ -61,7 +62,8 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kFar = 0x1p20f;
 
 // Places on the line, about 700 clocks each: of a tile of two units' rows, of one that a
-// unit takes alone, and of a block for its queries, ends and merge.
+// unit takes alone, and of a block for its queries, ends and merge. (Measured with 128
+// channels. With 64, where operands are half as large, they are taken over and not tuned.)
 constexpr int kBoth = 6, kAlone = 5, kExtra = 18;
 
 template <int D>
