@@ -566,10 +566,11 @@ KVQ_API kvq_status kvq_paged_attention_workspace_bytes(const kvq_paged_cache* ca
  * or range out of bounds is left out and sets the status word; so is a page out of range.
  * In the open page a later token does not reach an earlier one, not even by an
  * infinity or NaN; a complete page that took one in reads as NaN for every token that
- * attends any of it. softmax_scale: finite and >= 0; weights are rounded to fp16 (each to 2^-11 of
- * itself or 2^-30 of their sum, whichever is more; in a bf16 cache too), or in a bf16 cache to bf16 for a tile of 128 positions that holds open rows or a page whose scale
- * is beyond fp16; an fp16 cache's values are rounded to 2^-25 on pages whose scale is below 2^-15 (e4m3)
- * or 2^-24 (int8); sums are fp32 (tokens * 2^15 * |v| must stay below 3e38). max_tokens <=
+ * attends any of it. softmax_scale: finite and >= 0; weights are rounded to fp16 (each to 2^-11
+ * of itself or 2^-30 of their sum, whichever is more; in a bf16 cache too), or in a bf16 cache to
+ * bf16 for a tile of 128 positions that holds open rows or a page whose scale is beyond fp16; an
+ * fp16 cache's values are rounded to 2^-25 on pages whose scale is below 2^-15 (e4m3) or 2^-24
+ * (int8); sums are fp32 (tokens * 2^15 * |v| must stay below 3e38). max_tokens <=
  * 2^26. workspace (41 MB with 128 channels, 21 with 64): 16-byte aligned, any content, not shared with calls that
  * overlap on the GPU. Two launches (the second merges the partial sums of requests that
  * several CTAs share, in a fixed order). */
